@@ -285,6 +285,125 @@ rrb_status rrb_plan_launch_info(rrb_plan_t plan, const void *const *d_in,
  * decode-size collectives are measured against. */
 rrb_status rrb_empty_kernel(rrb_stream_t stream);
 
+/* ---- MoE: the gate, the experts' products and their gradients --------------- */
+
+/*
+ * The gate: for each of `tokens` rows of `experts` scores (dtype RRB_BF16 or
+ * RRB_F32), the topk experts of the largest scores in descending order, ties
+ * to the lower expert, and their softmax weights, in the arrays rrb_moe_route
+ * takes: d_topk_idx[tokens][topk], d_topk_w[tokens][topk] (float32,
+ *   w_i = e^(l_i - max) / sum over all experts,
+ * or, with RRB_GATE_RENORMALIZE, / sum over the chosen ones).  A score of -inf
+ * masks an expert: it has weight 0 and is chosen only where too few others
+ * are left (a row of -inf alone: experts 0..topk-1 with weight 0).  Scores of
+ * +inf share the weight equally.  NaN ranks above every number and makes the
+ * row's weights NaN; the experts stay distinct and in range.  experts <= 1024
+ * and topk <= 16 (RRB_EUNSUPPORTED).  Asynchronous on `stream`.
+ */
+#define RRB_GATE_RENORMALIZE 1u
+rrb_status rrb_moe_gate(int64_t tokens, int32_t experts, int32_t topk, int32_t dtype,
+                        uint32_t flags, const void *d_logits, int32_t *d_topk_idx,
+                        float *d_topk_w, rrb_stream_t stream);
+/*
+ * The scores' gradient: from the gate's scores and chosen experts and the
+ * weights' gradient d_dtopk_w[tokens][topk] to d_dlogits[tokens][experts] (the
+ * scores' dtype), every element written.  With p the softmax over all experts
+ * dl_j = p_j ([j chosen] dw_j - sum over the chosen of p_i dw_i); with
+ * RRB_GATE_RENORMALIZE dl_i = w_i (dw_i - sum w dw) for the chosen and 0 for the
+ * others.  Masked experts get 0 and their dw is not used.  d_topk_idx holds
+ * distinct experts per row; entries outside 0..experts-1 are passed over.
+ */
+rrb_status rrb_moe_gate_backward(int64_t tokens, int32_t experts, int32_t topk, int32_t dtype,
+                                 uint32_t flags, const void *d_logits, const int32_t *d_topk_idx,
+                                 const float *d_dtopk_w, void *d_dlogits, rrb_stream_t stream);
+
+/*
+ * Offsets of the experts' rows in a device-routed plan's arena, for the calls
+ * below: d_offsets[experts + 1] (device) receives the first arena row of each
+ * expert as the last rrb_moe_route placed it, then tokens*topk.  After a
+ * failed routing all of them are 0 (no rows).  Asynchronous on `stream`, after
+ * the route on the same stream.
+ */
+rrb_status rrb_moe_expert_offsets(rrb_plan_t plan, int32_t *d_offsets, rrb_stream_t stream);
+
+/*
+ * Gradient of an MoE combine plan's rrb_reduce, y[t] = sum of w_j z[slot_j]:
+ *   dz[slot_j] = RNE_bf16(fl32(w_j dy[t])),  dw[t][j] = sum of dy[t] z[slot_j] (fp32).
+ * d_dy[R]: the gradients of the token shards (the plan's outputs); d_z[R],
+ * d_dz[R]: the expert rows (the plan's inputs) and their gradients; d_weights
+ * as for rrb_reduce; d_dweights[tokens][topk] in the routing arrays' order.
+ * d_dz may be NULL (not computed), and so may d_dweights (then d_z is not
+ * read and may be NULL), not both.  dz must not overlap dy or z.  A
+ * dispatch's gradient is its combine with per-call weights of 1.
+ */
+rrb_status rrb_moe_combine_backward(rrb_plan_t plan, const void *const *d_dy, const void *const *d_z,
+                                    void *const *d_dz, const float *d_weights, float *d_dweights,
+                                    rrb_stream_t stream);
+
+/*
+ * The experts' products.  Rows are grouped: group e's rows are
+ * d_offsets[e] .. d_offsets[e + 1] - 1 of an arena of `rows` rows (int32, device,
+ * groups + 1 entries, not decreasing; NULL: one group of all rows), and each
+ * group has its own weights, [groups][out][in] back to back.  All elements are
+ * bf16; products accumulate in fp32 and each result is rounded once.  Rows
+ * before the first and behind the last offset are neither read nor written,
+ * and neither are the weights of a group without rows.  Offsets are read as
+ * clamped to 0..rows, so no access leaves the buffers; where they decrease the
+ * outputs are unspecified.  Buffers need the alignment of their elements only
+ * (16-byte aligned rows run faster); outputs must not overlap inputs, except
+ * that d_out may be d_residual.  Limits (RRB_EUNSUPPORTED): rows < 2^31, in and
+ * out <= 2^20, groups <= 4096.  All calls are asynchronous on `stream`.
+ */
+typedef enum {
+  RRB_ACT_NONE = 0,
+  RRB_ACT_SILU = 1,      /* x / (1 + e^-x) */
+  RRB_ACT_GELU = 2,      /* x Phi(x) */
+  RRB_ACT_GELU_TANH = 3, /* x / (1 + e^-2u), u = sqrt(2/pi) (x + 0.044715 x^3) */
+  RRB_ACT_RELU = 4
+} rrb_activation;
+
+typedef struct {
+  int64_t rows;       /* rows of the arena, >= 0 */
+  int64_t in;         /* elements of an input row */
+  int64_t out;        /* elements of an output row */
+  int32_t groups;
+  int32_t activation; /* rrb_activation */
+} rrb_expert_spec;
+
+/* Gated feed-forward: out = act(x Wg^T) * (x Wu^T), both projections, the
+ * activation and the product in one kernel.  d_save_gate, d_save_up (both or
+ * neither NULL): [rows][out], receive x Wg^T and x Wu^T for the backward pass. */
+rrb_status rrb_expert_gated(const rrb_expert_spec *spec, const void *d_x, const int32_t *d_offsets,
+                            const void *d_w_gate, const void *d_w_up, void *d_out,
+                            void *d_save_gate, void *d_save_up, rrb_stream_t stream);
+/* Its gradients from d_dout, the inputs and the saved projections.  d_dx may be
+ * NULL (not computed); so may d_dw_gate and d_dw_up together.  The weight
+ * gradients of a group without rows are written as 0.  The gradients of the two
+ * projections are held in bf16 in d_workspace (caller-owned, 16-byte aligned,
+ * of the size the query gives; in use until the call's work completes). */
+rrb_status rrb_expert_gated_backward_workspace(const rrb_expert_spec *spec, size_t *bytes);
+rrb_status rrb_expert_gated_backward(const rrb_expert_spec *spec, const void *d_dout, const void *d_x,
+                                     const int32_t *d_offsets, const void *d_w_gate,
+                                     const void *d_w_up, const void *d_gate, const void *d_up,
+                                     void *d_dx, void *d_dw_gate, void *d_dw_up, void *d_workspace,
+                                     size_t workspace_bytes, rrb_stream_t stream);
+
+/* Product with an epilogue: out = act(x W^T + bias) + residual.  d_bias
+ * (nullable): [groups][out]; d_residual (nullable): [rows][out]; d_save_pre
+ * (nullable): [rows][out], receives x W^T + bias for the backward pass. */
+rrb_status rrb_expert_linear(const rrb_expert_spec *spec, const void *d_x, const int32_t *d_offsets,
+                             const void *d_w, const void *d_bias, const void *d_residual,
+                             void *d_out, void *d_save_pre, rrb_stream_t stream);
+/* Its gradients; each of d_dx, d_dw, d_dbias may be NULL (not computed), not
+ * all.  d_pre is the saved pre-activation (not read without an activation).
+ * The residual's gradient is d_dout itself.  dw and dbias of a group without
+ * rows are written as 0.  Workspace as above. */
+rrb_status rrb_expert_linear_backward_workspace(const rrb_expert_spec *spec, size_t *bytes);
+rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d_dout, const void *d_x,
+                                      const int32_t *d_offsets, const void *d_w, const void *d_pre,
+                                      void *d_dx, void *d_dw, void *d_dbias, void *d_workspace,
+                                      size_t workspace_bytes, rrb_stream_t stream);
+
 /* ---- SNAC: stage / notify / consume chain --------------------------------- */
 
 /*

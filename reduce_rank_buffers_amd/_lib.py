@@ -33,6 +33,13 @@ RRB_BLOCK_COL = 5
 RRB_MOE_DISPATCH = 0
 RRB_MOE_COMBINE = 1
 
+RRB_GATE_RENORMALIZE = 1
+RRB_ACT_NONE = 0
+RRB_ACT_SILU = 1
+RRB_ACT_GELU = 2
+RRB_ACT_GELU_TANH = 3
+RRB_ACT_RELU = 4
+
 RRB_SNAC_DUAL_BUFFER = 1
 RRB_SNAC_SPECULATIVE = 2
 RRB_SNAC_GRAPH = 4
@@ -47,6 +54,9 @@ RRB_MAX_RANKS = 16
 EXPORTS = (
     "rrb_status_string", "rrb_last_error", "rrb_abi_version",
     "rrb_plan_create", "rrb_plan_create_rows", "rrb_plan_create_rows_device", "rrb_moe_route",
+    "rrb_moe_gate", "rrb_moe_gate_backward", "rrb_moe_expert_offsets", "rrb_moe_combine_backward",
+    "rrb_expert_gated", "rrb_expert_gated_backward_workspace", "rrb_expert_gated_backward",
+    "rrb_expert_linear", "rrb_expert_linear_backward_workspace", "rrb_expert_linear_backward",
     "rrb_moe_route_check", "rrb_plan_query", "rrb_plan_bind",
     "rrb_plan_segments", "rrb_plan_destroy",
     "rrb_copy", "rrb_reduce", "rrb_plan_launch_info", "rrb_empty_kernel",
@@ -69,6 +79,11 @@ class Spec(ctypes.Structure):
 class Segment(ctypes.Structure):
     _fields_ = [("src_off", ctypes.c_int64), ("dst_off", ctypes.c_int64), ("len", ctypes.c_int64),
                 ("src_rank", ctypes.c_int32), ("dst_mask", ctypes.c_uint32)]
+
+
+class ExpertSpec(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_", ctypes.c_int64), ("out", ctypes.c_int64),
+                ("groups", ctypes.c_int32), ("activation", ctypes.c_int32)]
 
 
 class SnacStats(ctypes.Structure):
@@ -99,6 +114,16 @@ _SIGS = {
     "rrb_plan_create_rows_device": (_I32, [_I32, _I64, _I64, _I32, _I32, _I32, ctypes.POINTER(_P)]),
     "rrb_moe_route": (_I32, [_P, _P, _P, _P, _P]),
     "rrb_moe_route_check": (_I32, [_P, _P]),
+    "rrb_moe_gate": (_I32, [_I64, _I32, _I32, _I32, _U32, _P, _P, _P, _P]),
+    "rrb_moe_gate_backward": (_I32, [_I64, _I32, _I32, _I32, _U32, _P, _P, _P, _P, _P]),
+    "rrb_moe_expert_offsets": (_I32, [_P, _P, _P]),
+    "rrb_moe_combine_backward": (_I32, [_P, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_P), _P, _P, _P]),
+    "rrb_expert_gated": (_I32, [ctypes.POINTER(ExpertSpec)] + [_P] * 8),
+    "rrb_expert_gated_backward_workspace": (_I32, [ctypes.POINTER(ExpertSpec), ctypes.POINTER(_SZ)]),
+    "rrb_expert_gated_backward": (_I32, [ctypes.POINTER(ExpertSpec)] + [_P] * 11 + [_SZ, _P]),
+    "rrb_expert_linear": (_I32, [ctypes.POINTER(ExpertSpec)] + [_P] * 8),
+    "rrb_expert_linear_backward_workspace": (_I32, [ctypes.POINTER(ExpertSpec), ctypes.POINTER(_SZ)]),
+    "rrb_expert_linear_backward": (_I32, [ctypes.POINTER(ExpertSpec)] + [_P] * 9 + [_SZ, _P]),
     "rrb_plan_query": (_I32, [_P, ctypes.POINTER(_SZ), _P, _P]),
     "rrb_plan_bind": (_I32, [_P, _P, _SZ, _P]),
     "rrb_plan_segments": (_I32, [_P, ctypes.POINTER(Segment), _I32, ctypes.POINTER(_I32)]),

@@ -357,7 +357,37 @@ def empty_kernel(stream=None):
 
 # ---- MoE --------------------------------------------------------------------
 
-class MoePlan(Plan):
+class _MoeRows:
+    """What combine plans of either kind add to Plan: their gradient."""
+
+    def backward(self, d_ys, zs, d_zs, d_weights=None, weights=None, stream=None):
+        """Gradient of a combine plan's run(zs, ys): d_ys are the gradients of
+        the token shards; d_zs (or None) receives those of the expert rows
+        zs, and d_weights (or None) float32 [tokens, topk] those of the
+        weights, in the routing order (zs may be None without it).
+        weights: the per-call weights that run() was given, if any."""
+        if self.tk is None:
+            raise ValueError("backward applies to MoE combine plans only")
+        if d_zs is None and d_weights is None:
+            raise ValueError("no gradient asked for: d_zs and d_weights are None")
+        R = self.nranks
+        checked = _check_rank_list(d_ys, R, self.out_count, self.dtype, "d_ys")
+        if d_weights is not None:
+            checked += _check_rank_list(zs, R, self.in_count, self.dtype, "zs")
+        if d_zs is not None:
+            checked += _check_rank_list(d_zs, R, self.in_count, self.dtype, "d_zs")
+        checked += _check_aux(d_weights, "d_weights", _F32_TYPES, self.tk)
+        checked += _check_aux(weights, "weights", _F32_TYPES, self.tk)
+        _all_on_gpu(checked)
+        self._check(self._lib.rrb_moe_combine_backward(
+            self.handle, _ptrs(d_ys, R), _ptrs(zs, R) if d_weights is not None else None,
+            _ptrs(d_zs, R) if d_zs is not None else None,
+            weights.data_ptr() if weights is not None else None,
+            d_weights.data_ptr() if d_weights is not None else None, _stream(stream)),
+            "rrb_moe_combine_backward")
+
+
+class MoePlan(_MoeRows, Plan):
     """Row-map plan for expert-parallel dispatch (copy) or combine (reduce)."""
 
     def __init__(self, nranks, hidden, experts, topk_idx, topk_w, direction, device=None):
@@ -384,7 +414,7 @@ class MoePlan(Plan):
         self.bind(device)
 
 
-class MoeDevicePlan(Plan):
+class MoeDevicePlan(_MoeRows, Plan):
     """Row-map plan whose maps are built on the GPU by route() each step.
 
     The receive side is one arena of tokens*topk rows (rank regions back to
@@ -428,6 +458,17 @@ class MoeDevicePlan(Plan):
             self.handle, ctypes.c_void_p(topk_idx.data_ptr()), ctypes.c_void_p(topk_w.data_ptr()),
             ctypes.c_void_p(rank_offsets.data_ptr() if rank_offsets is not None else 0),
             _stream(stream)), "rrb_moe_route")
+
+    def expert_offsets(self, offsets, stream=None):
+        """Write the arena row where each expert's rows start, then
+        tokens * topk, into offsets (int32 [experts + 1], device), as the last
+        route() placed them: the grouping the expert_* calls take.  After a
+        failed routing every offset is 0 (no rows)."""
+        if offsets is None:
+            raise ValueError("offsets is required")
+        _all_on_gpu(_check_aux(offsets, "offsets", (torch.int32,), self.experts + 1))
+        self._check(self._lib.rrb_moe_expert_offsets(self.handle, offsets.data_ptr(), _stream(stream)),
+                    "rrb_moe_expert_offsets")
 
     def check(self, stream=None):
         self._check(self._lib.rrb_moe_route_check(self.handle, _stream(stream)), "rrb_moe_route_check")

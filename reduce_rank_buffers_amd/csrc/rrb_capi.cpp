@@ -147,6 +147,36 @@ rrb_status rrb_moe_route_check(rrb_plan_t plan, rrb_stream_t stream) {
   return RRB_OK;
 }
 
+rrb_status rrb_moe_expert_offsets(rrb_plan_t plan, int32_t *d_offsets, rrb_stream_t stream) {
+  clear_error();
+  if (!plan || !d_offsets) return fail(RRB_EINVAL, "NULL plan or offsets");
+  const Plan &p = plan->p;
+  if (p.kind != PlanKind::RowsDevice) return fail(RRB_EINVAL, "rrb_moe_expert_offsets needs a device row plan");
+  if (!p.d_ws) return fail(RRB_EINVAL, "plan is not bound to a workspace");
+  return launch_expert_offsets(p, d_offsets, stream);
+}
+
+rrb_status rrb_moe_combine_backward(rrb_plan_t plan, const void *const *d_dy, const void *const *d_z,
+                                    void *const *d_dz, const float *d_weights, float *d_dweights,
+                                    rrb_stream_t stream) {
+  clear_error();
+  if (!plan) return fail(RRB_EINVAL, "NULL plan");
+  const Plan &p = plan->p;
+  if (p.kind == PlanKind::Uniform || p.rows.dir != RRB_MOE_COMBINE)
+    return fail(RRB_EINVAL, "rrb_moe_combine_backward needs an MoE combine plan");
+  if (!d_dz && !d_dweights) return fail(RRB_EINVAL, "no gradient asked for");
+  if (p.rows.tokens > 0) {
+    if (!p.d_ws) return fail(RRB_EINVAL, "row plan is not bound to a workspace");
+    if (!d_dy || (d_dweights && !d_z)) return fail(RRB_EINVAL, "NULL dy or z");
+    for (int32_t r = 0; r < p.nranks; ++r) {
+      if (p.out_count[r] && !d_dy[r]) return fail(RRB_EINVAL, "dy[%d] is NULL", r);
+      if (p.in_count[r] && ((d_dweights && !d_z[r]) || (d_dz && !d_dz[r])))
+        return fail(RRB_EINVAL, "z[%d] or dz[%d] is NULL", r, r);
+    }
+  }
+  return launch_combine_backward(p, d_dy, d_dweights ? d_z : nullptr, d_dz, d_weights, d_dweights, stream);
+}
+
 rrb_status rrb_plan_query(rrb_plan_t plan, size_t *workspace_bytes, int64_t *in_count,
                           int64_t *out_count) {
   clear_error();

@@ -1,0 +1,805 @@
+// The experts' products of an expert-parallel MoE step, between dispatch and
+// combine, and their gradients.
+//
+// Rows arrive grouped by expert (the dispatch layout): group e's rows are
+// offsets[e] .. offsets[e+1] of one arena, and each group has weights of its
+// own.  With X a group's rows, W its weight [out][in]:
+//   linear   Y = act(X W^T + b) + R
+//   gated    H = act(X Wg^T) * (X Wu^T)
+// and, with dZ the gradient before the activation,
+//   dX = dZ W,  dW = dZ^T X,  db = the column sums of dZ.
+// All of it is matrix products over ragged groups, computed by one tiled
+// kernel in three forms that differ in which side has the reduction index
+// contiguous in memory.
+#include <hip/hip_runtime.h>
+
+#include <cstring>
+
+#include "rrb_internal.h"
+#include "rrb_kernels.h"
+
+namespace rrb {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+
+// Groups that one wave's two ballots can search.
+constexpr int kMaxGroups = 4096;
+// Row widths whose tile offsets fit 32 bits.
+constexpr int64_t kMaxWidth = int64_t(1) << 20;
+
+// ---- activations ------------------------------------------------------------
+//
+// In fp32.  The sigmoid is v_rcp_f32 of 1 + v_exp_f32: about 2 ulp of fp32,
+// where every result is rounded to bf16 (2^16 ulp of fp32) afterwards.
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
+
+// Argument of the tanh form's sigmoid: gelu_tanh(x) = x sigmoid(2u),
+// u = sqrt(2/pi) (x + 0.044715 x^3).
+__device__ __forceinline__ float gelu_2u(float x) {
+  return 1.5957691216057308f * (x + 0.044715f * x * x * x);
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if (ACT == RRB_ACT_SILU) return x * sigmoid(x);
+  // erfc(-x / sqrt 2) keeps its relative precision where 1 + erf would cancel.
+  if (ACT == RRB_ACT_GELU) return 0.5f * x * erfcf(-0.70710678118654752f * x);
+  if (ACT == RRB_ACT_GELU_TANH) return x * sigmoid(gelu_2u(x));
+  if (ACT == RRB_ACT_RELU) return x < 0.f ? 0.f : x;
+  return x;
+}
+
+// act(x) and act'(x).
+template <int ACT>
+__device__ __forceinline__ void activate_grad(float x, float &f, float &df) {
+  if (ACT == RRB_ACT_SILU) {
+    const float s = sigmoid(x);
+    f = x * s;
+    df = s * (1.f + x * (1.f - s));
+  } else if (ACT == RRB_ACT_GELU) {
+    const float c = 0.5f * erfcf(-0.70710678118654752f * x);
+    f = x * c;
+    df = c + x * (0.3989422804014327f * __expf(-0.5f * x * x));
+  } else if (ACT == RRB_ACT_GELU_TANH) {
+    const float s = sigmoid(gelu_2u(x));
+    const float t = s * (1.f - s);
+    f = x * s;
+    // Where the sigmoid is flat the slope's term is 0, also where x^2
+    // overflows.
+    df = t == 0.f ? s : s + x * t * 1.5957691216057308f * (1.f + 0.134145f * x * x);
+  } else if (ACT == RRB_ACT_RELU) {
+    f = x < 0.f ? 0.f : x;
+    df = x > 0.f ? 1.f : 0.f;
+  } else {
+    f = x;
+    df = 1.f;
+  }
+}
+
+// ---- arguments --------------------------------------------------------------
+
+// Forms of the tiled product C[m][n] = sum over k of A(m, k) B(n, k).
+//   kForward  A = X rows, B = weight rows: both have k contiguous
+//   kGradX    A = dZ rows (k contiguous), B(n, k) = W[k][n] (n contiguous);
+//             gated: k runs over dG with Wg, then over dU with Wu
+//   kGradW    A(m, k) = dZ[k][m], B(n, k) = X[k][n]: k is the group's rows
+enum Form { kForward = 0, kGradX = 1, kGradW = 2 };
+
+struct ProductArgs {
+  const uint16_t *a[2];  // kGradX: per phase; kGradW: per output; else a[0]
+  const uint16_t *b[2];  // kForward gated: gate, up; kGradX: per phase
+  uint16_t *c[2];        // kGradW gated: dWg, dWu; else c[0]
+  uint16_t *save[2];     // kForward: pre-activation values to keep, or NULL
+  const uint16_t *bias, *residual;
+  const int32_t *offsets;  // [groups + 1], or NULL: one group of all rows
+  int64_t rows;
+  int64_t lda, ldb, ldc;  // row pitches, in elements
+  int64_t bstride;        // kForward, kGradX: weight elements per group (kGradW: dW's)
+  int32_t groups;
+  int32_t m, n, k;        // m: kGradW only; k: kForward, kGradX only
+  int32_t slots;          // kForward, kGradX: row-tile slots; kGradW: m tiles of both outputs
+  int32_t ntiles;
+  int32_t halves;         // kGradX: phases; kGradW: outputs
+  int32_t act;
+  int32_t cvec;           // every output row starts on an 8-byte boundary
+};
+
+// Offsets as the kernels read them: inside the arena whatever the array
+// holds.
+__device__ __forceinline__ int64_t offset_at(const ProductArgs &p, int e) {
+  if (!p.offsets) return e == 0 ? 0 : p.rows;
+  const int64_t v = p.offsets[e];
+  return v < 0 ? 0 : v > p.rows ? p.rows : v;
+}
+
+// Row tiles are numbered without knowing the group sizes on the host: group
+// e's tiles start at slot floor(offsets[e] / BM) + e, which leaves each group
+// room for its ceil(rows / BM) tiles, so rows / BM + groups slots hold any
+// grouping; a slot without a tile exits.  The group of a slot is the last one
+// that starts at or before it: two steps of a 64-way search by ballot, with
+// no map to build beforehand.
+template <int BM>
+__device__ __forceinline__ int group_of_slot(const ProductArgs &p, int slot) {
+  const int lane = threadIdx.x & 63;
+  const int stride = (p.groups + 63) >> 6;
+  const int e0 = lane * stride;
+  const bool at0 = e0 < p.groups && offset_at(p, e0) / BM + e0 <= slot;
+  const int block = __popcll(__ballot(at0)) - 1;
+  if (stride == 1) return block < 0 ? 0 : block;
+  const int first = (block < 0 ? 0 : block) * stride;
+  const int e1 = first + lane;
+  const bool at1 = lane < stride && e1 < p.groups && offset_at(p, e1) / BM + e1 <= slot;
+  const int in = __popcll(__ballot(at1)) - 1;
+  return first + (in < 0 ? 0 : in);
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = uniform(static_cast<int>(v)), hi = uniform(static_cast<int>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// ---- operand tiles in LDS -----------------------------------------------------
+//
+// kStep reduction indexes per step.  A row tile (k contiguous) is [rows][64]
+// bf16: 128-byte rows of eight 16-byte chunks, chunk c of row r stored at
+// chunk c ^ (r / 2 % 8), so that the 16 rows of a fragment read land on 16
+// different bank groups.  A column tile (k across rows) is [64][cols]: rows of
+// 32-byte slots, slot s of row k stored at slot s ^ (k % 4 + 4 * (k / 8 % 2)),
+// so that the eight rows that half a wave reads transposed (ds_read_b64_tr_b16)
+// land on eight different bank groups.
+constexpr int kStep = 64;
+
+__device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int col_swizzle(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+
+// Fragment of 16 rows x 32 k from a row tile: lane l holds row l % 16, k =
+// 8 (l / 16) .. + 7.
+__device__ __forceinline__ bf16x8_t row_fragment(const unsigned char *tile, int row, int kk) {
+  const int lane = threadIdx.x & 63;
+  const int r = row + (lane & 15);
+  const int c = (kk * 4 + (lane >> 4)) ^ row_swizzle(r);
+  return *reinterpret_cast<const bf16x8_t *>(tile + r * 128 + c * 16);
+}
+
+// The same fragment from a column tile of `cols` columns: two transposed
+// reads, each giving lane l column l % 16 of four rows k.
+template <int COLS>
+__device__ __forceinline__ bf16x8_t col_fragment(const unsigned char *tile, int col, int kk) {
+  const int lane = threadIdx.x & 63;
+  const int k = kk * 32 + (lane >> 4) * 8 + ((lane >> 2) & 3);
+  const int at = k * (COLS * 2) + (((col >> 4) ^ col_swizzle(k)) << 5) + (lane & 3) * 8;
+  typedef __attribute__((address_space(3))) s16x4_t *lds_ptr;
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at));
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at + 4 * COLS * 2));
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Eight bf16 from `src`, of which the first `have` exist (the others are 0).
+__device__ __forceinline__ u32x4_t load_chunk(const uint16_t *src, int64_t have) {
+  u32x4_t v = {0, 0, 0, 0};
+  if (have >= 8) {
+    __builtin_memcpy(&v, src, 16);
+  } else if (have > 0) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < have) w[i >> 1] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+    v = u32x4_t{w[0], w[1], w[2], w[3]};
+  }
+  return v;
+}
+
+// Four consecutive columns of one row.
+__device__ __forceinline__ void load4(const uint16_t *src, int have, bool vec, float (&v)[4]) {
+  if (vec && have >= 4) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(src);
+    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < have ? bf16_to_f32(src[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store4(uint16_t *dst, int have, bool vec, const float (&v)[4]) {
+  const uint32_t lo = cvt_pk_bf16(v[0], v[1]), hi = cvt_pk_bf16(v[2], v[3]);
+  if (vec && have >= 4) {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
+  } else {
+    const uint32_t w[2] = {lo, hi};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < have) dst[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// ---- epilogue -------------------------------------------------------------------
+//
+// The fragments are computed as B x A, so lane l holds row l % 16 and the four
+// consecutive columns 4 (l / 16) .. + 3 of each 16 x 16 block.
+template <int ACT, bool GATED, int FM, int FN>
+__device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (&acc)[FM][FN], uint16_t *c,
+                                           uint16_t *save0, uint16_t *save1, const uint16_t *bias,
+                                           const uint16_t *residual, int m0, int mvalid, int n0) {
+  const int lane = threadIdx.x & 63;
+  const bool vec = p.cvec;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int m = m0 + i * 16 + (lane & 15);
+    if (m >= mvalid) continue;
+    const int64_t row = m * p.ldc;
+#pragma unroll
+    for (int j = 0; j < FN; j += GATED ? 2 : 1) {
+      const int n = n0 + (GATED ? j / 2 : j) * 16 + (lane >> 4) * 4;
+      const int have = p.n - n;
+      if (have <= 0) continue;
+      float v[4];
+      if (GATED) {
+        float u[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = acc[i][j][q], u[q] = acc[i][j + (GATED ? 1 : 0)][q];
+        if (save0) {
+          store4(save0 + row + n, have, vec, v);
+          store4(save1 + row + n, have, vec, u);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = activate<ACT>(v[q]) * u[q];
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = acc[i][j][q];
+        if (bias) {
+          float b[4];
+          load4(bias + n, have, vec, b);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] += b[q];
+        }
+        if (save0) store4(save0 + row + n, have, vec, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = activate<ACT>(v[q]);
+        if (residual) {
+          float r[4];
+          load4(residual + row + n, have, vec, r);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] += r[q];
+        }
+      }
+      store4(c + row + n, have, vec, v);
+    }
+  }
+}
+
+// ---- the tiled product ------------------------------------------------------------
+
+template <int BM, int BN, int WR, int WC, int FORM, bool GATED>
+__global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
+  constexpr int NT = WR * WC * 64;
+  constexpr int FM = BM / WR / 16, FN = BN / WC / 16;
+  constexpr int A_BYTES = BM * kStep * 2, B_BYTES = BN * kStep * 2;
+  constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT;  // 16-byte chunks per thread
+  constexpr bool A_COL = FORM == kGradW, B_COL = FORM != kForward;
+  constexpr int NCOLS = GATED ? BN / 2 : BN;  // output columns per tile
+  __shared__ __align__(16) unsigned char lds[2 * (A_BYTES + B_BYTES)];
+
+  const int tid = threadIdx.x;
+  const int wave = uniform(tid >> 6);
+  const int slot = blockIdx.x % p.slots;
+  const int rest = blockIdx.x / p.slots;
+  const int nt = FORM == kGradW ? rest % p.ntiles : rest;
+  const int n0 = nt * NCOLS;
+
+  // The tile's place: operand bases and extents.
+  const uint16_t *a[2], *b[2];
+  uint16_t *c;
+  int64_t klen, row0 = 0;
+  int mvalid, half = 0, e, m0 = 0;
+  if (FORM == kGradW) {
+    e = rest / p.ntiles;
+    const int mt = p.slots / p.halves;
+    half = slot / mt;
+    m0 = (slot - half * mt) * BM;
+    const int64_t s = uniform64(offset_at(p, e)), t = uniform64(offset_at(p, e + 1));
+    klen = t > s ? t - s : 0;
+    mvalid = p.m - m0;
+    a[0] = a[1] = p.a[half] + s * p.lda + m0;
+    b[0] = b[1] = p.b[0] + s * p.ldb + n0;
+    c = p.c[half] + e * p.bstride + static_cast<int64_t>(m0) * p.ldc;
+  } else {
+    e = uniform(group_of_slot<BM>(p, slot));
+    const int64_t s = uniform64(offset_at(p, e)), t = uniform64(offset_at(p, e + 1));
+    const int64_t mt = slot - (s / BM + e);
+    row0 = s + mt * BM;
+    if (mt < 0 || row0 >= t) return;
+    mvalid = t - row0 < BM ? static_cast<int>(t - row0) : BM;
+    klen = p.k;
+    for (int h = 0; h < 2; ++h) {
+      a[h] = p.a[FORM == kGradX ? h : 0] + row0 * p.lda;
+      b[h] = p.b[h] + e * p.bstride + (FORM == kForward ? static_cast<int64_t>(n0) * p.ldb : n0);
+    }
+    c = p.c[0] + row0 * p.ldc;
+  }
+  const int64_t per = (klen + kStep - 1) / kStep;  // steps per phase
+  const int steps = static_cast<int>(FORM == kGradX ? per * p.halves : per);
+
+  u32x4_t ra[CA], rb[CB];
+  // Loads of one step's chunks into registers.
+  auto fetch = [&](int step) {
+    const int h = FORM == kGradX && step >= per ? 1 : 0;
+    const int64_t k0 = (step - h * per) * kStep;
+#pragma unroll
+    for (int i = 0; i < CA; ++i) {
+      const int id = i * NT + tid;
+      if (A_COL) {
+        const int kr = id / (BM / 8), pos = id % (BM / 8);
+        const int ch = pos ^ (col_swizzle(kr) << 1);
+        ra[i] = load_chunk(a[0] + (k0 + kr) * p.lda + ch * 8, k0 + kr < klen ? p.m - m0 - ch * 8 : 0);
+      } else {
+        const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
+        const int64_t have = klen - k0 - ch * 8;
+        ra[i] = load_chunk(a[h] + r * p.lda + k0 + ch * 8, r < mvalid ? have : 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+      const int id = i * NT + tid;
+      if (B_COL) {
+        const int kr = id / (BN / 8), pos = id % (BN / 8);
+        const int ch = pos ^ (col_swizzle(kr) << 1);
+        rb[i] = load_chunk(b[h] + (k0 + kr) * p.ldb + ch * 8, k0 + kr < klen ? p.n - n0 - ch * 8 : 0);
+      } else {
+        const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
+        const int64_t have = klen - k0 - ch * 8;
+        // Gated: blocks of 16 gate rows and 16 up rows by turns, so a lane
+        // holds both projections of its outputs.
+        const int n = GATED ? (r >> 5) * 16 + (r & 15) : r;
+        const uint16_t *src = GATED && (r & 16) ? b[1] : b[0];
+        rb[i] = load_chunk(src + n * p.ldb + k0 + ch * 8, n0 + n < p.n ? have : 0);
+      }
+    }
+  };
+  auto commit = [&](int buf) {
+    unsigned char *ta = lds + buf * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;
+#pragma unroll
+    for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4_t *>(ta + (i * NT + tid) * 16) = ra[i];
+#pragma unroll
+    for (int i = 0; i < CB; ++i) *reinterpret_cast<u32x4_t *>(tb + (i * NT + tid) * 16) = rb[i];
+  };
+
+  const int wm = wave / WC * (BM / WR), wn = wave % WC * (BN / WC);
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  if (steps > 0) {
+    fetch(0);
+    commit(0);
+  }
+  for (int s = 0; s < steps; ++s) {
+    __syncthreads();
+    if (s + 1 < steps) fetch(s + 1);
+    const unsigned char *ta = lds + (s & 1) * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;
+#pragma unroll
+    for (int kk = 0; kk < kStep / 32; ++kk) {
+      bf16x8_t fa[FM], fb[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        fa[i] = A_COL ? col_fragment<BM>(ta, wm + i * 16, kk) : row_fragment(ta, wm + i * 16, kk);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        fb[j] = B_COL ? col_fragment<BN>(tb, wn + j * 16, kk) : row_fragment(tb, wn + j * 16, kk);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+    if (s + 1 < steps) commit((s + 1) & 1);
+  }
+
+  const int wn0 = n0 + (GATED ? wn / 2 : wn);
+  if (FORM != kForward) {
+    store_tile<RRB_ACT_NONE, false>(p, acc, c, nullptr, nullptr, nullptr, nullptr, wm, mvalid, wn0);
+  } else {
+    uint16_t *s0 = p.save[0] ? p.save[0] + row0 * p.ldc : nullptr;
+    uint16_t *s1 = p.save[1] ? p.save[1] + row0 * p.ldc : nullptr;
+    const uint16_t *bias = p.bias ? p.bias + static_cast<int64_t>(e) * p.n : nullptr;
+    const uint16_t *res = p.residual ? p.residual + row0 * p.ldc : nullptr;
+    switch (p.act) {
+#define RRB_CASE(A)                                                                    \
+  case A:                                                                              \
+    store_tile<A, GATED>(p, acc, c, s0, s1, bias, res, wm, mvalid, wn0);               \
+    break;
+      RRB_CASE(RRB_ACT_SILU) RRB_CASE(RRB_ACT_GELU) RRB_CASE(RRB_ACT_GELU_TANH) RRB_CASE(RRB_ACT_RELU)
+#undef RRB_CASE
+      default: store_tile<RRB_ACT_NONE, GATED>(p, acc, c, s0, s1, bias, res, wm, mvalid, wn0);
+    }
+  }
+}
+
+// ---- gradients before the activation -------------------------------------------
+
+struct ActGradArgs {
+  const uint16_t *dout, *gate, *up;  // linear: gate is the pre-activation (or NULL), up NULL
+  uint16_t *dgate, *dup;             // pitch ldo, columns n .. ldc padded with 0
+  const int32_t *offsets;
+  int64_t rows, ldo;
+  int32_t n, groups;
+};
+
+// dG = dH * U * act'(G), dU = dH * act(G) (linear: dZ = dY * act'(pre)), one
+// 8-column chunk per thread, rows of groups only.  Memory-bound; the results
+// are rounded to bf16, as the matrix instructions take them.  Columns up to
+// the pitch are written as 0, so the products that reduce over them read
+// zeros and not what the workspace held.
+template <int ACT, bool GATED>
+__global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs p) {
+  const int64_t chunks = p.ldo / 8;
+  int64_t first = 0, last = p.rows;
+  if (p.offsets) {
+    first = p.offsets[0], last = p.offsets[p.groups];
+    if (first < 0) first = 0;
+    if (last > p.rows) last = p.rows;
+  }
+  const int64_t total = (last - first) * chunks;
+  for (int64_t id = blockIdx.x * 256ll + threadIdx.x; id < total; id += gridDim.x * 256ll) {
+    const int64_t r = first + id / chunks;
+    const int c0 = static_cast<int>(id % chunks) * 8;
+    const int have = p.n - c0;
+    const int64_t at = r * p.n + c0;
+    u32x4_t d = load_chunk(p.dout + at, have), g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
+    if (ACT != RRB_ACT_NONE || GATED) g = load_chunk(p.gate + at, have);
+    if (GATED) u = load_chunk(p.up + at, have);
+    u32x4_t og, ou;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float f0, df0, f1, df1;
+      activate_grad<ACT>(bf16_lo(g[q]), f0, df0);
+      activate_grad<ACT>(bf16_hi(g[q]), f1, df1);
+      const float d0 = bf16_lo(d[q]), d1 = bf16_hi(d[q]);
+      if (GATED) {
+        og[q] = cvt_pk_bf16(d0 * bf16_lo(u[q]) * df0, d1 * bf16_hi(u[q]) * df1);
+        ou[q] = cvt_pk_bf16(d0 * f0, d1 * f1);
+      } else {
+        og[q] = cvt_pk_bf16(d0 * df0, d1 * df1);
+      }
+    }
+    const int64_t to = r * p.ldo + c0;
+    *reinterpret_cast<u32x4_t *>(p.dgate + to) = og;
+    if (GATED) *reinterpret_cast<u32x4_t *>(p.dup + to) = ou;
+  }
+}
+
+// db[e][n] = the sum of dZ's rows of group e: 64 columns per workgroup, eight
+// lanes wide and 32 rows deep, fp32.
+struct BiasGradArgs {
+  const uint16_t *dz;
+  uint16_t *db;
+  ProductArgs p;  // offsets, rows, groups, lda
+  int32_t n;
+};
+
+__global__ void __launch_bounds__(256) bias_grad_kernel(BiasGradArgs a) {
+  __shared__ float part[32][64 + 1];
+  const int e = blockIdx.y, lane8 = threadIdx.x & 7, deep = threadIdx.x >> 3;
+  const int c0 = blockIdx.x * 64 + lane8 * 8;
+  const int64_t s = offset_at(a.p, e), t = offset_at(a.p, e + 1);
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t r = s + deep; r < t; r += 32) {
+    const u32x4_t v = load_chunk(a.dz + r * a.p.lda + c0, a.n - c0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      sum[2 * q] += bf16_lo(v[q]);
+      sum[2 * q + 1] += bf16_hi(v[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) part[deep][lane8 * 8 + q] = sum[q];
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    float total = 0.f;
+    for (int d = 0; d < 32; ++d) total += part[d][threadIdx.x];
+    const int col = blockIdx.x * 64 + threadIdx.x;
+    if (col < a.n) a.db[static_cast<int64_t>(e) * a.n + col] = f32_to_bf16_rne(total);
+  }
+}
+
+// ---- launchers -------------------------------------------------------------------
+
+rrb_status launched(const char *what) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? RRB_OK : fail(RRB_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+constexpr int kBM = 128, kBN = 128;
+
+template <int FORM, bool GATED>
+rrb_status launch_product(ProductArgs p, hipStream_t s) {
+  constexpr int cols = GATED ? kBN / 2 : kBN;
+  p.ntiles = (p.n + cols - 1) / cols;
+  int64_t grid;
+  if (FORM == kGradW) {
+    p.slots = (p.m + kBM - 1) / kBM * p.halves;
+    grid = static_cast<int64_t>(p.slots) * p.ntiles * p.groups;
+  } else {
+    p.slots = static_cast<int32_t>(p.rows / kBM) + p.groups;
+    grid = static_cast<int64_t>(p.slots) * p.ntiles;
+  }
+  if (grid > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
+  hipLaunchKernelGGL((product_kernel<kBM, kBN, 2, 2, FORM, GATED>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+  return launched("expert product");
+}
+
+int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+
+// What every entry point checks of its sizes.
+rrb_status check_spec(const rrb_expert_spec *s, const int32_t *offsets) {
+  if (!s) return fail(RRB_EINVAL, "NULL spec");
+  if (s->rows < 0 || s->in < 1 || s->out < 1 || s->groups < 1)
+    return fail(RRB_EINVAL, "rows %lld, in %lld, out %lld, groups %d: rows >= 0 and the others >= 1 needed",
+                (long long)s->rows, (long long)s->in, (long long)s->out, s->groups);
+  if (s->activation < RRB_ACT_NONE || s->activation > RRB_ACT_RELU)
+    return fail(RRB_EINVAL, "unknown activation %d", s->activation);
+  if (!offsets && s->groups != 1) return fail(RRB_EINVAL, "NULL offsets with %d groups", s->groups);
+  if (s->rows > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "rows %lld >= 2^31", (long long)s->rows);
+  if (s->in > kMaxWidth || s->out > kMaxWidth)
+    return fail(RRB_EUNSUPPORTED, "in %lld, out %lld: at most 2^20", (long long)s->in, (long long)s->out);
+  if (s->groups > kMaxGroups) return fail(RRB_EUNSUPPORTED, "groups %d: at most %d", s->groups, kMaxGroups);
+  return RRB_OK;
+}
+
+ProductArgs base_args(const rrb_expert_spec &s, const int32_t *offsets) {
+  ProductArgs p;
+  std::memset(&p, 0, sizeof p);
+  p.offsets = offsets;
+  p.rows = s.rows;
+  p.groups = s.groups;
+  p.halves = 1;
+  p.bstride = s.in * s.out;
+  return p;
+}
+
+template <bool GATED>
+rrb_status launch_act_grad(const ActGradArgs &a, int act, hipStream_t s) {
+  if (a.rows == 0) return RRB_OK;
+  const int64_t blocks = (a.rows * (a.ldo / 8) + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(blocks < 8192 ? blocks : 8192));
+  switch (act) {
+#define RRB_CASE(A)                                                                         \
+  case A:                                                                                   \
+    hipLaunchKernelGGL((act_grad_kernel<A, GATED>), grid, dim3(256), 0, s, a);              \
+    break;
+    RRB_CASE(RRB_ACT_NONE) RRB_CASE(RRB_ACT_SILU) RRB_CASE(RRB_ACT_GELU) RRB_CASE(RRB_ACT_GELU_TANH)
+    RRB_CASE(RRB_ACT_RELU)
+#undef RRB_CASE
+  }
+  return launched("activation gradient");
+}
+
+const uint16_t *u16(const void *p) { return static_cast<const uint16_t *>(p); }
+uint16_t *u16(void *p) { return static_cast<uint16_t *>(p); }
+
+}  // namespace
+}  // namespace rrb
+
+using namespace rrb;
+
+extern "C" {
+
+rrb_status rrb_expert_gated(const rrb_expert_spec *spec, const void *d_x, const int32_t *d_offsets,
+                            const void *d_w_gate, const void *d_w_up, void *d_out, void *d_save_gate,
+                            void *d_save_up, rrb_stream_t stream) {
+  clear_error();
+  rrb_status st = check_spec(spec, d_offsets);
+  if (st != RRB_OK) return st;
+  if (spec->rows == 0) return RRB_OK;
+  if (!d_x || !d_w_gate || !d_w_up || !d_out) return fail(RRB_EINVAL, "NULL x, w_gate, w_up or out");
+  if (!d_save_gate != !d_save_up) return fail(RRB_EINVAL, "save_gate and save_up go together");
+  ProductArgs p = base_args(*spec, d_offsets);
+  p.a[0] = p.a[1] = u16(d_x);
+  p.b[0] = u16(d_w_gate);
+  p.b[1] = u16(d_w_up);
+  p.c[0] = u16(d_out);
+  p.save[0] = u16(d_save_gate);
+  p.save[1] = u16(d_save_up);
+  p.lda = p.ldb = spec->in;
+  p.ldc = spec->out;
+  p.n = static_cast<int32_t>(spec->out);
+  p.k = static_cast<int32_t>(spec->in);
+  p.act = spec->activation;
+  p.cvec = p.ldc % 4 == 0 && aligned(d_out, 8) && aligned(d_save_gate, 8) && aligned(d_save_up, 8);
+  return launch_product<kForward, true>(p, static_cast<hipStream_t>(stream));
+}
+
+rrb_status rrb_expert_linear(const rrb_expert_spec *spec, const void *d_x, const int32_t *d_offsets,
+                             const void *d_w, const void *d_bias, const void *d_residual, void *d_out,
+                             void *d_save_pre, rrb_stream_t stream) {
+  clear_error();
+  rrb_status st = check_spec(spec, d_offsets);
+  if (st != RRB_OK) return st;
+  if (spec->rows == 0) return RRB_OK;
+  if (!d_x || !d_w || !d_out) return fail(RRB_EINVAL, "NULL x, w or out");
+  ProductArgs p = base_args(*spec, d_offsets);
+  p.a[0] = p.a[1] = u16(d_x);
+  p.b[0] = p.b[1] = u16(d_w);
+  p.c[0] = u16(d_out);
+  p.save[0] = u16(d_save_pre);
+  p.bias = u16(d_bias);
+  p.residual = u16(d_residual);
+  p.lda = p.ldb = spec->in;
+  p.ldc = spec->out;
+  p.n = static_cast<int32_t>(spec->out);
+  p.k = static_cast<int32_t>(spec->in);
+  p.act = spec->activation;
+  p.cvec = p.ldc % 4 == 0 && aligned(d_out, 8) && aligned(d_save_pre, 8) && aligned(d_bias, 8) &&
+           aligned(d_residual, 8);
+  return launch_product<kForward, false>(p, static_cast<hipStream_t>(stream));
+}
+
+rrb_status rrb_expert_gated_backward_workspace(const rrb_expert_spec *spec, size_t *bytes) {
+  clear_error();
+  if (!bytes) return fail(RRB_EINVAL, "NULL bytes");
+  *bytes = 0;
+  static const int32_t any = 0;
+  rrb_status st = check_spec(spec, &any);
+  if (st != RRB_OK) return st;
+  *bytes = static_cast<size_t>(2 * spec->rows * padded(spec->out) * 2);
+  return RRB_OK;
+}
+
+rrb_status rrb_expert_linear_backward_workspace(const rrb_expert_spec *spec, size_t *bytes) {
+  clear_error();
+  if (!bytes) return fail(RRB_EINVAL, "NULL bytes");
+  *bytes = 0;
+  static const int32_t any = 0;
+  rrb_status st = check_spec(spec, &any);
+  if (st != RRB_OK) return st;
+  *bytes = static_cast<size_t>(spec->rows * padded(spec->out) * 2);
+  return RRB_OK;
+}
+
+rrb_status rrb_expert_gated_backward(const rrb_expert_spec *spec, const void *d_dout, const void *d_x,
+                                     const int32_t *d_offsets, const void *d_w_gate, const void *d_w_up,
+                                     const void *d_gate, const void *d_up, void *d_dx, void *d_dw_gate,
+                                     void *d_dw_up, void *d_workspace, size_t workspace_bytes,
+                                     rrb_stream_t stream) {
+  clear_error();
+  rrb_status st = check_spec(spec, d_offsets);
+  if (st != RRB_OK) return st;
+  if (!d_dx && !d_dw_gate) return fail(RRB_EINVAL, "no gradient asked for");
+  if (!d_dw_gate != !d_dw_up) return fail(RRB_EINVAL, "dw_gate and dw_up go together");
+  size_t need = 0;
+  st = rrb_expert_gated_backward_workspace(spec, &need);
+  if (st != RRB_OK) return st;
+  if (spec->rows > 0) {
+    if (!d_dout || !d_gate || !d_up) return fail(RRB_EINVAL, "NULL dout, gate or up");
+    if (d_dx && (!d_w_gate || !d_w_up)) return fail(RRB_EINVAL, "NULL w_gate or w_up");
+    if (d_dw_gate && !d_x) return fail(RRB_EINVAL, "NULL x");
+    if (!d_workspace || workspace_bytes < need || !aligned(d_workspace, 16))
+      return fail(RRB_EINVAL, "workspace of %zu bytes, 16-byte aligned, needed", need);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t pitch = padded(spec->out);
+  uint16_t *dgate = u16(d_workspace);
+  uint16_t *dup = dgate ? dgate + spec->rows * pitch : nullptr;
+  ActGradArgs g;
+  std::memset(&g, 0, sizeof g);
+  g.dout = u16(d_dout);
+  g.gate = u16(d_gate);
+  g.up = u16(d_up);
+  g.dgate = dgate;
+  g.dup = dup;
+  g.offsets = d_offsets;
+  g.rows = spec->rows;
+  g.ldo = pitch;
+  g.n = static_cast<int32_t>(spec->out);
+  g.groups = spec->groups;
+  if ((st = launch_act_grad<true>(g, spec->activation, s)) != RRB_OK) return st;
+  ProductArgs p = base_args(*spec, d_offsets);
+  p.a[0] = dgate;
+  p.a[1] = dup;
+  p.lda = g.ldo;
+  p.halves = 2;
+  p.n = static_cast<int32_t>(spec->in);
+  if (d_dx && spec->rows > 0) {
+    ProductArgs q = p;
+    q.b[0] = u16(d_w_gate);
+    q.b[1] = u16(d_w_up);
+    q.c[0] = u16(d_dx);
+    q.ldb = q.ldc = spec->in;
+    q.k = static_cast<int32_t>(spec->out);
+    q.cvec = q.ldc % 4 == 0 && aligned(d_dx, 8);
+    if ((st = launch_product<kGradX, false>(q, s)) != RRB_OK) return st;
+  }
+  if (d_dw_gate) {
+    p.b[0] = p.b[1] = u16(d_x);
+    p.c[0] = u16(d_dw_gate);
+    p.c[1] = u16(d_dw_up);
+    p.ldb = p.ldc = spec->in;
+    p.m = static_cast<int32_t>(spec->out);
+    p.cvec = p.ldc % 4 == 0 && aligned(d_dw_gate, 8) && aligned(d_dw_up, 8);
+    if ((st = launch_product<kGradW, false>(p, s)) != RRB_OK) return st;
+  }
+  return RRB_OK;
+}
+
+rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d_dout, const void *d_x,
+                                      const int32_t *d_offsets, const void *d_w, const void *d_pre, void *d_dx,
+                                      void *d_dw, void *d_dbias, void *d_workspace, size_t workspace_bytes,
+                                      rrb_stream_t stream) {
+  clear_error();
+  rrb_status st = check_spec(spec, d_offsets);
+  if (st != RRB_OK) return st;
+  if (!d_dx && !d_dw && !d_dbias) return fail(RRB_EINVAL, "no gradient asked for");
+  size_t need = 0;
+  st = rrb_expert_linear_backward_workspace(spec, &need);
+  if (st != RRB_OK) return st;
+  const bool act = spec->activation != RRB_ACT_NONE;
+  if (spec->rows > 0) {
+    if (!d_dout) return fail(RRB_EINVAL, "NULL dout");
+    if (act && !d_pre) return fail(RRB_EINVAL, "an activation's gradient needs pre");
+    if (d_dx && !d_w) return fail(RRB_EINVAL, "NULL w");
+    if (d_dw && !d_x) return fail(RRB_EINVAL, "NULL x");
+    if (!d_workspace || workspace_bytes < need || !aligned(d_workspace, 16))
+      return fail(RRB_EINVAL, "workspace of %zu bytes, 16-byte aligned, needed", need);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ProductArgs p = base_args(*spec, d_offsets);
+  p.a[0] = p.a[1] = u16(d_dout);
+  p.lda = spec->out;
+  // Without an activation dZ is dY itself; rows that do not start on 16-byte
+  // boundaries are copied into padded ones first.
+  if (act || spec->out % 8 || !aligned(d_dout, 16)) {
+    ActGradArgs g;
+    std::memset(&g, 0, sizeof g);
+    g.dout = u16(d_dout);
+    g.gate = u16(d_pre);
+    g.dgate = u16(d_workspace);
+    g.offsets = d_offsets;
+    g.rows = spec->rows;
+    g.ldo = padded(spec->out);
+    g.n = static_cast<int32_t>(spec->out);
+    g.groups = spec->groups;
+    if ((st = launch_act_grad<false>(g, spec->activation, s)) != RRB_OK) return st;
+    p.a[0] = p.a[1] = g.dgate;
+    p.lda = g.ldo;
+  }
+  p.n = static_cast<int32_t>(spec->in);
+  if (d_dx && spec->rows > 0) {
+    ProductArgs q = p;
+    q.b[0] = q.b[1] = u16(d_w);
+    q.c[0] = u16(d_dx);
+    q.ldb = q.ldc = spec->in;
+    q.k = static_cast<int32_t>(spec->out);
+    q.cvec = q.ldc % 4 == 0 && aligned(d_dx, 8);
+    if ((st = launch_product<kGradX, false>(q, s)) != RRB_OK) return st;
+  }
+  if (d_dw) {
+    ProductArgs q = p;
+    q.b[0] = q.b[1] = u16(d_x);
+    q.c[0] = q.c[1] = u16(d_dw);
+    q.ldb = q.ldc = spec->in;
+    q.m = static_cast<int32_t>(spec->out);
+    q.cvec = q.ldc % 4 == 0 && aligned(d_dw, 8);
+    if ((st = launch_product<kGradW, false>(q, s)) != RRB_OK) return st;
+  }
+  if (d_dbias) {
+    BiasGradArgs b;
+    std::memset(&b, 0, sizeof b);
+    b.dz = p.a[0];
+    b.db = u16(d_dbias);
+    b.p = p;
+    b.n = static_cast<int32_t>(spec->out);
+    hipLaunchKernelGGL(bias_grad_kernel, dim3(static_cast<unsigned>((spec->out + 63) / 64), spec->groups), dim3(256),
+                       0, s, b);
+    if ((st = launched("bias gradient")) != RRB_OK) return st;
+  }
+  return RRB_OK;
+}
+
+}  // extern "C"

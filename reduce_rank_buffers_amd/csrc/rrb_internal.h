@@ -113,6 +113,14 @@ rrb_status clear_route_maps(const Plan &plan, void *stream);
 rrb_status launch_rows(const Plan &plan, const void *const *in, void *const *out,
                        const float *d_weights, void *stream);
 
+// Launches a combine plan's gradient: dz (nullable) and d_dweights (nullable;
+// z is read for it alone) (rrb_moe.hip).
+rrb_status launch_combine_backward(const Plan &plan, const void *const *dy, const void *const *z,
+                                   void *const *dz, const float *d_weights, float *d_dweights,
+                                   void *stream);
+// Copies a device-routed plan's expert offsets and their total (rrb_moe.hip).
+rrb_status launch_expert_offsets(const Plan &plan, int32_t *d_offsets, void *stream);
+
 constexpr int kSlotRankShift = 26;
 constexpr int32_t kSlotRowMask = (1 << kSlotRankShift) - 1;
 

@@ -298,6 +298,70 @@ __global__ void __launch_bounds__(256) moe_combine_elem_kernel(RowArgs a) {
   }
 }
 
+// ---- the combine's gradient --------------------------------------------------
+//
+// With y[t] = sum over j of w_j z[slot_j]: dz[slot_j] = w_j dy[t] (rounded once
+// to bf16) and dw_j = <dy[t], z[slot_j]> (fp32).  Every arena row belongs to
+// one (token, expert), so each is written once and no sum crosses workgroups.
+
+struct BackArgs {
+  const unsigned char *dy[RRB_MAX_RANKS];
+  const unsigned char *z[RRB_MAX_RANKS];
+  unsigned char *dz[RRB_MAX_RANKS];
+  float *dw;  // [T][k] in routing order, or NULL: z is not read
+  RowArgs r;  // maps, weights, sizes
+};
+
+// Sum over the workgroup's `waves` waves of one value per thread; thread 0
+// holds it.
+__device__ __forceinline__ float block_sum(float v, float *part) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float total = 0.f;
+  for (unsigned q = 0; q < blockDim.x / 64; ++q) total += part[q];
+  return total;
+}
+
+// One workgroup per token, its k rows in turn.  Any top-k, width and
+// alignment.
+__global__ void __launch_bounds__(256) moe_combine_backward_kernel(BackArgs b) {
+  __shared__ float part[4];
+  const RowArgs &a = b.r;
+  if (route_failed(a)) return;
+  const int64_t t = blockIdx.x;
+  const int64_t rank = t / a.tokens_per_rank;
+  const uint16_t *dy = reinterpret_cast<const uint16_t *>(b.dy[rank] + (t - rank * a.tokens_per_rank) * a.row_bytes);
+  for (int j = 0; j < a.k; ++j) {
+    const int32_t s = a.slot[t * a.k + j];
+    const int32_t c = a.col[t * a.k + j];
+    const float w = a.wover ? a.wover[t * a.k + c] : a.weight[t * a.k + j];
+    const int64_t at = static_cast<int64_t>(s & kSlotRowMask) * a.row_bytes;
+    const uint16_t *z = reinterpret_cast<const uint16_t *>(b.z[s >> kSlotRankShift] + at);
+    uint16_t *dz = b.dz[s >> kSlotRankShift] ? reinterpret_cast<uint16_t *>(b.dz[s >> kSlotRankShift] + at) : nullptr;
+    float dot = 0.f;
+    for (int64_t i = threadIdx.x; i < a.hidden; i += 256) {
+      const float d = bf16_to_f32(dy[i]);
+      if (b.dw) dot = __builtin_fmaf(d, bf16_to_f32(z[i]), dot);
+      if (dz) dz[i] = f32_to_bf16_rne(w * d);
+    }
+    if (b.dw) {
+      dot = block_sum(dot, part);
+      if (threadIdx.x == 0) b.dw[t * a.k + c] = dot;
+    }
+  }
+}
+
+// A device-routed plan's expert offsets and their total; zeros (no rows)
+// after a failed routing.
+__global__ void moe_expert_offsets_kernel(const int32_t *expert_off, const int32_t *status, int32_t *out,
+                                          int32_t experts, int32_t total) {
+  const int e = blockIdx.x * blockDim.x + threadIdx.x;
+  if (e > experts) return;
+  out[e] = *status != 0 ? 0 : e < experts ? expert_off[e] : total;
+}
 
 // ---- device-side routing maps ----------------------------------------------
 //
@@ -995,6 +1059,45 @@ rrb_status launch_rows(const Plan &p, const void *const *in, void *const *out, c
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(RRB_EHIP, "moe launch: %s", hipGetErrorString(e));
   return RRB_OK;
+}
+
+rrb_status launch_combine_backward(const Plan &p, const void *const *dy, const void *const *z, void *const *dz,
+                                   const float *d_weights, float *d_dweights, void *stream) {
+  const RowMaps &m = p.rows;
+  if (m.tokens == 0) return RRB_OK;
+  if (m.tokens > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tokens for one launch");
+  BackArgs b;
+  std::memset(&b, 0, sizeof b);
+  for (int32_t r = 0; r < p.nranks; ++r) {
+    b.dy[r] = static_cast<const unsigned char *>(dy[r]);
+    b.z[r] = z ? static_cast<const unsigned char *>(z[r]) : nullptr;
+    b.dz[r] = dz ? static_cast<unsigned char *>(dz[r]) : nullptr;
+  }
+  const char *ws = static_cast<const char *>(p.d_ws);
+  RowArgs &a = b.r;
+  a.slot = reinterpret_cast<const int32_t *>(ws + m.off_slot);
+  a.weight = reinterpret_cast<const float *>(ws + m.off_weight);
+  a.col = reinterpret_cast<const int32_t *>(ws + m.off_col);
+  a.wover = d_weights;
+  if (p.kind == PlanKind::RowsDevice) a.route_status = reinterpret_cast<const int32_t *>(ws + m.off_status);
+  a.tokens_per_rank = m.tokens / p.nranks;
+  a.row_bytes = m.hidden * 2;
+  a.hidden = m.hidden;
+  a.k = m.topk;
+  b.dw = d_dweights;
+  hipLaunchKernelGGL(moe_combine_backward_kernel, dim3(static_cast<unsigned>(m.tokens)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), b);
+  return route_launch_check("combine backward");
+}
+
+rrb_status launch_expert_offsets(const Plan &p, int32_t *d_offsets, void *stream) {
+  const RowMaps &m = p.rows;
+  const char *ws = static_cast<const char *>(p.d_ws);
+  hipLaunchKernelGGL(moe_expert_offsets_kernel, dim3(static_cast<unsigned>(m.experts / 256 + 1)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), reinterpret_cast<const int32_t *>(ws + m.off_expert),
+                     reinterpret_cast<const int32_t *>(ws + m.off_status), d_offsets, m.experts,
+                     static_cast<int32_t>(m.tokens * m.topk));
+  return route_launch_check("expert offsets");
 }
 
 }  // namespace rrb
