@@ -273,6 +273,96 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (
 
 // ---- the tiled product ------------------------------------------------------------
 
+// Where a workgroup's tile lies: operand bases at the tile's first row (or
+// column) and extents.
+struct Place {
+  const uint16_t *a[2], *b[2];
+  uint16_t *c;
+  int64_t row0, klen;   // klen: reduction length (per phase)
+  int32_t e, n0, m0, mvalid;
+  bool empty;
+};
+
+// BM x NCOLS outputs per tile.
+template <int BM, int NCOLS, int FORM>
+__device__ __forceinline__ Place place_tile(const ProductArgs &p) {
+  Place t;
+  const int slot = blockIdx.x % p.slots;
+  const int rest = blockIdx.x / p.slots;
+  t.empty = false;
+  t.row0 = 0;
+  t.m0 = 0;
+  if (FORM == kGradW) {
+    t.n0 = rest % p.ntiles * NCOLS;
+    t.e = rest / p.ntiles;
+    const int mt = p.slots / p.halves;
+    const int half = slot / mt;
+    t.m0 = (slot - half * mt) * BM;
+    const int64_t first = uniform64(offset_at(p, t.e)), last = uniform64(offset_at(p, t.e + 1));
+    t.klen = last > first ? last - first : 0;
+    t.mvalid = p.m - t.m0;
+    t.a[0] = t.a[1] = p.a[half] + first * p.lda + t.m0;
+    t.b[0] = t.b[1] = p.b[0] + first * p.ldb + t.n0;
+    t.c = p.c[half] + t.e * p.bstride + static_cast<int64_t>(t.m0) * p.ldc;
+  } else {
+    t.n0 = rest * NCOLS;
+    t.e = uniform(group_of_slot<BM>(p, slot));
+    const int64_t first = uniform64(offset_at(p, t.e)), last = uniform64(offset_at(p, t.e + 1));
+    const int64_t mt = slot - (first / BM + t.e);
+    t.row0 = first + mt * BM;
+    t.empty = mt < 0 || t.row0 >= last;
+    t.mvalid = last - t.row0 < BM ? static_cast<int>(last - t.row0) : BM;
+    t.klen = p.k;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      t.a[h] = p.a[FORM == kGradX ? h : 0] + t.row0 * p.lda;
+      t.b[h] = p.b[h] + t.e * p.bstride + (FORM == kForward ? static_cast<int64_t>(t.n0) * p.ldb : t.n0);
+    }
+    t.c = p.c[0] + t.row0 * p.ldc;
+  }
+  return t;
+}
+
+// Stores a wave's part of the tile, at rows wm and output columns wn of it.
+template <int FORM, bool GATED, int FM, int FN>
+__device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t, const f32x4_t (&acc)[FM][FN], int wm,
+                                            int wn) {
+  const int n = t.n0 + wn;
+  if (FORM != kForward) {
+    store_tile<RRB_ACT_NONE, false>(p, acc, t.c, nullptr, nullptr, nullptr, nullptr, wm, t.mvalid, n);
+    return;
+  }
+  uint16_t *s0 = p.save[0] ? p.save[0] + t.row0 * p.ldc : nullptr;
+  uint16_t *s1 = p.save[1] ? p.save[1] + t.row0 * p.ldc : nullptr;
+  const uint16_t *bias = p.bias ? p.bias + static_cast<int64_t>(t.e) * p.n : nullptr;
+  const uint16_t *res = p.residual ? p.residual + t.row0 * p.ldc : nullptr;
+  switch (p.act) {
+#define RRB_CASE(A)                                                          \
+  case A:                                                                    \
+    store_tile<A, GATED>(p, acc, t.c, s0, s1, bias, res, wm, t.mvalid, n);   \
+    break;
+    RRB_CASE(RRB_ACT_SILU) RRB_CASE(RRB_ACT_GELU) RRB_CASE(RRB_ACT_GELU_TANH) RRB_CASE(RRB_ACT_RELU)
+#undef RRB_CASE
+    default: store_tile<RRB_ACT_NONE, GATED>(p, acc, t.c, s0, s1, bias, res, wm, t.mvalid, n);
+  }
+}
+
+template <int FM, int FN>
+__device__ __forceinline__ void clear_tile(f32x4_t (&acc)[FM][FN]) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+}
+
+// Row j of a gated B tile: blocks of 16 gate rows and 16 up rows by turns, so
+// that a lane holds both projections of its outputs.
+__device__ __forceinline__ int gated_row(int j) { return (j >> 5) * 16 + (j & 15); }
+__device__ __forceinline__ bool gated_up(int j) { return j & 16; }
+
+// Operands whose rows do not start on 16-byte boundaries: tiles go through
+// registers, with 16-byte loads that need no alignment and the last, partial
+// chunk of a row read element by element.
 template <int BM, int BN, int WR, int WC, int FORM, bool GATED>
 __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
   constexpr int NT = WR * WC * 64;
@@ -280,46 +370,13 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
   constexpr int A_BYTES = BM * kStep * 2, B_BYTES = BN * kStep * 2;
   constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT;  // 16-byte chunks per thread
   constexpr bool A_COL = FORM == kGradW, B_COL = FORM != kForward;
-  constexpr int NCOLS = GATED ? BN / 2 : BN;  // output columns per tile
   __shared__ __align__(16) unsigned char lds[2 * (A_BYTES + B_BYTES)];
 
   const int tid = threadIdx.x;
   const int wave = uniform(tid >> 6);
-  const int slot = blockIdx.x % p.slots;
-  const int rest = blockIdx.x / p.slots;
-  const int nt = FORM == kGradW ? rest % p.ntiles : rest;
-  const int n0 = nt * NCOLS;
-
-  // The tile's place: operand bases and extents.
-  const uint16_t *a[2], *b[2];
-  uint16_t *c;
-  int64_t klen, row0 = 0;
-  int mvalid, half = 0, e, m0 = 0;
-  if (FORM == kGradW) {
-    e = rest / p.ntiles;
-    const int mt = p.slots / p.halves;
-    half = slot / mt;
-    m0 = (slot - half * mt) * BM;
-    const int64_t s = uniform64(offset_at(p, e)), t = uniform64(offset_at(p, e + 1));
-    klen = t > s ? t - s : 0;
-    mvalid = p.m - m0;
-    a[0] = a[1] = p.a[half] + s * p.lda + m0;
-    b[0] = b[1] = p.b[0] + s * p.ldb + n0;
-    c = p.c[half] + e * p.bstride + static_cast<int64_t>(m0) * p.ldc;
-  } else {
-    e = uniform(group_of_slot<BM>(p, slot));
-    const int64_t s = uniform64(offset_at(p, e)), t = uniform64(offset_at(p, e + 1));
-    const int64_t mt = slot - (s / BM + e);
-    row0 = s + mt * BM;
-    if (mt < 0 || row0 >= t) return;
-    mvalid = t - row0 < BM ? static_cast<int>(t - row0) : BM;
-    klen = p.k;
-    for (int h = 0; h < 2; ++h) {
-      a[h] = p.a[FORM == kGradX ? h : 0] + row0 * p.lda;
-      b[h] = p.b[h] + e * p.bstride + (FORM == kForward ? static_cast<int64_t>(n0) * p.ldb : n0);
-    }
-    c = p.c[0] + row0 * p.ldc;
-  }
+  const Place t = place_tile<BM, GATED ? BN / 2 : BN, FORM>(p);
+  if (t.empty) return;
+  const int64_t klen = t.klen;
   const int64_t per = (klen + kStep - 1) / kStep;  // steps per phase
   const int steps = static_cast<int>(FORM == kGradX ? per * p.halves : per);
 
@@ -334,11 +391,11 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
       if (A_COL) {
         const int kr = id / (BM / 8), pos = id % (BM / 8);
         const int ch = pos ^ (col_swizzle(kr) << 1);
-        ra[i] = load_chunk(a[0] + (k0 + kr) * p.lda + ch * 8, k0 + kr < klen ? p.m - m0 - ch * 8 : 0);
+        ra[i] = load_chunk(t.a[0] + (k0 + kr) * p.lda + ch * 8, k0 + kr < klen ? p.m - t.m0 - ch * 8 : 0);
       } else {
         const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
         const int64_t have = klen - k0 - ch * 8;
-        ra[i] = load_chunk(a[h] + r * p.lda + k0 + ch * 8, r < mvalid ? have : 0);
+        ra[i] = load_chunk(t.a[h] + r * p.lda + k0 + ch * 8, r < t.mvalid ? have : 0);
       }
     }
 #pragma unroll
@@ -347,15 +404,13 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
       if (B_COL) {
         const int kr = id / (BN / 8), pos = id % (BN / 8);
         const int ch = pos ^ (col_swizzle(kr) << 1);
-        rb[i] = load_chunk(b[h] + (k0 + kr) * p.ldb + ch * 8, k0 + kr < klen ? p.n - n0 - ch * 8 : 0);
+        rb[i] = load_chunk(t.b[h] + (k0 + kr) * p.ldb + ch * 8, k0 + kr < klen ? p.n - t.n0 - ch * 8 : 0);
       } else {
         const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
         const int64_t have = klen - k0 - ch * 8;
-        // Gated: blocks of 16 gate rows and 16 up rows by turns, so a lane
-        // holds both projections of its outputs.
-        const int n = GATED ? (r >> 5) * 16 + (r & 15) : r;
-        const uint16_t *src = GATED && (r & 16) ? b[1] : b[0];
-        rb[i] = load_chunk(src + n * p.ldb + k0 + ch * 8, n0 + n < p.n ? have : 0);
+        const int n = GATED ? gated_row(r) : r;
+        const uint16_t *src = GATED && gated_up(r) ? t.b[1] : t.b[0];
+        rb[i] = load_chunk(src + n * p.ldb + k0 + ch * 8, t.n0 + n < p.n ? have : 0);
       }
     }
   };
@@ -369,11 +424,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
 
   const int wm = wave / WC * (BM / WR), wn = wave % WC * (BN / WC);
   f32x4_t acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
+  clear_tile(acc);
   if (steps > 0) {
     fetch(0);
     commit(0);
@@ -399,25 +450,153 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
     }
     if (s + 1 < steps) commit((s + 1) & 1);
   }
+  finish_tile<FORM, GATED>(p, t, acc, wm, GATED ? wn / 2 : wn);
+}
 
-  const int wn0 = n0 + (GATED ? wn / 2 : wn);
-  if (FORM != kForward) {
-    store_tile<RRB_ACT_NONE, false>(p, acc, c, nullptr, nullptr, nullptr, nullptr, wm, mvalid, wn0);
-  } else {
-    uint16_t *s0 = p.save[0] ? p.save[0] + row0 * p.ldc : nullptr;
-    uint16_t *s1 = p.save[1] ? p.save[1] + row0 * p.ldc : nullptr;
-    const uint16_t *bias = p.bias ? p.bias + static_cast<int64_t>(e) * p.n : nullptr;
-    const uint16_t *res = p.residual ? p.residual + row0 * p.ldc : nullptr;
-    switch (p.act) {
-#define RRB_CASE(A)                                                                    \
-  case A:                                                                              \
-    store_tile<A, GATED>(p, acc, c, s0, s1, bias, res, wm, mvalid, wn0);               \
-    break;
-      RRB_CASE(RRB_ACT_SILU) RRB_CASE(RRB_ACT_GELU) RRB_CASE(RRB_ACT_GELU_TANH) RRB_CASE(RRB_ACT_RELU)
-#undef RRB_CASE
-      default: store_tile<RRB_ACT_NONE, GATED>(p, acc, c, s0, s1, bias, res, wm, mvalid, wn0);
+// ---- the tiled product, loads straight to LDS -----------------------------------
+//
+// Operands with rows on 16-byte boundaries.  Each lane moves 16-byte chunks
+// from memory to LDS without a register (buffer_load_dwordx4 ... lds): a wave
+// fills 1 KiB in lane order, so the swizzle is applied to the address each
+// lane reads.  Rows past a tile's last valid one read that row again (their
+// results are not stored); chunks past the reduction's end, and rows of a
+// column tile past it, lie outside the descriptor and arrive as zeros, on both
+// sides, so that nothing behind a group reaches its sums.
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const uint16_t *base, int64_t bytes) {
+  const int64_t n = bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(base), static_cast<short>(0),
+                                           static_cast<int>(n), 0x00020000);
+}
+constexpr int kOutside = 0x7fffffff;
+
+// 16 bytes per lane from `d` at voffset + soffset to LDS at `to` (the wave's
+// first byte) + 16 * lane.  The host pass of the compiler does not know the
+// 16-byte form.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t d, unsigned char *to, int voffset, int soffset) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(d, (__attribute__((address_space(3))) void *)to, 16, voffset, soffset, 0, 0);
+#endif
+}
+
+template <int BM, int BN, int WR, int WC, int FORM, bool GATED>
+__global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs p) {
+  constexpr int NT = WR * WC * 64;
+  constexpr int FM = BM / WR / 16, FN = BN / WC / 16;
+  constexpr int A_BYTES = BM * kStep * 2, B_BYTES = BN * kStep * 2;
+  constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT;
+  constexpr bool A_COL = FORM == kGradW, B_COL = FORM != kForward;
+  __shared__ __align__(16) unsigned char lds[2 * (A_BYTES + B_BYTES)];
+
+  const int tid = threadIdx.x;
+  const int wave = uniform(tid >> 6);
+  const Place t = place_tile<BM, GATED ? BN / 2 : BN, FORM>(p);
+  if (t.empty) return;
+  const int64_t klen = t.klen;
+  const int per = static_cast<int>((klen + kStep - 1) / kStep);  // steps per phase
+  const int steps = FORM == kGradX ? per * p.halves : per;
+  const int lda2 = static_cast<int>(p.lda * 2), ldb2 = static_cast<int>(p.ldb * 2);
+
+  // Byte offsets of this thread's chunks in a step's tile.
+  int va[CA], vb[CB];
+#pragma unroll
+  for (int i = 0; i < CA; ++i) {
+    const int id = i * NT + tid;
+    if (A_COL) {
+      const int kr = id / (BM / 8), pos = id % (BM / 8);
+      va[i] = kr * lda2 + (pos ^ (col_swizzle(kr) << 1)) * 16;
+    } else {
+      const int r = id >> 3;
+      va[i] = (r < t.mvalid ? r : t.mvalid - 1) * lda2 + ((id & 7) ^ row_swizzle(r)) * 16;
     }
   }
+#pragma unroll
+  for (int i = 0; i < CB; ++i) {
+    const int id = i * NT + tid;
+    if (B_COL) {
+      const int kr = id / (BN / 8), pos = id % (BN / 8);
+      vb[i] = kr * ldb2 + (pos ^ (col_swizzle(kr) << 1)) * 16;
+    } else {
+      const int r = id >> 3;
+      const int n = GATED ? gated_row(r) : r;
+      vb[i] = (t.n0 + n < p.n ? n : p.n - 1 - t.n0) * ldb2 + ((id & 7) ^ row_swizzle(r)) * 16;
+    }
+  }
+
+  // Starts one step's loads into buffer `buf`.
+  auto issue = [&](int step, int buf) {
+    const int h = FORM == kGradX && step >= per ? 1 : 0;
+    const int kstep = step - h * per;
+    const int64_t k0 = static_cast<int64_t>(kstep) * kStep;
+    const int64_t left = klen - k0;
+    unsigned char *ta = lds + buf * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;
+    if (A_COL) {
+      const auto d = descriptor(t.a[0] + k0 * p.lda, left * lda2 - static_cast<int64_t>(t.m0) * 2);
+#pragma unroll
+      for (int i = 0; i < CA; ++i)
+        load_to_lds(d, ta + (i * NT + wave * 64) * 16, va[i], 0);
+    } else {
+      const auto d = descriptor(t.a[h], static_cast<int64_t>(t.mvalid) * lda2);
+#pragma unroll
+      for (int i = 0; i < CA; ++i) {
+        int v = va[i];
+        if (left < kStep) {
+          const int id = i * NT + tid;
+          if (((id & 7) ^ row_swizzle(id >> 3)) * 8 >= left) v = kOutside;
+        }
+        load_to_lds(d, ta + (i * NT + wave * 64) * 16, v, kstep * 128);
+      }
+    }
+    if (B_COL) {
+      const auto d = descriptor(t.b[h] + k0 * p.ldb, left * ldb2 - static_cast<int64_t>(t.n0) * 2);
+#pragma unroll
+      for (int i = 0; i < CB; ++i)
+        load_to_lds(d, tb + (i * NT + wave * 64) * 16, vb[i], 0);
+    } else {
+      const int64_t bytes = static_cast<int64_t>(p.n - t.n0) * ldb2;
+      const auto d0 = descriptor(t.b[0], bytes);
+      const auto d1 = descriptor(GATED ? t.b[1] : t.b[0], bytes);
+#pragma unroll
+      for (int i = 0; i < CB; ++i) {
+        int v = vb[i];
+        if (left < kStep) {
+          const int id = i * NT + tid;
+          if (((id & 7) ^ row_swizzle(id >> 3)) * 8 >= left) v = kOutside;
+        }
+        // The wave's eight rows are all gate rows or all up rows.
+        const bool up = GATED && gated_up((i * NT + wave * 64) >> 3);
+        load_to_lds(up ? d1 : d0, tb + (i * NT + wave * 64) * 16, v, kstep * 128);
+      }
+    }
+  };
+
+  const int wm = wave / WC * (BM / WR), wn = wave % WC * (BN / WC);
+  f32x4_t acc[FM][FN];
+  clear_tile(acc);
+  if (steps > 0) issue(0, 0);
+  for (int s = 0; s < steps; ++s) {
+    // This step's loads have landed, and every wave is done with the other
+    // buffer.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (s + 1 < steps) issue(s + 1, (s + 1) & 1);
+    const unsigned char *ta = lds + (s & 1) * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;
+#pragma unroll
+    for (int kk = 0; kk < kStep / 32; ++kk) {
+      bf16x8_t fa[FM], fb[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        fb[j] = B_COL ? col_fragment<BN>(tb, wn + j * 16, kk) : row_fragment(tb, wn + j * 16, kk);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        fa[i] = A_COL ? col_fragment<BM>(ta, wm + i * 16, kk) : row_fragment(ta, wm + i * 16, kk);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  finish_tile<FORM, GATED>(p, t, acc, wm, GATED ? wn / 2 : wn);
 }
 
 // ---- gradients before the activation -------------------------------------------
@@ -516,23 +695,30 @@ rrb_status launched(const char *what) {
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-constexpr int kBM = 128, kBN = 128;
-
-template <int FORM, bool GATED>
-rrb_status launch_product(ProductArgs p, hipStream_t s) {
-  constexpr int cols = GATED ? kBN / 2 : kBN;
+// Launches the form over BM x BN tiles with the given kernel.
+template <int BM, int BN, int FORM, bool GATED>
+rrb_status launch_tiles(void (*kernel)(ProductArgs), int threads, ProductArgs p, hipStream_t s) {
+  constexpr int cols = GATED ? BN / 2 : BN;
   p.ntiles = (p.n + cols - 1) / cols;
   int64_t grid;
   if (FORM == kGradW) {
-    p.slots = (p.m + kBM - 1) / kBM * p.halves;
+    p.slots = (p.m + BM - 1) / BM * p.halves;
     grid = static_cast<int64_t>(p.slots) * p.ntiles * p.groups;
   } else {
-    p.slots = static_cast<int32_t>(p.rows / kBM) + p.groups;
+    p.slots = static_cast<int32_t>(p.rows / BM) + p.groups;
     grid = static_cast<int64_t>(p.slots) * p.ntiles;
   }
   if (grid > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
-  hipLaunchKernelGGL((product_kernel<kBM, kBN, 2, 2, FORM, GATED>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, p);
   return launched("expert product");
+}
+
+template <int FORM, bool GATED>
+rrb_status launch_product(const ProductArgs &p, hipStream_t s) {
+  bool direct = p.lda % 8 == 0 && p.ldb % 8 == 0;
+  for (int h = 0; h < 2; ++h) direct = direct && aligned(p.a[h], 16) && aligned(p.b[h], 16);
+  if (!direct) return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
+  return launch_tiles<256, 256, FORM, GATED>(product_direct_kernel<256, 256, 2, 4, FORM, GATED>, 512, p, s);
 }
 
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
