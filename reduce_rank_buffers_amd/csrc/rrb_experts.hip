@@ -96,13 +96,14 @@ struct ProductArgs {
   uint16_t *save[2];     // kForward: pre-activation values to keep, or NULL
   const uint16_t *bias, *residual;
   const int32_t *offsets;  // [groups + 1], or NULL: one group of all rows
-  int64_t rows;
+  int32_t rows;
   int64_t lda, ldb, ldc;  // row pitches, in elements
   int64_t bstride;        // kForward, kGradX: weight elements per group (kGradW: dW's)
   int32_t groups;
   int32_t m, n, k;        // m: kGradW only; k: kForward, kGradX only
   int32_t slots;          // kForward, kGradX: row-tile slots; kGradW: m tiles of both outputs
   int32_t ntiles;
+  int32_t bm, bn;         // tiles of one XCD's block: bm slots x bn column tiles
   int32_t halves;         // kGradX: phases; kGradW: outputs
   int32_t act;
   int32_t cvec;           // every output row starts on an 8-byte boundary
@@ -110,9 +111,9 @@ struct ProductArgs {
 
 // Offsets as the kernels read them: inside the arena whatever the array
 // holds.
-__device__ __forceinline__ int64_t offset_at(const ProductArgs &p, int e) {
+__device__ __forceinline__ int32_t offset_at(const ProductArgs &p, int e) {
   if (!p.offsets) return e == 0 ? 0 : p.rows;
-  const int64_t v = p.offsets[e];
+  const int32_t v = p.offsets[e];
   return v < 0 ? 0 : v > p.rows ? p.rows : v;
 }
 
@@ -138,9 +139,10 @@ __device__ __forceinline__ int group_of_slot(const ProductArgs &p, int slot) {
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
+__device__ __forceinline__ const uint16_t *uniform(const uint16_t *q) {
+  const uint64_t v = reinterpret_cast<uint64_t>(q);
   const uint32_t lo = uniform(static_cast<int>(v)), hi = uniform(static_cast<int>(v >> 32));
-  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+  return reinterpret_cast<const uint16_t *>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 // ---- operand tiles in LDS -----------------------------------------------------
@@ -194,79 +196,98 @@ __device__ __forceinline__ u32x4_t load_chunk(const uint16_t *src, int64_t have)
   return v;
 }
 
-// Four consecutive columns of one row.
-__device__ __forceinline__ void load4(const uint16_t *src, int have, bool vec, float (&v)[4]) {
-  if (vec && have >= 4) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(src);
-    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+// W consecutive columns of one row, W = 4 or 8, as fp32.
+template <int W>
+__device__ __forceinline__ void load_cols(const uint16_t *src, int have, bool whole, float (&v)[W]) {
+  if (whole) {
+#pragma unroll
+    for (int q = 0; q < W; q += 4) {
+      const uint2 w = *reinterpret_cast<const uint2 *>(src + q);
+      v[q] = bf16_lo(w.x); v[q + 1] = bf16_hi(w.x); v[q + 2] = bf16_lo(w.y); v[q + 3] = bf16_hi(w.y);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < have ? bf16_to_f32(src[i]) : 0.f;
+    for (int q = 0; q < W; ++q) v[q] = q < have ? bf16_to_f32(src[q]) : 0.f;
   }
 }
-__device__ __forceinline__ void store4(uint16_t *dst, int have, bool vec, const float (&v)[4]) {
-  const uint32_t lo = cvt_pk_bf16(v[0], v[1]), hi = cvt_pk_bf16(v[2], v[3]);
-  if (vec && have >= 4) {
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
-  } else {
-    const uint32_t w[2] = {lo, hi};
+template <int W>
+__device__ __forceinline__ void store_cols(uint16_t *dst, int have, bool whole, const float (&v)[W]) {
+  uint32_t w[W / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < have) dst[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+  for (int q = 0; q < W / 2; ++q) w[q] = cvt_pk_bf16(v[2 * q], v[2 * q + 1]);
+  if (whole) {
+    if (W == 8) {
+      // The pair of stores becomes one of 16 bytes where the pitch allows;
+      // rows are known to start on 8-byte boundaries only.
+      typedef uint32_t __attribute__((ext_vector_type(4), aligned(8))) quad;
+      *reinterpret_cast<quad *>(dst) = quad{w[0], w[1], w[W / 2 - 2], w[W / 2 - 1]};
+    } else {
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < W; ++q)
+      if (q < have) dst[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
   }
 }
 
 // ---- epilogue -------------------------------------------------------------------
 //
-// The fragments are computed as B x A, so lane l holds row l % 16 and the four
-// consecutive columns 4 (l / 16) .. + 3 of each 16 x 16 block.
-template <int ACT, bool GATED, int FM, int FN>
+// The fragments are computed as B x A, so lane l holds row l % 16 and four
+// consecutive columns of each 16 x 16 block: 4 (l / 16) .. + 3, or, where two
+// blocks were dealt together (WIDE), the first or second half of eight at
+// 8 (l / 16).  Gated: blocks are gate and up by turns.
+// `whole`: rows start on 8-byte boundaries and all of the wave's columns exist.
+template <int ACT, bool GATED, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (&acc)[FM][FN], uint16_t *c,
                                            uint16_t *save0, uint16_t *save1, const uint16_t *bias,
-                                           const uint16_t *residual, int m0, int mvalid, int n0) {
+                                           const uint16_t *residual, int m0, int mvalid, int n0, bool whole) {
+  constexpr int W = WIDE ? 8 : 4;                       // consecutive columns per lane
+  constexpr int BLOCKS = (GATED ? 2 : 1) * (WIDE ? 2 : 1);  // blocks that make them
   const int lane = threadIdx.x & 63;
-  const bool vec = p.cvec;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int m = m0 + i * 16 + (lane & 15);
-    if (m >= mvalid) continue;
-    const int64_t row = m * p.ldc;
+  for (int j = 0; j < FN; j += BLOCKS) {
+    const int n = n0 + j / BLOCKS * W * 4 + (lane >> 4) * W;
+    const int have = p.n - n;
+    float b[W];
+    if (!GATED && bias && have > 0) load_cols<W>(bias + n, have, whole, b);
 #pragma unroll
-    for (int j = 0; j < FN; j += GATED ? 2 : 1) {
-      const int n = n0 + (GATED ? j / 2 : j) * 16 + (lane >> 4) * 4;
-      const int have = p.n - n;
-      if (have <= 0) continue;
-      float v[4];
+    for (int i = 0; i < FM; ++i) {
+      const int m = m0 + i * 16 + (lane & 15);
+      if (m >= mvalid || have <= 0) continue;
+      const int64_t at = m * p.ldc + n;
+      float v[W];
       if (GATED) {
-        float u[4];
+        float u[W];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = acc[i][j][q], u[q] = acc[i][j + (GATED ? 1 : 0)][q];
+        for (int q = 0; q < W; ++q) {
+          v[q] = acc[i][j + (q >> 2) * 2][q & 3];
+          u[q] = acc[i][j + (q >> 2) * 2 + (GATED ? 1 : 0)][q & 3];
+        }
         if (save0) {
-          store4(save0 + row + n, have, vec, v);
-          store4(save1 + row + n, have, vec, u);
+          store_cols<W>(save0 + at, have, whole, v);
+          store_cols<W>(save1 + at, have, whole, u);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = activate<ACT>(v[q]) * u[q];
+        for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]) * u[q];
       } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = acc[i][j][q];
+        for (int q = 0; q < W; ++q) v[q] = acc[i][j + (q >> 2)][q & 3];
         if (bias) {
-          float b[4];
-          load4(bias + n, have, vec, b);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] += b[q];
+          for (int q = 0; q < W; ++q) v[q] += b[q];
         }
-        if (save0) store4(save0 + row + n, have, vec, v);
+        if (save0) store_cols<W>(save0 + at, have, whole, v);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = activate<ACT>(v[q]);
+        for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]);
         if (residual) {
-          float r[4];
-          load4(residual + row + n, have, vec, r);
+          float r[W];
+          load_cols<W>(residual + at, have, whole, r);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] += r[q];
+          for (int q = 0; q < W; ++q) v[q] += r[q];
         }
       }
-      store4(c + row + n, have, vec, v);
+      store_cols<W>(c + at, have, whole, v);
     }
   }
 }
@@ -274,11 +295,11 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (
 // ---- the tiled product ------------------------------------------------------------
 
 // Where a workgroup's tile lies: operand bases at the tile's first row (or
-// column) and extents.
+// column) and extents.  All uniform, and kept in scalar registers.
 struct Place {
   const uint16_t *a[2], *b[2];
   uint16_t *c;
-  int64_t row0, klen;   // klen: reduction length (per phase)
+  int32_t row0, klen;   // klen: reduction length (per phase)
   int32_t e, n0, m0, mvalid;
   bool empty;
 };
@@ -287,36 +308,49 @@ struct Place {
 template <int BM, int NCOLS, int FORM>
 __device__ __forceinline__ Place place_tile(const ProductArgs &p) {
   Place t;
-  const int slot = blockIdx.x % p.slots;
-  const int rest = blockIdx.x / p.slots;
-  t.empty = false;
+  // Workgroup i runs on XCD i % 8.  Each XCD takes blocks of bm x bn tiles,
+  // every eighth block, so that the tiles that share operand rows at the same
+  // time share an L2.
+  const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+  const int size = p.bm * p.bn;
+  int block = at / size * 8 + xcd;
+  const int in = at % size;
+  const int down = (p.slots + p.bm - 1) / p.bm, across = (p.ntiles + p.bn - 1) / p.bn;
+  t.e = 0;
+  if (FORM == kGradW) {
+    t.e = block / (down * across);
+    block -= t.e * (down * across);
+  }
+  const int slot = block / across * p.bm + in % p.bm;
+  const int nt = block % across * p.bn + in / p.bm;
   t.row0 = 0;
   t.m0 = 0;
+  t.n0 = nt * NCOLS;
+  t.empty = slot >= p.slots || nt >= p.ntiles || t.e >= p.groups;
+  if (t.empty) return t;
   if (FORM == kGradW) {
-    t.n0 = rest % p.ntiles * NCOLS;
-    t.e = rest / p.ntiles;
     const int mt = p.slots / p.halves;
     const int half = slot / mt;
     t.m0 = (slot - half * mt) * BM;
-    const int64_t first = uniform64(offset_at(p, t.e)), last = uniform64(offset_at(p, t.e + 1));
+    const int32_t first = uniform(offset_at(p, t.e)), last = uniform(offset_at(p, t.e + 1));
     t.klen = last > first ? last - first : 0;
     t.mvalid = p.m - t.m0;
-    t.a[0] = t.a[1] = p.a[half] + first * p.lda + t.m0;
-    t.b[0] = t.b[1] = p.b[0] + first * p.ldb + t.n0;
-    t.c = p.c[half] + t.e * p.bstride + static_cast<int64_t>(t.m0) * p.ldc;
+    t.a[0] = t.a[1] = uniform(p.a[half] + first * p.lda + t.m0);
+    t.b[0] = t.b[1] = uniform(p.b[0] + first * p.ldb + t.n0);
+    t.c = p.c[half] + t.e * p.bstride + t.m0 * p.ldc;
   } else {
-    t.n0 = rest * NCOLS;
     t.e = uniform(group_of_slot<BM>(p, slot));
-    const int64_t first = uniform64(offset_at(p, t.e)), last = uniform64(offset_at(p, t.e + 1));
-    const int64_t mt = slot - (first / BM + t.e);
-    t.row0 = first + mt * BM;
-    t.empty = mt < 0 || t.row0 >= last;
-    t.mvalid = last - t.row0 < BM ? static_cast<int>(last - t.row0) : BM;
+    const int32_t first = uniform(offset_at(p, t.e)), last = uniform(offset_at(p, t.e + 1));
+    const int32_t mt = slot - (first / BM + t.e);
+    // A slot of a later group's numbering may lie past this one's rows.
+    t.empty = mt < 0 || mt >= (last - first + BM - 1) / BM;
+    t.row0 = t.empty ? 0 : first + mt * BM;
+    t.mvalid = uniform(last - t.row0 < BM ? last - t.row0 : BM);
     t.klen = p.k;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      t.a[h] = p.a[FORM == kGradX ? h : 0] + t.row0 * p.lda;
-      t.b[h] = p.b[h] + t.e * p.bstride + (FORM == kForward ? static_cast<int64_t>(t.n0) * p.ldb : t.n0);
+      t.a[h] = uniform(p.a[FORM == kGradX ? h : 0] + t.row0 * p.lda);
+      t.b[h] = uniform(p.b[h] + t.e * p.bstride + (FORM == kForward ? t.n0 * p.ldb : t.n0));
     }
     t.c = p.c[0] + t.row0 * p.ldc;
   }
@@ -324,27 +358,37 @@ __device__ __forceinline__ Place place_tile(const ProductArgs &p) {
 }
 
 // Stores a wave's part of the tile, at rows wm and output columns wn of it.
-template <int FORM, bool GATED, int FM, int FN>
+// DEALT: row regions were dealt for eight columns per lane.
+template <int FORM, bool GATED, bool DEALT, int FM, int FN>
 __device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t, const f32x4_t (&acc)[FM][FN], int wm,
                                             int wn) {
+  constexpr bool WIDE = DEALT && FORM == kForward;
+  constexpr int COLS = FN * 16 / (GATED ? 2 : 1);
   const int n = t.n0 + wn;
+  const bool whole = p.cvec && n + COLS <= p.n;
+  uint16_t *s0 = nullptr, *s1 = nullptr;
+  const uint16_t *bias = nullptr, *res = nullptr;
+  if (FORM == kForward) {
+    if (p.save[0]) s0 = p.save[0] + t.row0 * p.ldc;
+    if (p.save[1]) s1 = p.save[1] + t.row0 * p.ldc;
+    if (p.bias) bias = p.bias + static_cast<int64_t>(t.e) * p.n;
+    if (p.residual) res = p.residual + t.row0 * p.ldc;
+  }
+#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, wm, t.mvalid, n, whole);
   if (FORM != kForward) {
-    store_tile<RRB_ACT_NONE, false>(p, acc, t.c, nullptr, nullptr, nullptr, nullptr, wm, t.mvalid, n);
+    RRB_STORE(RRB_ACT_NONE)
     return;
   }
-  uint16_t *s0 = p.save[0] ? p.save[0] + t.row0 * p.ldc : nullptr;
-  uint16_t *s1 = p.save[1] ? p.save[1] + t.row0 * p.ldc : nullptr;
-  const uint16_t *bias = p.bias ? p.bias + static_cast<int64_t>(t.e) * p.n : nullptr;
-  const uint16_t *res = p.residual ? p.residual + t.row0 * p.ldc : nullptr;
   switch (p.act) {
-#define RRB_CASE(A)                                                          \
-  case A:                                                                    \
-    store_tile<A, GATED>(p, acc, t.c, s0, s1, bias, res, wm, t.mvalid, n);   \
+#define RRB_CASE(A)  \
+  case A:            \
+    RRB_STORE(A)     \
     break;
     RRB_CASE(RRB_ACT_SILU) RRB_CASE(RRB_ACT_GELU) RRB_CASE(RRB_ACT_GELU_TANH) RRB_CASE(RRB_ACT_RELU)
 #undef RRB_CASE
-    default: store_tile<RRB_ACT_NONE, GATED>(p, acc, t.c, s0, s1, bias, res, wm, t.mvalid, n);
+    default: RRB_STORE(RRB_ACT_NONE)
   }
+#undef RRB_STORE
 }
 
 template <int FM, int FN>
@@ -376,15 +420,15 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
   const int wave = uniform(tid >> 6);
   const Place t = place_tile<BM, GATED ? BN / 2 : BN, FORM>(p);
   if (t.empty) return;
-  const int64_t klen = t.klen;
-  const int64_t per = (klen + kStep - 1) / kStep;  // steps per phase
-  const int steps = static_cast<int>(FORM == kGradX ? per * p.halves : per);
+  const int klen = t.klen;
+  const int per = (klen + kStep - 1) / kStep;  // steps per phase
+  const int steps = FORM == kGradX ? per * p.halves : per;
 
   u32x4_t ra[CA], rb[CB];
   // Loads of one step's chunks into registers.
   auto fetch = [&](int step) {
     const int h = FORM == kGradX && step >= per ? 1 : 0;
-    const int64_t k0 = (step - h * per) * kStep;
+    const int64_t k0 = static_cast<int64_t>(step - h * per) * kStep;
 #pragma unroll
     for (int i = 0; i < CA; ++i) {
       const int id = i * NT + tid;
@@ -450,7 +494,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
     }
     if (s + 1 < steps) commit((s + 1) & 1);
   }
-  finish_tile<FORM, GATED>(p, t, acc, wm, GATED ? wn / 2 : wn);
+  finish_tile<FORM, GATED, false>(p, t, acc, wm, GATED ? wn / 2 : wn);
 }
 
 // ---- the tiled product, loads straight to LDS -----------------------------------
@@ -463,20 +507,27 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
 // column tile past it, lie outside the descriptor and arrive as zeros, on both
 // sides, so that nothing behind a group reaches its sums.
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const uint16_t *base, int64_t bytes) {
-  const int64_t n = bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : bytes;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(base), static_cast<short>(0),
-                                           static_cast<int>(n), 0x00020000);
+__device__ __forceinline__ u32x4_t descriptor(const uint16_t *base, int bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(uniform(base));
+  return u32x4_t{static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32), static_cast<uint32_t>(uniform(bytes)),
+                 0x00020000u};
 }
 constexpr int kOutside = 0x7fffffff;
 
-// 16 bytes per lane from `d` at voffset + soffset to LDS at `to` (the wave's
-// first byte) + 16 * lane.  The host pass of the compiler does not know the
-// 16-byte form.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t d, unsigned char *to, int voffset, int soffset) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(d, (__attribute__((address_space(3))) void *)to, 16, voffset, soffset, 0, 0);
-#endif
+// Address of a workgroup's LDS as the loads below take it.
+__device__ __forceinline__ int lds_address(const unsigned char *lds) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const unsigned char *)lds));
+}
+
+// 16 bytes per lane from `d` at voffset + soffset to LDS address `at` (the
+// wave's first byte, uniform) + 16 * lane.  As assembly, because the compiler
+// would wait for every such load in flight before it reads any LDS
+// transposed; the kernels wait themselves, by count.
+__device__ __forceinline__ void load_to_lds(u32x4_t d, int at, int voffset, int soffset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(uniform(at)), "v"(voffset), "s"(d), "s"(uniform(soffset))
+               : "memory");
 }
 
 template <int BM, int BN, int WR, int WC, int FORM, bool GATED>
@@ -484,7 +535,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
   constexpr int NT = WR * WC * 64;
   constexpr int FM = BM / WR / 16, FN = BN / WC / 16;
   constexpr int A_BYTES = BM * kStep * 2, B_BYTES = BN * kStep * 2;
-  constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT;
+  constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT, NCOLS = GATED ? BN / 2 : BN;
   constexpr bool A_COL = FORM == kGradW, B_COL = FORM != kForward;
   __shared__ __align__(16) unsigned char lds[2 * (A_BYTES + B_BYTES)];
 
@@ -492,8 +543,8 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
   const int wave = uniform(tid >> 6);
   const Place t = place_tile<BM, GATED ? BN / 2 : BN, FORM>(p);
   if (t.empty) return;
-  const int64_t klen = t.klen;
-  const int per = static_cast<int>((klen + kStep - 1) / kStep);  // steps per phase
+  const int klen = t.klen;
+  const int per = (klen + kStep - 1) / kStep;  // steps per phase
   const int steps = FORM == kGradX ? per * p.halves : per;
   const int lda2 = static_cast<int>(p.lda * 2), ldb2 = static_cast<int>(p.ldb * 2);
 
@@ -527,16 +578,17 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
   auto issue = [&](int step, int buf) {
     const int h = FORM == kGradX && step >= per ? 1 : 0;
     const int kstep = step - h * per;
-    const int64_t k0 = static_cast<int64_t>(kstep) * kStep;
-    const int64_t left = klen - k0;
-    unsigned char *ta = lds + buf * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;
+    const int k0 = kstep * kStep;
+    const int left = klen - k0;
+    const int rows = left < kStep ? left : kStep;  // of the column tiles
+    const int ta = lds_address(lds) + buf * (A_BYTES + B_BYTES) + wave * 1024, tb = ta + A_BYTES;
     if (A_COL) {
-      const auto d = descriptor(t.a[0] + k0 * p.lda, left * lda2 - static_cast<int64_t>(t.m0) * 2);
+      const auto d = descriptor(t.a[0] + k0 * p.lda, rows * lda2 - t.m0 * 2);
 #pragma unroll
       for (int i = 0; i < CA; ++i)
-        load_to_lds(d, ta + (i * NT + wave * 64) * 16, va[i], 0);
+        load_to_lds(d, ta + i * NT * 16, va[i], 0);
     } else {
-      const auto d = descriptor(t.a[h], static_cast<int64_t>(t.mvalid) * lda2);
+      const auto d = descriptor(t.a[h], t.mvalid * lda2);
 #pragma unroll
       for (int i = 0; i < CA; ++i) {
         int v = va[i];
@@ -544,16 +596,16 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
           const int id = i * NT + tid;
           if (((id & 7) ^ row_swizzle(id >> 3)) * 8 >= left) v = kOutside;
         }
-        load_to_lds(d, ta + (i * NT + wave * 64) * 16, v, kstep * 128);
+        load_to_lds(d, ta + i * NT * 16, v, kstep * 128);
       }
     }
     if (B_COL) {
-      const auto d = descriptor(t.b[h] + k0 * p.ldb, left * ldb2 - static_cast<int64_t>(t.n0) * 2);
+      const auto d = descriptor(t.b[h] + k0 * p.ldb, rows * ldb2 - t.n0 * 2);
 #pragma unroll
       for (int i = 0; i < CB; ++i)
-        load_to_lds(d, tb + (i * NT + wave * 64) * 16, vb[i], 0);
+        load_to_lds(d, tb + i * NT * 16, vb[i], 0);
     } else {
-      const int64_t bytes = static_cast<int64_t>(p.n - t.n0) * ldb2;
+      const int bytes = (p.n - t.n0 < NCOLS ? p.n - t.n0 : NCOLS) * ldb2;
       const auto d0 = descriptor(t.b[0], bytes);
       const auto d1 = descriptor(GATED ? t.b[1] : t.b[0], bytes);
 #pragma unroll
@@ -565,7 +617,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
         }
         // The wave's eight rows are all gate rows or all up rows.
         const bool up = GATED && gated_up((i * NT + wave * 64) >> 3);
-        load_to_lds(up ? d1 : d0, tb + (i * NT + wave * 64) * 16, v, kstep * 128);
+        load_to_lds(up ? d1 : d0, tb + i * NT * 16, v, kstep * 128);
       }
     }
   };
@@ -596,7 +648,230 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
   }
-  finish_tile<FORM, GATED>(p, t, acc, wm, GATED ? wn / 2 : wn);
+  finish_tile<FORM, GATED, false>(p, t, acc, wm, GATED ? wn / 2 : wn);
+}
+
+// ---- the tiled product, two wave groups by turns -----------------------------------
+//
+// 256 x 256 tiles for products that are bound by the matrix cores.  Eight waves
+// (2 x 4, 128 x 64 outputs each) in two groups of one wave per SIMD: while one
+// group issues 16 matrix instructions (a quarter of its step) the other reads
+// its next fragments and starts loads, so a SIMD's matrix core and the LDS work
+// at the same time.  A step's tiles are kept as four regions of 16 KiB, the
+// first and second halves of each wave's rows (A0, A1) and columns (B0, B1),
+// two steps deep:
+//   phase 0  read A0, B0; start A1 of step s + 1;      A0 x B0
+//   phase 1  read B1;                                  A0 x B1
+//   phase 2  read A1; start A0, B0 of step s + 2;      A1 x B1
+//   phase 3  start B1 of step s + 2;                   A1 x B0
+// Each phase is: reads and loads, barrier, products, barrier; the second group
+// runs one barrier behind.  A region is loaded again no earlier than two
+// barriers after both groups have its fragments in registers, and a wave lets
+// at most eight of its loads be in flight when it passes a phase 1 or 3, which
+// leaves the region that the next phases read complete: loads have five to
+// seven phases to arrive.  Steps past the end load through an empty descriptor
+// (zeros, no memory access), so the count holds to the last step.
+
+// Row of B (column of the output) that sits at row r of half h of a row region.
+// Sixteen rows make a fragment and a lane holds four consecutive ones of each;
+// rows are dealt so that two fragments give a lane eight consecutive columns.
+template <bool GATED>
+__device__ __forceinline__ int dealt_row(int r, int h) {
+  if (GATED) return (r >> 5) * 32 + ((r >> 2) & 3) * 8 + h * 4 + (r & 3);  // gate and up rows of the same outputs
+  return (r >> 5) * 64 + h * 32 + ((r >> 2) & 3) * 8 + ((r >> 4) & 1) * 4 + (r & 3);
+}
+
+template <int FORM, bool GATED>
+__global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
+  constexpr int REGION = 16384, BUFFER = 4 * REGION, NCOLS = GATED ? 128 : 256;
+  constexpr bool A_COL = FORM == kGradW, B_COL = FORM != kForward;
+  __shared__ __align__(16) unsigned char lds[2 * BUFFER];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uniform(tid >> 6);
+  const Place t = place_tile<256, NCOLS, FORM>(p);
+  if (t.empty) return;
+  const int klen = t.klen;
+  const int per = (klen + kStep - 1) / kStep;
+  const int steps = FORM == kGradX ? per * p.halves : per;
+  const int lda2 = static_cast<int>(p.lda * 2), ldb2 = static_cast<int>(p.ldb * 2);
+
+  // Byte offsets of this thread's two chunks in each region.
+  int va[2][2], vb[2][2];
+  const int ch = (tid & 7) ^ row_swizzle(tid >> 3);  // row regions: the chunk of the row
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int id = i * 512 + tid;
+      const int kr = id >> 4, c = (id & 15) ^ (col_swizzle(kr) << 1);
+      const int r = id >> 3;
+      if (A_COL) {
+        va[h][i] = kr * lda2 + ((c >> 3) * 128 + h * 64 + (c & 7) * 8) * 2;
+      } else {
+        const int m = (r >> 6) * 128 + h * 64 + (r & 63);
+        va[h][i] = (m < t.mvalid ? m : t.mvalid - 1) * lda2 + ch * 16;
+      }
+      if (B_COL) {
+        vb[h][i] = kr * ldb2 + ((c >> 2) * 64 + h * 32 + (c & 3) * 8) * 2;
+      } else {
+        const int n = dealt_row<GATED>(r, h);
+        vb[h][i] = (t.n0 + n < p.n ? n : p.n - 1 - t.n0) * ldb2 + ch * 16;
+      }
+    }
+  }
+  const int to = lds_address(lds) + wave * 1024;
+
+  auto start_a = [&](int step, int h) {
+    const int ph = FORM == kGradX && step >= per ? 1 : 0;
+    const int ks = step - ph * per;
+    const int k0 = ks * kStep, left = klen - k0;
+    const int rows = left < kStep ? left : kStep;
+    const int dst = to + (step & 1) * BUFFER + h * REGION;
+    const bool live = step < steps;
+    if (A_COL) {
+      const auto d = descriptor(t.a[0] + k0 * p.lda, live ? rows * lda2 - t.m0 * 2 : 0);
+      load_to_lds(d, dst, va[h][0], 0);
+      load_to_lds(d, dst + 8192, va[h][1], 0);
+    } else {
+      const auto d = descriptor(t.a[ph], live ? t.mvalid * lda2 : 0);
+      const bool out = left < kStep && ch * 8 >= left;
+      load_to_lds(d, dst, out ? kOutside : va[h][0], ks * 128);
+      load_to_lds(d, dst + 8192, out ? kOutside : va[h][1], ks * 128);
+    }
+  };
+  auto start_b = [&](int step, int h) {
+    const int ph = FORM == kGradX && step >= per ? 1 : 0;
+    const int ks = step - ph * per;
+    const int k0 = ks * kStep, left = klen - k0;
+    const int rows = left < kStep ? left : kStep;
+    const int dst = to + (step & 1) * BUFFER + (2 + h) * REGION;
+    const bool live = step < steps;
+    if (B_COL) {
+      const auto d = descriptor(t.b[ph] + k0 * p.ldb, live ? rows * ldb2 - t.n0 * 2 : 0);
+      load_to_lds(d, dst, vb[h][0], 0);
+      load_to_lds(d, dst + 8192, vb[h][1], 0);
+    } else {
+      // The wave's eight rows are all gate rows or all up rows.
+      const bool up = GATED && (wave & 2);
+      const int cols = p.n - t.n0 < NCOLS ? p.n - t.n0 : NCOLS;
+      const auto d = descriptor(up ? t.b[1] : t.b[0], live ? cols * ldb2 : 0);
+      const bool out = left < kStep && ch * 8 >= left;
+      load_to_lds(d, dst, out ? kOutside : vb[h][0], ks * 128);
+      load_to_lds(d, dst + 8192, out ? kOutside : vb[h][1], ks * 128);
+    }
+  };
+
+  // Fragment addresses within a region: by kk for rows (the swizzle moves
+  // with the chunk), by fragment for columns (it moves with the slot).
+  const int wr = wave >> 2, wc = wave & 3;
+  int fa_at[4], fb_at[2];
+  if (A_COL) {
+    const int k = (lane >> 4) * 8 + ((lane >> 2) & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fa_at[i] = k * 256 + (((wr * 4 + i) ^ col_swizzle(k)) << 5) + (lane & 3) * 8;
+  } else {
+    const int r = wr * 64 + (lane & 15);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) fa_at[kk] = r * 128 + ((kk * 4 + (lane >> 4)) ^ row_swizzle(r)) * 16;
+  }
+  if (B_COL) {
+    const int k = (lane >> 4) * 8 + ((lane >> 2) & 3);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fb_at[j] = k * 256 + (((wc * 2 + j) ^ col_swizzle(k)) << 5) + (lane & 3) * 8;
+  } else {
+    const int r = wc * 32 + (lane & 15);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) fb_at[kk] = r * 128 + ((kk * 4 + (lane >> 4)) ^ row_swizzle(r)) * 16;
+  }
+  auto rows_at = [](const unsigned char *q) { return *reinterpret_cast<const bf16x8_t *>(q); };
+  auto cols_at = [](const unsigned char *q) {
+    typedef __attribute__((address_space(3))) s16x4_t *lds_ptr;
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)q);
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q + 1024));
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  bf16x8_t fa[2][4], fb[2][2][2];
+  auto read_a = [&](const unsigned char *region) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        fa[kk][i] = A_COL ? cols_at(region + fa_at[i] + kk * 8192) : rows_at(region + fa_at[kk] + i * 2048);
+  };
+  auto read_b = [&](const unsigned char *region, int h) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        fb[h][kk][j] = B_COL ? cols_at(region + fb_at[j] + kk * 8192) : rows_at(region + fb_at[kk] + j * 2048);
+  };
+  f32x4_t acc[8][4];
+  clear_tile(acc);
+#define RRB_BARRIER()                       \
+  __builtin_amdgcn_sched_barrier(0);        \
+  asm volatile("s_barrier" ::: "memory");   \
+  __builtin_amdgcn_sched_barrier(0)
+  auto multiply = [&](int ah, int bh) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[ah * 4 + i][bh * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[bh][kk][j], fa[kk][i],
+                                                                                acc[ah * 4 + i][bh * 2 + j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+  };
+
+  if (steps > 0) {
+    start_a(0, 0);
+    start_b(0, 0);
+    start_b(0, 1);
+    start_a(0, 1);
+    start_a(1, 0);
+    start_b(1, 0);
+    start_b(1, 1);
+    asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    RRB_BARRIER();
+    if (wr) {
+      RRB_BARRIER();
+    }
+    for (int s = 0; s < steps; ++s) {
+      const unsigned char *buf = lds + (s & 1) * BUFFER;
+      read_a(buf);
+      read_b(buf + 2 * REGION, 0);
+      start_a(s + 1, 1);
+      RRB_BARRIER();
+      multiply(0, 0);
+      RRB_BARRIER();
+      read_b(buf + 3 * REGION, 1);
+      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      RRB_BARRIER();
+      multiply(0, 1);
+      RRB_BARRIER();
+      read_a(buf + REGION);
+      start_a(s + 2, 0);
+      start_b(s + 2, 0);
+      RRB_BARRIER();
+      multiply(1, 1);
+      RRB_BARRIER();
+      start_b(s + 2, 1);
+      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      RRB_BARRIER();
+      multiply(1, 0);
+      RRB_BARRIER();
+    }
+    if (!wr) {
+      RRB_BARRIER();
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+#undef RRB_BARRIER
+  finish_tile<FORM, GATED, true>(p, t, acc, wr * 128, GATED ? wc * 32 : wc * 64);
 }
 
 // ---- gradients before the activation -------------------------------------------
@@ -665,7 +940,7 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(BiasGradArgs a) {
   __shared__ float part[32][64 + 1];
   const int e = blockIdx.y, lane8 = threadIdx.x & 7, deep = threadIdx.x >> 3;
   const int c0 = blockIdx.x * 64 + lane8 * 8;
-  const int64_t s = offset_at(a.p, e), t = offset_at(a.p, e + 1);
+  const int32_t s = offset_at(a.p, e), t = offset_at(a.p, e + 1);
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int64_t r = s + deep; r < t; r += 32) {
     const u32x4_t v = load_chunk(a.dz + r * a.p.lda + c0, a.n - c0);
@@ -700,14 +975,15 @@ template <int BM, int BN, int FORM, bool GATED>
 rrb_status launch_tiles(void (*kernel)(ProductArgs), int threads, ProductArgs p, hipStream_t s) {
   constexpr int cols = GATED ? BN / 2 : BN;
   p.ntiles = (p.n + cols - 1) / cols;
-  int64_t grid;
-  if (FORM == kGradW) {
-    p.slots = (p.m + BM - 1) / BM * p.halves;
-    grid = static_cast<int64_t>(p.slots) * p.ntiles * p.groups;
-  } else {
-    p.slots = static_cast<int32_t>(p.rows / BM) + p.groups;
-    grid = static_cast<int64_t>(p.slots) * p.ntiles;
-  }
+  const int64_t each = FORM == kGradW ? p.groups : 1;
+  p.slots = FORM == kGradW ? (p.m + BM - 1) / BM * p.halves : static_cast<int32_t>(p.rows / BM) + p.groups;
+  // Blocks of 4 x 8 tiles (one per CU of an XCD) where there are enough of
+  // them to go round, single tiles otherwise.
+  const bool many = static_cast<int64_t>(p.slots) * p.ntiles * each >= 1024;
+  p.bm = many ? 4 : 1;
+  p.bn = many ? 8 : 1;
+  const int64_t blocks = static_cast<int64_t>((p.slots + p.bm - 1) / p.bm) * ((p.ntiles + p.bn - 1) / p.bn) * each;
+  const int64_t grid = (blocks + 7) / 8 * 8 * p.bm * p.bn;
   if (grid > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, p);
   return launched("expert product");
@@ -718,7 +994,7 @@ rrb_status launch_product(const ProductArgs &p, hipStream_t s) {
   bool direct = p.lda % 8 == 0 && p.ldb % 8 == 0;
   for (int h = 0; h < 2; ++h) direct = direct && aligned(p.a[h], 16) && aligned(p.b[h], 16);
   if (!direct) return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
-  return launch_tiles<256, 256, FORM, GATED>(product_direct_kernel<256, 256, 2, 4, FORM, GATED>, 512, p, s);
+  return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED>, 512, p, s);
 }
 
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
@@ -732,7 +1008,7 @@ rrb_status check_spec(const rrb_expert_spec *s, const int32_t *offsets) {
   if (s->activation < RRB_ACT_NONE || s->activation > RRB_ACT_RELU)
     return fail(RRB_EINVAL, "unknown activation %d", s->activation);
   if (!offsets && s->groups != 1) return fail(RRB_EINVAL, "NULL offsets with %d groups", s->groups);
-  if (s->rows > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "rows %lld >= 2^31", (long long)s->rows);
+  if (s->rows >= 1LL << 30) return fail(RRB_EUNSUPPORTED, "rows %lld >= 2^30", (long long)s->rows);
   if (s->in > kMaxWidth || s->out > kMaxWidth)
     return fail(RRB_EUNSUPPORTED, "in %lld, out %lld: at most 2^20", (long long)s->in, (long long)s->out);
   if (s->groups > kMaxGroups) return fail(RRB_EUNSUPPORTED, "groups %d: at most %d", s->groups, kMaxGroups);
@@ -743,7 +1019,7 @@ ProductArgs base_args(const rrb_expert_spec &s, const int32_t *offsets) {
   ProductArgs p;
   std::memset(&p, 0, sizeof p);
   p.offsets = offsets;
-  p.rows = s.rows;
+  p.rows = static_cast<int32_t>(s.rows);
   p.groups = s.groups;
   p.halves = 1;
   p.bstride = s.in * s.out;
