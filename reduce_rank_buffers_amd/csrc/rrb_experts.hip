@@ -43,11 +43,26 @@ __device__ __forceinline__ float gelu_2u(float x) {
   return 1.5957691216057308f * (x + 0.044715f * x * x * x);
 }
 
+// Phi(x) = erfc(-x / sqrt 2) / 2 by Abramowitz and Stegun's formula 7.1.26,
+// erfc(z) = (a1 t + .. + a5 t^5) e^(-z^2), t = 1 / (1 + p z), z >= 0: within
+// 1.5e-7 of erfc, and in the tail, which it scales by e^(-z^2), within 2^-10 of
+// it relatively up to z = 3.  About 15 instructions where the library's erfc
+// takes some 100 (it was an eighth of a 4096-deep product's time).
+__device__ __forceinline__ float normal_cdf(float x) {
+  const float z = 0.70710678118654752f * fabsf(x);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, z, 1.f));
+  float q = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+  q = __builtin_fmaf(q, t, 1.421413741f);
+  q = __builtin_fmaf(q, t, -0.284496736f);
+  q = __builtin_fmaf(q, t, 0.254829592f);
+  const float half = 0.5f * q * t * __expf(-z * z);
+  return x < 0.f ? half : 1.f - half;
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float x) {
   if (ACT == RRB_ACT_SILU) return x * sigmoid(x);
-  // erfc(-x / sqrt 2) keeps its relative precision where 1 + erf would cancel.
-  if (ACT == RRB_ACT_GELU) return 0.5f * x * erfcf(-0.70710678118654752f * x);
+  if (ACT == RRB_ACT_GELU) return x * normal_cdf(x);
   if (ACT == RRB_ACT_GELU_TANH) return x * sigmoid(gelu_2u(x));
   if (ACT == RRB_ACT_RELU) return x < 0.f ? 0.f : x;
   return x;
@@ -61,7 +76,7 @@ __device__ __forceinline__ void activate_grad(float x, float &f, float &df) {
     f = x * s;
     df = s * (1.f + x * (1.f - s));
   } else if (ACT == RRB_ACT_GELU) {
-    const float c = 0.5f * erfcf(-0.70710678118654752f * x);
+    const float c = normal_cdf(x);
     f = x * c;
     df = c + x * (0.3989422804014327f * __expf(-0.5f * x * x));
   } else if (ACT == RRB_ACT_GELU_TANH) {
@@ -656,20 +671,21 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 // 256 x 256 tiles for products that are bound by the matrix cores.  Eight waves
 // (2 x 4, 128 x 64 outputs each) in two groups of one wave per SIMD: while one
 // group issues 16 matrix instructions (a quarter of its step) the other reads
-// its next fragments and starts loads, so a SIMD's matrix core and the LDS work
-// at the same time.  A step's tiles are kept as four regions of 16 KiB, the
-// first and second halves of each wave's rows (A0, A1) and columns (B0, B1),
-// two steps deep:
-//   phase 0  read A0, B0; start A1 of step s + 1;      A0 x B0
-//   phase 1  read B1;                                  A0 x B1
-//   phase 2  read A1; start A0, B0 of step s + 2;      A1 x B1
-//   phase 3  start B1 of step s + 2;                   A1 x B0
-// Each phase is: reads and loads, barrier, products, barrier; the second group
-// runs one barrier behind.  A region is loaded again no earlier than two
-// barriers after both groups have its fragments in registers, and a wave lets
-// at most eight of its loads be in flight when it passes a phase 1 or 3, which
-// leaves the region that the next phases read complete: loads have five to
-// seven phases to arrive.  Steps past the end load through an empty descriptor
+// fragments and starts loads, so a SIMD's matrix core and the LDS work at the
+// same time.  A step's tiles are kept as four regions of 16 KiB, the first and
+// second halves of each wave's rows (A0, A1) and columns (B0, B1), two steps
+// deep.  In phase p a group reads and starts
+//   0  reads B0, half of A1;            starts A1 of step s + 1;    A0 x B0
+//   1  reads the rest of A1;                                        A0 x B1
+//   2  reads half of A0 of s + 1;       starts A0, B0 of s + 2;     A1 x B1
+//   3  reads the rest of it, B1 of s + 1; starts B1 of s + 2;       A1 x B0
+// then a barrier, the products, a barrier; the second group runs one barrier
+// behind.  Only B0 is read in the phase that uses it.  A region is loaded again
+// no earlier than a whole phase after both groups have used its fragments: A0
+// and B0 by products 0, B1 by products 1, A1 by products 2.  A wave lets at most
+// six of its loads be in flight when it passes phase 1, 2 or 3, which leaves
+// what the next phase reads (A0; B1; A1 and B0) complete in every wave before
+// the barrier between.  Steps past the end load through an empty descriptor
 // (zeros, no memory access), so the count holds to the last step.
 
 // Row of B (column of the output) that sits at row r of half h of a row region.
@@ -791,15 +807,15 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
     const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q + 1024));
     return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  bf16x8_t fa[2][4], fb[2][2][2];
-  auto read_a = [&](const unsigned char *region) {
+  bf16x8_t fa[2][2][4], fb[2][2][2];  // [half][kk][block]
+  auto read_a = [&](const unsigned char *buf, int h, int kk) {
+    const unsigned char *region = buf + h * REGION;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        fa[kk][i] = A_COL ? cols_at(region + fa_at[i] + kk * 8192) : rows_at(region + fa_at[kk] + i * 2048);
+    for (int i = 0; i < 4; ++i)
+      fa[h][kk][i] = A_COL ? cols_at(region + fa_at[i] + kk * 8192) : rows_at(region + fa_at[kk] + i * 2048);
   };
-  auto read_b = [&](const unsigned char *region, int h) {
+  auto read_b = [&](const unsigned char *buf, int h) {
+    const unsigned char *region = buf + (2 + h) * REGION;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -813,8 +829,6 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
   asm volatile("s_barrier" ::: "memory");   \
   __builtin_amdgcn_sched_barrier(0)
   auto multiply = [&](int ah, int bh) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
@@ -822,8 +836,8 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          acc[ah * 4 + i][bh * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[bh][kk][j], fa[kk][i],
-                                                                                acc[ah * 4 + i][bh * 2 + j], 0, 0, 0);
+          acc[ah * 4 + i][bh * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              fb[bh][kk][j], fa[ah][kk][i], acc[ah * 4 + i][bh * 2 + j], 0, 0, 0);
     __builtin_amdgcn_s_setprio(0);
   };
 
@@ -835,32 +849,38 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
     start_a(1, 0);
     start_b(1, 0);
     start_b(1, 1);
-    asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
     RRB_BARRIER();
+    read_a(lds, 0, 0);
+    read_a(lds, 0, 1);
+    read_b(lds, 1);
     if (wr) {
       RRB_BARRIER();
     }
     for (int s = 0; s < steps; ++s) {
-      const unsigned char *buf = lds + (s & 1) * BUFFER;
-      read_a(buf);
-      read_b(buf + 2 * REGION, 0);
+      const unsigned char *buf = lds + (s & 1) * BUFFER, *next = lds + (~s & 1) * BUFFER;
+      read_b(buf, 0);
+      read_a(buf, 1, 0);
       start_a(s + 1, 1);
       RRB_BARRIER();
       multiply(0, 0);
       RRB_BARRIER();
-      read_b(buf + 3 * REGION, 1);
-      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      read_a(buf, 1, 1);
+      asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
       RRB_BARRIER();
       multiply(0, 1);
       RRB_BARRIER();
-      read_a(buf + REGION);
+      read_a(next, 0, 0);
       start_a(s + 2, 0);
       start_b(s + 2, 0);
+      asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
       RRB_BARRIER();
       multiply(1, 1);
       RRB_BARRIER();
+      read_a(next, 0, 1);
+      read_b(next, 1);
       start_b(s + 2, 1);
-      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
       RRB_BARRIER();
       multiply(1, 0);
       RRB_BARRIER();
