@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstring>
+#include <cstdlib>
 
 #include "rrb_internal.h"
 #include "rrb_kernels.h"
@@ -1014,6 +1015,7 @@ rrb_status launch_product(const ProductArgs &p, hipStream_t s) {
   bool direct = p.lda % 8 == 0 && p.ldb % 8 == 0;
   for (int h = 0; h < 2; ++h) direct = direct && aligned(p.a[h], 16) && aligned(p.b[h], 16);
   if (!direct) return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
+  if (getenv("RRB_T128")) return launch_tiles<128, 128, FORM, GATED>(product_direct_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
   return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED>, 512, p, s);
 }
 

@@ -2,11 +2,12 @@
 // experts and their softmax weights, as rrb_moe_route takes them, and the
 // gradient of the scores.
 //
-// One wave per token.  The experts are chosen on the scores themselves (the
-// softmax keeps their order, and rounding a probability could only merge
-// two), as a 64-bit key (score as an ordered integer, then the lower expert
-// first), so the choice is exact and ties are decided.  Weights are fp32:
-// w_i = e^(l_i - m) / sum, over all experts, or over the chosen ones.
+// L lanes of a wave share a token, each with V of its scores.  The experts are
+// chosen on the scores themselves (the softmax keeps their order, and rounding
+// a probability could only merge two): k rounds of a maximum over integers
+// that order as the scores do, ties to the lower expert, so the choice is
+// exact.  Weights are fp32: w_i = e^(l_i - m) / sum, over all experts, or over
+// the chosen ones.
 #include <hip/hip_runtime.h>
 
 #include "rrb_internal.h"
@@ -25,8 +26,15 @@ struct GateArgs {
   int32_t experts, topk, renorm;
 };
 
-__device__ __forceinline__ float load_score(const float *p) { return *p; }
-__device__ __forceinline__ float load_score(const uint16_t *p) { return bf16_to_f32(*p); }
+// Tokens up to which a wave takes one token.
+constexpr int64_t kFewTokens = 4096;
+
+// Scores that one 16-byte load brings.
+template <typename T>
+constexpr int kPerLoad = 16 / sizeof(T);
+
+__device__ __forceinline__ float score(float v) { return v; }
+__device__ __forceinline__ float score(uint16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void store_score(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_score(uint16_t *p, float v) { *p = f32_to_bf16_rne(v); }
 
@@ -38,6 +46,9 @@ __device__ __forceinline__ uint32_t score_key(float f) {
   const uint32_t u = __float_as_uint(f == 0.f ? 0.f : f);
   return u >> 31 ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);  // NaN keeps being one
+}
 
 // e^(l - m), where an expert masked out by -inf has no share (also where all
 // are) and scores of +inf share equally.
@@ -46,65 +57,129 @@ __device__ __forceinline__ float share(float l, float m) {
   return l == m ? 1.f : expf(l - m);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+// All-reduce over the L = 16 or 64 lanes of a token: within 16 lanes by DPP
+// (two quad permutations, two row rotations), across rows by shuffles.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, false);
+}
+template <int L, typename F>
+__device__ __forceinline__ int across(int v, F f) {
+  v = f(v, dpp<0xb1>(v));   // quad_perm [1,0,3,2]
+  v = f(v, dpp<0x4e>(v));   // quad_perm [2,3,0,1]
+  v = f(v, dpp<0x124>(v));  // row_ror:4
+  v = f(v, dpp<0x128>(v));  // row_ror:8
+  if (L == 64) {
+    v = f(v, __shfl_xor(v, 16, 64));
+    v = f(v, __shfl_xor(v, 32, 64));
+  }
   return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
+template <int L>
+__device__ __forceinline__ uint32_t most(uint32_t v) {
+  return across<L>(static_cast<int>(v), [](int a, int b) {
+    return static_cast<int>(max(static_cast<uint32_t>(a), static_cast<uint32_t>(b)));
+  });
+}
+template <int L>
+__device__ __forceinline__ uint32_t least(uint32_t v) {
+  return ~most<L>(~v);
+}
+template <int L>
+__device__ __forceinline__ float sum_of(float v) {
+  return __int_as_float(across<L>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
+}
+template <int L>
+__device__ __forceinline__ float max_of(float v) {
+  return __int_as_float(across<L>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+  }));
 }
 
-// V = scores per lane: expert e sits in lane e % 64.
-template <typename T, int V>
+// The expert of score i of lane `lane`: W consecutive ones per load.
+template <int L, int W>
+__device__ __forceinline__ int expert_of(int i, int lane) {
+  return (i / W * L + lane) * W + i % W;
+}
+
+// A lane's V scores of a row; -inf past its end.  W = 1, or a whole load's.
+template <typename T, int L, int V, int W>
+__device__ __forceinline__ void load_scores(const T *row, int experts, int lane, float (&l)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += W) {
+    const int e = expert_of<L, W>(i, lane);
+    if (W > 1) {
+      T part[W];
+      if (e < experts) __builtin_memcpy(part, __builtin_assume_aligned(row + e, 16), sizeof part);
+#pragma unroll
+      for (int q = 0; q < W; ++q) l[i + q] = e < experts ? score(part[q]) : -INFINITY;
+    } else {
+      l[i] = e < experts ? score(row[e]) : -INFINITY;
+    }
+  }
+}
+
+template <typename T, int L, int V, int W>
 __global__ void __launch_bounds__(256) gate_kernel(GateArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = blockIdx.x * 4ll + (threadIdx.x >> 6);
-  if (t >= a.tokens) return;
-  const T *row = static_cast<const T *>(a.logits) + t * a.experts;
+  constexpr bool kShort = sizeof(T) == 2;
+  const int lane = threadIdx.x & (L - 1);
+  const int64_t t = blockIdx.x * (256ll / L) + threadIdx.x / L;
+  if (t >= a.tokens) return;  // whole tokens leave: the others' lanes are all there
   float l[V];
-  uint64_t key[V];
+  load_scores<T, L, V, W>(static_cast<const T *>(a.logits) + t * a.experts, a.experts, lane, l);
+  // bf16 scores: the key's upper half and the expert in one word, so a round
+  // is one maximum.  fp32: a maximum, then the lowest expert that has it.
+  uint32_t key[V];
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = i * 64 + lane;
-    l[i] = e < a.experts ? load_score(row + e) : -INFINITY;
-    key[i] = e < a.experts ? static_cast<uint64_t>(score_key(l[i])) << 32 | (0xffffffffu - e) : 0;
+    const int e = expert_of<L, W>(i, lane);
+    const uint32_t k = score_key(l[i]);
+    key[i] = e >= a.experts ? 0 : kShort ? (k & 0xffff0000u) | (0xffffu - e) : k;
     m = fmaxf(m, l[i]);
   }
-  m = wave_max(m);
+  m = max_of<L>(m);
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) sum += share(l[i], m);
-  sum = wave_sum(sum);
   float mine = 0.f;
   int chosen = 0;
   for (int j = 0; j < a.topk; ++j) {
-    uint64_t best = 0;
+    uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) best = key[i] > best ? key[i] : best;
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    best = most<L>(best);
+    int e;
+    float le;
+    if (kShort) {
+      e = static_cast<int>(0xffffu - (best & 0xffffu));
+      le = key_score(best | 0xffffu);
+      // the key of a negative score is complemented: its lower half is ones
+      if (best >> 31) le = key_score(best & 0xffff0000u);
+      if (best >= 0xff810000u) le = NAN;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      const uint64_t o = __shfl_xor(best, d, 64);
-      best = o > best ? o : best;
-    }
-    const int e = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
-    float le = -INFINITY;
+      for (int i = 0; i < V; ++i) key[i] = key[i] == best ? 0 : key[i];
+    } else {
+      uint32_t low = 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] == best) {
-        key[i] = 0;
-        le = l[i];
+      for (int i = 0; i < V; ++i) {
+        const uint32_t x = expert_of<L, W>(i, lane);
+        low = key[i] == best ? min(low, x) : low;
       }
-    le = __shfl(le, e & 63, 64);
+      low = least<L>(low);
+      e = static_cast<int>(low);
+      le = key_score(best);
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = expert_of<L, W>(i, lane) == e ? 0 : key[i];
+    }
     if (lane == j) {
       chosen = e;
       mine = share(le, m);
     }
   }
-  if (a.renorm) sum = wave_sum(mine);
+  sum = sum_of<L>(a.renorm ? mine : sum);
   if (lane < a.topk) {
     a.idx[t * a.topk + lane] = chosen;
     a.w[t * a.topk + lane] = sum == 0.f ? 0.f : mine / sum;
@@ -112,70 +187,81 @@ __global__ void __launch_bounds__(256) gate_kernel(GateArgs a) {
 }
 
 // With p the softmax over all experts and c the chosen ones' sum of p_i dw_i:
-//   dl_j = p_j (dw_j - c) for a chosen expert, -p_j c for the others;
+//   dl_j = [j chosen] p_j dw_j - p_j c;
 // renormalised, with w over the chosen ones alone, dl_i = w_i (dw_i - sum w dw)
-// for these and 0 for the others.  A masked expert takes no part: its dw is
-// not used.  Indices outside the experts are passed over.
-template <typename T, int V>
+// for these and 0 for the others.  Lane j takes the j-th chosen expert: the
+// chosen ones' terms meet the row through LDS.  A masked expert takes no part:
+// its dw is not used.  Indices outside the experts are passed over.
+template <typename T, int L, int V, int W>
 __global__ void __launch_bounds__(256) gate_backward_kernel(GateArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = blockIdx.x * 4ll + (threadIdx.x >> 6);
+  __shared__ float term[256 * V];  // [token][expert]
+  const int lane = threadIdx.x & (L - 1), local = threadIdx.x / L;
+  const int64_t t = blockIdx.x * (256ll / L) + local;
   if (t >= a.tokens) return;
   const T *row = static_cast<const T *>(a.logits) + t * a.experts;
   T *out = static_cast<T *>(a.dlogits) + t * a.experts;
-  const int32_t mine = lane < a.topk ? a.idx[t * a.topk + lane] : -1;
-  const float dwj = lane < a.topk ? a.dw[t * a.topk + lane] : 0.f;
-  float l[V], dw[V];
-  bool on[V];
+  float *mine = term + local * (L * V);
+  int32_t e = lane < a.topk ? a.idx[t * a.topk + lane] : -1;
+  float dw = lane < a.topk ? a.dw[t * a.topk + lane] : 0.f;
+  if (e >= a.experts) e = -1;
+  const float le = e >= 0 ? score(row[e]) : -INFINITY;
+  if (le == -INFINITY) dw = 0.f;
+  float l[V];
+  load_scores<T, L, V, W>(row, a.experts, lane, l);
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = i * 64 + lane;
-    l[i] = e < a.experts ? load_score(row + e) : -INFINITY;
     m = fmaxf(m, l[i]);
-    dw[i] = 0.f;
-    on[i] = false;
+    mine[expert_of<L, W>(i, lane)] = 0.f;
   }
-  for (int j = 0; j < a.topk; ++j) {
-    const int e = __shfl(mine, j, 64);
-    const float d = __shfl(dwj, j, 64);
+  m = max_of<L>(m);
+  float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e == i * 64 + lane && l[i] != -INFINITY) {
-        on[i] = true;
-        dw[i] = d;
-      }
-  }
-  m = wave_max(m);
-  float sum = 0.f, dot = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    l[i] = share(l[i], m);
-    if (!a.renorm || on[i]) sum += l[i];
-    if (on[i]) dot += l[i] * dw[i];
-  }
-  sum = wave_sum(sum);
-  dot = wave_sum(dot);
+  for (int i = 0; i < V; ++i) sum += l[i] = share(l[i], m);
+  const float se = share(le, m);
+  sum = sum_of<L>(a.renorm ? se : sum);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const float mean = sum == 0.f ? 0.f : dot / sum;
+  const float pe = se * inv;
+  const float c = sum_of<L>(pe * dw);
+  // A token's lanes are of one wave, whose LDS accesses keep their order; the
+  // fence keeps the compiler's.
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (se != 0.f) mine[e] = a.renorm ? pe * (dw - c) : pe * dw;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = i * 64 + lane;
-    if (e >= a.experts) continue;
-    float d = on[i] ? dw[i] - mean : a.renorm ? 0.f : -mean;
-    d = l[i] == 0.f ? 0.f : l[i] * inv * d;
-    store_score(out + e, d);
+  for (int i = 0; i < V; i += W) {
+    const int x = expert_of<L, W>(i, lane);
+    if (x >= a.experts) continue;
+    T part[W];
+#pragma unroll
+    for (int q = 0; q < W; ++q) {
+      float d = mine[x + q];
+      if (!a.renorm) d = l[i + q] == 0.f ? d : d - l[i + q] * inv * c;
+      store_score(part + q, d);
+    }
+    if (W > 1)
+      __builtin_memcpy(__builtin_assume_aligned(out + x, 16), part, sizeof part);
+    else
+      out[x] = part[0];
   }
 }
 
 using GateFn = void (*)(GateArgs);
 
-template <typename T>
-GateFn gate_for(int experts, bool back) {
-  const int v = (experts + 63) / 64;
-#define RRB_PICK(n) \
-  if (v <= n) return back ? gate_backward_kernel<T, n> : gate_kernel<T, n>;
-  RRB_PICK(1) RRB_PICK(2) RRB_PICK(4) RRB_PICK(8) RRB_PICK(16)
+// Sixteen lanes per token where that leaves at most 16 scores a lane, the
+// whole wave otherwise, and where tokens are few: a lane's rounds are then a
+// quarter as long.
+template <typename T, int W>
+GateFn gate_pick(const GateArgs &a, bool back, int *lanes) {
+#define RRB_PICK(LANES, n)                                                       \
+  if (a.experts <= LANES * (n)) {                                                \
+    *lanes = LANES;                                                              \
+    return back ? gate_backward_kernel<T, LANES, n, W> : gate_kernel<T, LANES, n, W>; \
+  }
+  if (a.tokens > kFewTokens) {
+    RRB_PICK(16, 4 < W ? W : 4) RRB_PICK(16, 8) RRB_PICK(16, 16)
+  }
+  RRB_PICK(64, 4 < W ? W : 4) RRB_PICK(64, 8) RRB_PICK(64, 16)
 #undef RRB_PICK
   return nullptr;
 }
@@ -189,11 +275,19 @@ rrb_status gate(const GateArgs &a, int32_t dtype, uint32_t flags, bool back, rrb
   if (a.experts > kRouteMaxExperts || a.topk > kRouteMaxTopk)
     return fail(RRB_EUNSUPPORTED, "experts %d, topk %d: at most %d and %d", a.experts, a.topk, kRouteMaxExperts,
                 kRouteMaxTopk);
-  const int64_t blocks = (a.tokens + 3) / 4;
-  if (blocks > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tokens for one launch");
+  if (a.tokens > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tokens for one launch");
   if (a.tokens == 0) return RRB_OK;
   if (!a.logits || !a.idx || (back ? !a.dw || !a.dlogits : !a.w)) return fail(RRB_EINVAL, "NULL array");
-  const GateFn fn = dtype == RRB_F32 ? gate_for<float>(a.experts, back) : gate_for<uint16_t>(a.experts, back);
+  // Whole 16-byte loads where every row starts on such a boundary.
+  const int per = dtype == RRB_F32 ? kPerLoad<float> : kPerLoad<uint16_t>;
+  const bool wide = a.experts % per == 0 &&
+                    ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) & 15) == 0;
+  int lanes = 64;
+  const GateFn fn = dtype == RRB_F32 ? (wide ? gate_pick<float, kPerLoad<float>>(a, back, &lanes)
+                                             : gate_pick<float, 1>(a, back, &lanes))
+                                     : (wide ? gate_pick<uint16_t, kPerLoad<uint16_t>>(a, back, &lanes)
+                                             : gate_pick<uint16_t, 1>(a, back, &lanes));
+  const int64_t blocks = (a.tokens + 256 / lanes - 1) / (256 / lanes);
   hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? RRB_OK : fail(RRB_EHIP, "gate launch: %s", hipGetErrorString(e));

@@ -309,26 +309,104 @@ struct BackArgs {
   const unsigned char *z[RRB_MAX_RANKS];
   unsigned char *dz[RRB_MAX_RANKS];
   float *dw;  // [T][k] in routing order, or NULL: z is not read
+  bool has_dz;
   RowArgs r;  // maps, weights, sizes
 };
 
-// Sum over the workgroup's `waves` waves of one value per thread; thread 0
-// holds it.
-__device__ __forceinline__ float block_sum(float v, float *part) {
+constexpr int kBackBlock = 256;
+
+// Sums of K values per thread over the workgroup, to dw in routing order (the
+// threads below K hold one each at the end).
+template <int K>
+__device__ __forceinline__ void store_dots(float (&dot)[K], float *dw, const int32_t *col) {
+  __shared__ float part[kBackBlock / 64][K];
 #pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+  for (int j = 0; j < K; ++j) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) dot[j] += __shfl_xor(dot[j], d, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) part[threadIdx.x >> 6][j] = dot[j];
+  }
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float total = 0.f;
-  for (unsigned q = 0; q < blockDim.x / 64; ++q) total += part[q];
-  return total;
+  if (threadIdx.x < K) {
+    float total = 0.f;
+#pragma unroll
+    for (int q = 0; q < kBackBlock / 64; ++q) total += part[q][threadIdx.x];
+    dw[col[threadIdx.x]] = total;
+  }
 }
 
-// One workgroup per token, its k rows in turn.  Any top-k, width and
-// alignment.
-__global__ void __launch_bounds__(256) moe_combine_backward_kernel(BackArgs b) {
-  __shared__ float part[4];
+// One workgroup per token: dy is read once, the K rows of z beside it, each
+// 16-byte vector of the K products written as it is made (non-temporal, like
+// the dispatch's).  HBM-bound.
+template <int K>
+__global__ void __launch_bounds__(kBackBlock) moe_combine_backward_kernel(BackArgs b) {
+  const RowArgs &a = b.r;
+  const uint32_t t = blockIdx.x;
+  const int64_t tk = static_cast<int64_t>(t) * K;
+  const int32_t status = route_status_word(a);
+  int32_t s[K];
+  float w[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    s[j] = a.slot[tk + j];
+    w[j] = a.weight[tk + j];
+  }
+  if (status != 0) return;
+  if (a.wover) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j] = a.wover[tk + a.col[tk + j]];
+  }
+  const uint32_t tpr = static_cast<uint32_t>(a.tokens_per_rank), rank = t / tpr;
+  const unsigned char *dy = b.dy[rank] + static_cast<int64_t>(t - rank * tpr) * a.row_bytes;
+  const uint32_t nv = static_cast<uint32_t>(a.nvec);
+  float dot[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) dot[j] = 0.f;
+  for (uint32_t i = threadIdx.x; i < nv; i += kBackBlock) {
+    const v4u d = *reinterpret_cast<const v4u *>(dy + i * 16);
+    v4u z[K];
+    if (b.dw) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        z[j] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(
+            b.z[s[j] >> kSlotRankShift] + static_cast<int64_t>(s[j] & kSlotRowMask) * a.row_bytes + i * 16));
+    }
+    float f[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[2 * q] = bf16_lo(d[q]);
+      f[2 * q + 1] = bf16_hi(d[q]);
+    }
+    if (b.has_dz) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        float g[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) g[q] = w[j] * f[q];
+        const uint4 o = pack_bf16x8(g);
+        __builtin_nontemporal_store(v4u{o.x, o.y, o.z, o.w}, reinterpret_cast<v4u *>(
+            b.dz[s[j] >> kSlotRankShift] + static_cast<int64_t>(s[j] & kSlotRowMask) * a.row_bytes + i * 16));
+      }
+    }
+    if (b.dw) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          dot[j] = __builtin_fmaf(f[2 * q], bf16_lo(z[j][q]), dot[j]);
+          dot[j] = __builtin_fmaf(f[2 * q + 1], bf16_hi(z[j][q]), dot[j]);
+        }
+      }
+    }
+  }
+  if (b.dw) store_dots<K>(dot, b.dw + tk, a.col + tk);
+}
+
+// Any top-k, width and alignment: one workgroup per token, its k rows in turn.
+__global__ void __launch_bounds__(kBackBlock) moe_combine_backward_any_kernel(BackArgs b) {
   const RowArgs &a = b.r;
   if (route_failed(a)) return;
   const int64_t t = blockIdx.x;
@@ -336,20 +414,20 @@ __global__ void __launch_bounds__(256) moe_combine_backward_kernel(BackArgs b) {
   const uint16_t *dy = reinterpret_cast<const uint16_t *>(b.dy[rank] + (t - rank * a.tokens_per_rank) * a.row_bytes);
   for (int j = 0; j < a.k; ++j) {
     const int32_t s = a.slot[t * a.k + j];
-    const int32_t c = a.col[t * a.k + j];
-    const float w = a.wover ? a.wover[t * a.k + c] : a.weight[t * a.k + j];
+    const int32_t *c = a.col + t * a.k + j;
+    const float w = a.wover ? a.wover[t * a.k + *c] : a.weight[t * a.k + j];
     const int64_t at = static_cast<int64_t>(s & kSlotRowMask) * a.row_bytes;
     const uint16_t *z = reinterpret_cast<const uint16_t *>(b.z[s >> kSlotRankShift] + at);
-    uint16_t *dz = b.dz[s >> kSlotRankShift] ? reinterpret_cast<uint16_t *>(b.dz[s >> kSlotRankShift] + at) : nullptr;
-    float dot = 0.f;
-    for (int64_t i = threadIdx.x; i < a.hidden; i += 256) {
+    uint16_t *dz = reinterpret_cast<uint16_t *>(b.dz[s >> kSlotRankShift] + at);
+    float dot[1] = {0.f};
+    for (int64_t i = threadIdx.x; i < a.hidden; i += kBackBlock) {
       const float d = bf16_to_f32(dy[i]);
-      if (b.dw) dot = __builtin_fmaf(d, bf16_to_f32(z[i]), dot);
-      if (dz) dz[i] = f32_to_bf16_rne(w * d);
+      if (b.dw) dot[0] = __builtin_fmaf(d, bf16_to_f32(z[i]), dot[0]);
+      if (b.has_dz) dz[i] = f32_to_bf16_rne(w * d);
     }
     if (b.dw) {
-      dot = block_sum(dot, part);
-      if (threadIdx.x == 0) b.dw[t * a.k + c] = dot;
+      store_dots<1>(dot, b.dw + t * a.k, c);
+      __syncthreads();  // its LDS is written again for the next row
     }
   }
 }
@@ -989,6 +1067,22 @@ RowFn combine_for(int k, int *cu) {
   }
 }
 
+using BackFn = void (*)(BackArgs);
+
+// Combine gradient for top-k up to 16 (nullptr above: the any-k kernel).
+BackFn combine_backward_for(int k) {
+  switch (k) {
+#define RRB_CASE(n) \
+  case n:           \
+    return moe_combine_backward_kernel<n>;
+    RRB_CASE(1) RRB_CASE(2) RRB_CASE(3) RRB_CASE(4) RRB_CASE(5) RRB_CASE(6) RRB_CASE(7)
+    RRB_CASE(8) RRB_CASE(9) RRB_CASE(10) RRB_CASE(11) RRB_CASE(12) RRB_CASE(13)
+    RRB_CASE(14) RRB_CASE(15) RRB_CASE(16)
+#undef RRB_CASE
+    default: return nullptr;
+  }
+}
+
 // Row parts: the fewest parts of at most `cap` vectors, all of equal size
 // (the last may be shorter).
 void split_row(RowArgs &a, int64_t cap) {
@@ -1084,8 +1178,16 @@ rrb_status launch_combine_backward(const Plan &p, const void *const *dy, const v
   a.row_bytes = m.hidden * 2;
   a.hidden = m.hidden;
   a.k = m.topk;
+  a.nvec = a.row_bytes / 16;
   b.dw = d_dweights;
-  hipLaunchKernelGGL(moe_combine_backward_kernel, dim3(static_cast<unsigned>(m.tokens)), dim3(256), 0,
+  b.has_dz = dz != nullptr;
+  uintptr_t bits = static_cast<uintptr_t>(a.row_bytes);
+  for (int32_t r = 0; r < p.nranks; ++r)
+    bits |= reinterpret_cast<uintptr_t>(b.dy[r]) | reinterpret_cast<uintptr_t>(b.z[r]) |
+            reinterpret_cast<uintptr_t>(b.dz[r]);
+  BackFn kern = (bits & 15) == 0 ? combine_backward_for(m.topk) : nullptr;
+  if (!kern) kern = moe_combine_backward_any_kernel;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(m.tokens)), dim3(kBackBlock), 0,
                      static_cast<hipStream_t>(stream), b);
   return route_launch_check("combine backward");
 }
