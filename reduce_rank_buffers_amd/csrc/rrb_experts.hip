@@ -1037,6 +1037,35 @@ rrb_status check_spec(const rrb_expert_spec *s, const int32_t *offsets) {
   return RRB_OK;
 }
 
+// A buffer of a call: outputs must not share memory with any other.
+struct Span {
+  const void *at;
+  int64_t bytes;
+  const char *name;
+  bool out;
+};
+
+template <int N>
+rrb_status check_disjoint(const Span (&s)[N]) {
+  for (int i = 0; i < N; ++i) {
+    for (int j = 0; j < i; ++j) {
+      if ((!s[i].out && !s[j].out) || !s[i].at || !s[j].at) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].at), b = reinterpret_cast<uintptr_t>(s[j].at);
+      if (a < b + static_cast<uintptr_t>(s[j].bytes) && b < a + static_cast<uintptr_t>(s[i].bytes))
+        return fail(RRB_EINVAL, "%s overlaps %s", s[i].name, s[j].name);
+    }
+  }
+  return RRB_OK;
+}
+
+// Bytes of the arrays that the sizes name.
+struct Bytes {
+  int64_t x, y, w, bias, offsets;
+  explicit Bytes(const rrb_expert_spec &s)
+      : x(s.rows * s.in * 2), y(s.rows * s.out * 2), w(s.groups * s.in * s.out * 2), bias(s.groups * s.out * 2),
+        offsets((s.groups + 1ll) * 4) {}
+};
+
 ProductArgs base_args(const rrb_expert_spec &s, const int32_t *offsets) {
   ProductArgs p;
   std::memset(&p, 0, sizeof p);
@@ -1084,6 +1113,12 @@ rrb_status rrb_expert_gated(const rrb_expert_spec *spec, const void *d_x, const 
   if (spec->rows == 0) return RRB_OK;
   if (!d_x || !d_w_gate || !d_w_up || !d_out) return fail(RRB_EINVAL, "NULL x, w_gate, w_up or out");
   if (!d_save_gate != !d_save_up) return fail(RRB_EINVAL, "save_gate and save_up go together");
+  const Bytes z(*spec);
+  const Span spans[] = {{d_x, z.x, "x", false}, {d_offsets, z.offsets, "offsets", false},
+                        {d_w_gate, z.w, "w_gate", false}, {d_w_up, z.w, "w_up", false},
+                        {d_out, z.y, "out", true}, {d_save_gate, z.y, "save_gate", true},
+                        {d_save_up, z.y, "save_up", true}};
+  if ((st = check_disjoint(spans)) != RRB_OK) return st;
   ProductArgs p = base_args(*spec, d_offsets);
   p.a[0] = p.a[1] = u16(d_x);
   p.b[0] = u16(d_w_gate);
@@ -1108,6 +1143,14 @@ rrb_status rrb_expert_linear(const rrb_expert_spec *spec, const void *d_x, const
   if (st != RRB_OK) return st;
   if (spec->rows == 0) return RRB_OK;
   if (!d_x || !d_w || !d_out) return fail(RRB_EINVAL, "NULL x, w or out");
+  const Bytes z(*spec);
+  // The residual is read where the output is written, by the same lane: it
+  // may be the output itself.
+  const Span spans[] = {{d_x, z.x, "x", false}, {d_offsets, z.offsets, "offsets", false}, {d_w, z.w, "w", false},
+                        {d_bias, z.bias, "bias", false},
+                        {d_residual == d_out ? nullptr : d_residual, z.y, "residual", false},
+                        {d_out, z.y, "out", true}, {d_save_pre, z.y, "save_pre", true}};
+  if ((st = check_disjoint(spans)) != RRB_OK) return st;
   ProductArgs p = base_args(*spec, d_offsets);
   p.a[0] = p.a[1] = u16(d_x);
   p.b[0] = p.b[1] = u16(d_w);
@@ -1167,6 +1210,12 @@ rrb_status rrb_expert_gated_backward(const rrb_expert_spec *spec, const void *d_
     if (!d_workspace || workspace_bytes < need || !aligned(d_workspace, 16))
       return fail(RRB_EINVAL, "workspace of %zu bytes, 16-byte aligned, needed", need);
   }
+  const Bytes z(*spec);
+  const Span spans[] = {{d_dout, z.y, "dout", false}, {d_x, z.x, "x", false}, {d_offsets, z.offsets, "offsets", false},
+                        {d_w_gate, z.w, "w_gate", false}, {d_w_up, z.w, "w_up", false}, {d_gate, z.y, "gate", false},
+                        {d_up, z.y, "up", false}, {d_dx, z.x, "dx", true}, {d_dw_gate, z.w, "dw_gate", true},
+                        {d_dw_up, z.w, "dw_up", true}, {d_workspace, static_cast<int64_t>(need), "workspace", true}};
+  if ((st = check_disjoint(spans)) != RRB_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t pitch = padded(spec->out);
   uint16_t *dgate = u16(d_workspace);
@@ -1232,6 +1281,12 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
     if (!d_workspace || workspace_bytes < need || !aligned(d_workspace, 16))
       return fail(RRB_EINVAL, "workspace of %zu bytes, 16-byte aligned, needed", need);
   }
+  const Bytes z(*spec);
+  const Span spans[] = {{d_dout, z.y, "dout", false}, {d_x, z.x, "x", false}, {d_offsets, z.offsets, "offsets", false},
+                        {d_w, z.w, "w", false}, {act ? d_pre : nullptr, z.y, "pre", false}, {d_dx, z.x, "dx", true},
+                        {d_dw, z.w, "dw", true}, {d_dbias, z.bias, "dbias", true},
+                        {d_workspace, static_cast<int64_t>(need), "workspace", true}};
+  if ((st = check_disjoint(spans)) != RRB_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   ProductArgs p = base_args(*spec, d_offsets);
   p.a[0] = p.a[1] = u16(d_dout);

@@ -5,8 +5,9 @@ routing arrays from scores, the ``expert_*`` calls run on the dispatched rows,
 grouped by expert (``MoeDevicePlan.expert_offsets``), and each has its
 gradient.  Outputs are the caller's tensors, written in place; argument rules
 are api.py's (contiguous, on the current GPU, bf16 as torch.bfloat16 or its
-int16 / uint16 bit patterns), and shapes are checked too.  None of the calls
-takes part in autograd.
+int16 / uint16 bit patterns), and shapes are checked too; the library refuses
+outputs that overlap what a call reads.  None of the calls takes part in
+autograd.
 """
 
 import ctypes
@@ -14,17 +15,17 @@ import ctypes
 import torch
 
 from . import _lib as L
-from .api import _BF16_TYPES, _F32_TYPES, _dtype_of, _on_gpu, _stream
+from .api import _BF16_TYPES, _F32_TYPES, _dtype_of, _on_gpu
 
 ACTIVATIONS = {"none": L.RRB_ACT_NONE, "silu": L.RRB_ACT_SILU, "gelu": L.RRB_ACT_GELU,
                "gelu_tanh": L.RRB_ACT_GELU_TANH, "relu": L.RRB_ACT_RELU}
 
 
 def _shaped(t, what, shape, dtypes=_BF16_TYPES):
-    """ValueError unless t is a contiguous tensor of that shape and one of
-    these types; returns it (None for None)."""
+    """ValueError unless t is None or a contiguous tensor of that shape and
+    one of these types; returns (what, t) for _addresses."""
     if t is None:
-        return None
+        return what, None
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
@@ -33,46 +34,34 @@ def _shaped(t, what, shape, dtypes=_BF16_TYPES):
         raise ValueError(f"{what}: shape {tuple(t.shape)} is not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: tensor is not contiguous")
-    return t
+    return what, t
 
 
 def _addresses(named, optional=()):
-    """Addresses of the checked tensors, in order; those not in `optional`
-    must be there and every one on the current GPU."""
-    out = []
+    """Addresses of checked tensors, in order; those not in `optional` must be
+    there and every one on the current GPU.  Also its index."""
+    out, dev = [], None
     for what, t in named:
         if t is None:
             if what not in optional:
                 raise ValueError(f"{what} is required")
             out.append(None)
             continue
-        _on_gpu(t, what)
+        if t.get_device() != dev:
+            _on_gpu(t, what)
+            dev = t.get_device()
         out.append(t.data_ptr())
-    return out
+    return out, dev
 
 
-def _disjoint(outputs, inputs):
-    """ValueError where an output's memory overlaps an input's or another
-    output's (names and tensors; None entries are passed over)."""
-    spans = []
-    for is_out, group in ((True, outputs), (False, inputs)):
-        for what, t in group:
-            if t is not None and t.numel():
-                a = t.data_ptr()
-                spans.append((a, a + t.numel() * t.element_size(), is_out, what))
-    spans.sort()
-    end, last = 0, None
-    for a, b, is_out, what in spans:
-        if a < end and (is_out or last[0]):
-            raise ValueError(f"{what} overlaps {last[1]}")
-        if b > end:
-            end, last = b, (is_out, what)
-
-
-def _on_stream(stream):
-    if stream is not None and stream.device.index != torch.cuda.current_device():
+def _raw_stream(stream, dev):
+    """The HIP stream to launch on, without a Stream object where it is the
+    current one (building one takes as long as the rest of a call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
         raise ValueError(f"stream of {stream.device}, not of the current GPU")
-    return _stream(stream)
+    return stream.cuda_stream
 
 
 # ---- the gate ----------------------------------------------------------------
@@ -94,11 +83,11 @@ def moe_gate(logits, topk_idx, topk_w, renormalize=False, stream=None):
     them.  renormalize: weights over the chosen experts alone."""
     T, E, k = _gate_sizes(logits, topk_idx)
     dt = _dtype_of(logits)
-    named = [("logits", _shaped(logits, "logits", (T, E), (logits.dtype,))),
-             ("topk_idx", _shaped(topk_idx, "topk_idx", (T, k), (torch.int32,))),
-             ("topk_w", _shaped(topk_w, "topk_w", (T, k), _F32_TYPES))]
-    at = _addresses(named)
-    L.check(L.lib().rrb_moe_gate(T, E, k, dt, L.RRB_GATE_RENORMALIZE if renormalize else 0, *at, _on_stream(stream)),
+    named = [_shaped(logits, "logits", (T, E), (logits.dtype,)),
+             _shaped(topk_idx, "topk_idx", (T, k), (torch.int32,)),
+             _shaped(topk_w, "topk_w", (T, k), _F32_TYPES)]
+    at, dev = _addresses(named)
+    L.check(L.lib().rrb_moe_gate(T, E, k, dt, L.RRB_GATE_RENORMALIZE if renormalize else 0, *at, _raw_stream(stream, dev)),
             "rrb_moe_gate")
     return topk_idx, topk_w
 
@@ -108,13 +97,13 @@ def moe_gate_backward(logits, topk_idx, d_topk_w, d_logits, renormalize=False, s
     d_logits [T, E] of the scores' type, for moe_gate's logits and topk_idx."""
     T, E, k = _gate_sizes(logits, topk_idx)
     dt = _dtype_of(logits)
-    named = [("logits", _shaped(logits, "logits", (T, E), (logits.dtype,))),
-             ("topk_idx", _shaped(topk_idx, "topk_idx", (T, k), (torch.int32,))),
-             ("d_topk_w", _shaped(d_topk_w, "d_topk_w", (T, k), _F32_TYPES)),
-             ("d_logits", _shaped(d_logits, "d_logits", (T, E), (logits.dtype,)))]
-    at = _addresses(named)
+    named = [_shaped(logits, "logits", (T, E), (logits.dtype,)),
+             _shaped(topk_idx, "topk_idx", (T, k), (torch.int32,)),
+             _shaped(d_topk_w, "d_topk_w", (T, k), _F32_TYPES),
+             _shaped(d_logits, "d_logits", (T, E), (logits.dtype,))]
+    at, dev = _addresses(named)
     L.check(L.lib().rrb_moe_gate_backward(T, E, k, dt, L.RRB_GATE_RENORMALIZE if renormalize else 0, *at,
-                                          _on_stream(stream)), "rrb_moe_gate_backward")
+                                          _raw_stream(stream, dev)), "rrb_moe_gate_backward")
     return d_logits
 
 
@@ -136,7 +125,7 @@ def _spec(x, w, activation, what):
 def _offsets(offsets, G):
     if offsets is None and G != 1:
         raise ValueError(f"offsets is required with {G} groups")
-    return ("offsets", _shaped(offsets, "offsets", (G + 1,), (torch.int32,)))
+    return _shaped(offsets, "offsets", (G + 1,), (torch.int32,))
 
 
 def expert_gated(x, offsets, w_gate, w_up, out, activation="silu", save_gate=None, save_up=None, stream=None):
@@ -147,13 +136,12 @@ def expert_gated(x, offsets, w_gate, w_up, out, activation="silu", save_gate=Non
     spec, N, i, o, G = _spec(x, w_gate, activation, "w_gate")
     if (save_gate is None) != (save_up is None):
         raise ValueError("save_gate and save_up go together")
-    ins = [("x", _shaped(x, "x", (N, i))), _offsets(offsets, G),
-           ("w_gate", _shaped(w_gate, "w_gate", (G, o, i))), ("w_up", _shaped(w_up, "w_up", (G, o, i)))]
-    outs = [("out", _shaped(out, "out", (N, o))), ("save_gate", _shaped(save_gate, "save_gate", (N, o))),
-            ("save_up", _shaped(save_up, "save_up", (N, o)))]
-    at = _addresses(ins + outs, ("offsets", "save_gate", "save_up"))
-    _disjoint(outs, ins)
-    L.check(L.lib().rrb_expert_gated(ctypes.byref(spec), *at, _on_stream(stream)), "rrb_expert_gated")
+    ins = [_shaped(x, "x", (N, i)), _offsets(offsets, G),
+           _shaped(w_gate, "w_gate", (G, o, i)), _shaped(w_up, "w_up", (G, o, i))]
+    outs = [_shaped(out, "out", (N, o)), _shaped(save_gate, "save_gate", (N, o)),
+            _shaped(save_up, "save_up", (N, o))]
+    at, dev = _addresses(ins + outs, ("offsets", "save_gate", "save_up"))
+    L.check(L.lib().rrb_expert_gated(ctypes.byref(spec), *at, _raw_stream(stream, dev)), "rrb_expert_gated")
     return out
 
 
@@ -163,13 +151,11 @@ def expert_linear(x, offsets, w, out, bias=None, activation="none", residual=Non
     residual [N, out] (may be out itself).  save_pre [N, out] receives the
     pre-activation values that expert_linear_backward takes."""
     spec, N, i, o, G = _spec(x, w, activation, "w")
-    ins = [("x", _shaped(x, "x", (N, i))), _offsets(offsets, G), ("w", _shaped(w, "w", (G, o, i))),
-           ("bias", _shaped(bias, "bias", (G, o))), ("residual", _shaped(residual, "residual", (N, o)))]
-    outs = [("out", _shaped(out, "out", (N, o))), ("save_pre", _shaped(save_pre, "save_pre", (N, o)))]
-    at = _addresses(ins + outs, ("offsets", "bias", "residual", "save_pre"))
-    in_place = residual is not None and out is not None and residual.data_ptr() == out.data_ptr()
-    _disjoint(outs, ins[:-1] if in_place else ins)
-    L.check(L.lib().rrb_expert_linear(ctypes.byref(spec), *at, _on_stream(stream)), "rrb_expert_linear")
+    ins = [_shaped(x, "x", (N, i)), _offsets(offsets, G), _shaped(w, "w", (G, o, i)),
+           _shaped(bias, "bias", (G, o)), _shaped(residual, "residual", (N, o))]
+    outs = [_shaped(out, "out", (N, o)), _shaped(save_pre, "save_pre", (N, o))]
+    at, dev = _addresses(ins + outs, ("offsets", "bias", "residual", "save_pre"))
+    L.check(L.lib().rrb_expert_linear(ctypes.byref(spec), *at, _raw_stream(stream, dev)), "rrb_expert_linear")
     return out
 
 
@@ -216,16 +202,15 @@ def expert_gated_backward(d_out, x, offsets, w_gate, w_up, gate, up, activation=
         raise ValueError("d_w_gate and d_w_up go together")
     if d_x is None and d_w_gate is None:
         raise ValueError("no gradient asked for: d_x and d_w_gate are None")
-    ins = [("d_out", _shaped(d_out, "d_out", (N, o))), ("x", _shaped(x, "x", (N, i))), _offsets(offsets, G),
-           ("w_gate", _shaped(w_gate, "w_gate", (G, o, i))), ("w_up", _shaped(w_up, "w_up", (G, o, i))),
-           ("gate", _shaped(gate, "gate", (N, o))), ("up", _shaped(up, "up", (N, o)))]
-    outs = [("d_x", _shaped(d_x, "d_x", (N, i))), ("d_w_gate", _shaped(d_w_gate, "d_w_gate", (G, o, i))),
-            ("d_w_up", _shaped(d_w_up, "d_w_up", (G, o, i)))]
-    at = _addresses(ins + outs, ("offsets", "d_x", "d_w_gate", "d_w_up"))
+    ins = [_shaped(d_out, "d_out", (N, o)), _shaped(x, "x", (N, i)), _offsets(offsets, G),
+           _shaped(w_gate, "w_gate", (G, o, i)), _shaped(w_up, "w_up", (G, o, i)),
+           _shaped(gate, "gate", (N, o)), _shaped(up, "up", (N, o))]
+    outs = [_shaped(d_x, "d_x", (N, i)), _shaped(d_w_gate, "d_w_gate", (G, o, i)),
+            _shaped(d_w_up, "d_w_up", (G, o, i))]
+    at, dev = _addresses(ins + outs, ("offsets", "d_x", "d_w_gate", "d_w_up"))
     need = expert_gated_backward_workspace(N, i, o, G)
     ws = _workspace(workspace, need, x, stream)
-    _disjoint(outs + [("workspace", ws)], ins)
-    L.check(L.lib().rrb_expert_gated_backward(ctypes.byref(spec), *at, ws.data_ptr(), need, _on_stream(stream)),
+    L.check(L.lib().rrb_expert_gated_backward(ctypes.byref(spec), *at, ws.data_ptr(), need, _raw_stream(stream, dev)),
             "rrb_expert_gated_backward")
     return d_x, d_w_gate, d_w_up
 
@@ -243,14 +228,13 @@ def expert_linear_backward(d_out, x, offsets, w, pre=None, activation="none", d_
         raise ValueError("no gradient asked for: d_x, d_w and d_bias are None")
     if activation != "none" and pre is None:
         raise ValueError(f"pre is required with activation {activation!r}")
-    ins = [("d_out", _shaped(d_out, "d_out", (N, o))), ("x", _shaped(x, "x", (N, i))), _offsets(offsets, G),
-           ("w", _shaped(w, "w", (G, o, i))), ("pre", _shaped(pre, "pre", (N, o)))]
-    outs = [("d_x", _shaped(d_x, "d_x", (N, i))), ("d_w", _shaped(d_w, "d_w", (G, o, i))),
-            ("d_bias", _shaped(d_bias, "d_bias", (G, o)))]
-    at = _addresses(ins + outs, ("offsets", "pre", "d_x", "d_w", "d_bias"))
+    ins = [_shaped(d_out, "d_out", (N, o)), _shaped(x, "x", (N, i)), _offsets(offsets, G),
+           _shaped(w, "w", (G, o, i)), _shaped(pre, "pre", (N, o))]
+    outs = [_shaped(d_x, "d_x", (N, i)), _shaped(d_w, "d_w", (G, o, i)),
+            _shaped(d_bias, "d_bias", (G, o))]
+    at, dev = _addresses(ins + outs, ("offsets", "pre", "d_x", "d_w", "d_bias"))
     need = expert_linear_backward_workspace(N, i, o, G)
     ws = _workspace(workspace, need, x, stream)
-    _disjoint(outs + [("workspace", ws)], ins)
-    L.check(L.lib().rrb_expert_linear_backward(ctypes.byref(spec), *at, ws.data_ptr(), need, _on_stream(stream)),
+    L.check(L.lib().rrb_expert_linear_backward(ctypes.byref(spec), *at, ws.data_ptr(), need, _raw_stream(stream, dev)),
             "rrb_expert_linear_backward")
     return d_x, d_w, d_bias

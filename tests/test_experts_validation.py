@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import reduce_rank_buffers_amd as rrb
-from reduce_rank_buffers_amd import _lib as L, experts as X
+from reduce_rank_buffers_amd import _lib as L
 
 
 def _bf(*shape):
@@ -115,19 +115,6 @@ def test_binding_refuses(librrb, case):
     assert message in str(e.value)
 
 
-def test_overlaps_refused():
-    buf = torch.zeros(100, dtype=torch.bfloat16)
-    a, b, c = buf[:40], buf[30:60], buf[40:80]
-    X._disjoint([("a", a)], [("c", c)])
-    X._disjoint([("a", a), ("n", None)], [("c", c), ("b2", c)])  # inputs may share
-    with pytest.raises(ValueError):
-        X._disjoint([("a", a)], [("b", b)])
-    with pytest.raises(ValueError):
-        X._disjoint([("b", b), ("c", c)], [])
-    with pytest.raises(ValueError):
-        X._disjoint([("b", buf[90:95])], [("all", buf), ("a", a)])
-
-
 def _bare_plan(tk):
     p = rrb.MoeDevicePlan.__new__(rrb.MoeDevicePlan)
     p.handle = None
@@ -175,6 +162,11 @@ def test_expert_offsets_refuses():
 P = 4096  # a non-NULL address that no refused call reads
 
 
+def at(n):
+    """n addresses far apart."""
+    return [P + (i << 36) for i in range(n)]
+
+
 def _spec(rows=4, i=8, o=8, G=1, act=0):
     return ctypes.byref(L.ExpertSpec(rows, i, o, G, act))
 
@@ -202,39 +194,64 @@ def test_abi_refuses_pointers(librrb):
     s, E = _spec(), L.RRB_EINVAL
     f = librrb.rrb_expert_gated
     for i in (0, 2, 3, 4):
-        a = [P, P, P, P, P, None, None]
+        a = at(5) + [None, None]
         a[i] = None
         assert f(s, *a, None) == E
-    assert f(s, P, P, P, P, P, P, None, None) == E
+    assert f(s, *at(6), None, None) == E
     assert f(_spec(G=2), P, None, P, P, P, None, None, None) == E
     f = librrb.rrb_expert_linear
     for i in (0, 2, 5):
-        a = [P, P, P, None, None, P, None]
+        a = at(3) + [None, None, P << 20, None]
         a[i] = None
         assert f(s, *a, None) == E
     f = librrb.rrb_expert_gated_backward
     for i in (0, 1, 3, 4, 5, 6, 8, 10):
-        a = [P] * 11
+        a = at(11)
         a[i] = None
         assert f(s, *a, 1 << 20, None) == E
-    a = [P] * 11
+    a = at(11)
     a[7] = a[8] = a[9] = None
     assert f(s, *a, 1 << 20, None) == E
-    assert f(s, *([P] * 11), 4 * 8 * 4 - 1, None) == E
-    assert f(s, *([P] * 10), P + 8, 1 << 20, None) == E
+    assert f(s, *at(11), 4 * 8 * 4 - 1, None) == E
+    assert f(s, *at(10), (P << 30) + 8, 1 << 20, None) == E
     f = librrb.rrb_expert_linear_backward
     for i in (0, 1, 3, 8):
-        a = [P] * 9
+        a = at(9)
         a[i] = None
         assert f(s, *a, 1 << 20, None) == E
-    a = [P] * 9
+    a = at(9)
     a[4] = None
     assert f(_spec(act=1), *a, 1 << 20, None) == E
-    a = [P] * 9
+    a = at(9)
     a[5] = a[6] = a[7] = None
     assert f(s, *a, 1 << 20, None) == E
     assert librrb.rrb_expert_gated_backward_workspace(s, None) == E
     assert librrb.rrb_expert_linear_backward_workspace(s, None) == E
+
+
+def test_abi_refuses_overlaps(librrb):
+    """An output that shares its last byte with an input or another output."""
+    s, E = _spec(rows=4, i=8, o=16, G=2), L.RRB_EINVAL
+    x, y, w, off = 4 * 8 * 2, 4 * 16 * 2, 2 * 8 * 16 * 2, 12
+
+    def refused(f, args, sizes, outs, *more):
+        for o in outs:
+            for i in range(len(args)):
+                if i == o or args[i] is None:
+                    continue
+                a = list(args)
+                a[o] = a[i] + sizes[i] - 1
+                a[o] -= a[o] % 16 if o == len(args) - 1 and more else 0
+                assert f(s, *a, *more, None) == E
+                assert b"overlaps" in librrb.rrb_last_error()
+
+    refused(librrb.rrb_expert_gated, at(7), [x, off, w, w, y, y, y], (4, 5, 6))
+    refused(librrb.rrb_expert_linear, at(7), [x, off, w, 2 * 16 * 2, y, y, y], (5, 6))
+    ws = 4 * 16 * 2 * 2
+    refused(librrb.rrb_expert_gated_backward, at(11), [y, x, off, w, w, y, y, x, w, w, ws], (7, 8, 9, 10), 1 << 20)
+    a = at(9)
+    a[4] = None
+    refused(librrb.rrb_expert_linear_backward, a, [y, x, off, w, y, x, w, 64, ws // 2], (5, 6, 7, 8), 1 << 20)
 
 
 def test_abi_gate_refuses(librrb):

@@ -494,7 +494,7 @@ def test_stream_argument():
 # below (E + |l - m| + 8) 2^-23 relative.  bf16 gradients add half a step.
 
 GATES = [(1, 1, 1), (1, 8, 8), (5, 7, 3), (64, 64, 6), (33, 65, 16), (130, 128, 1), (40, 256, 8), (9, 300, 7),
-         (17, 1000, 16), (3, 1024, 16), (4099, 96, 4)]
+         (17, 1000, 16), (3, 1024, 16), (4099, 96, 4), (5000, 40, 5), (4500, 256, 8), (4200, 130, 16), (4100, 250, 3), (4097, 600, 2)]
 
 
 def _scores(T, E, kind, dtype):
