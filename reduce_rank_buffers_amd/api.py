@@ -110,6 +110,19 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(stream, dev=None):
+    """The HIP stream to launch on: the current one of the current GPU
+    (`dev`, where the caller knows it), without a torch Stream object (making
+    one takes longer than a launch), or `stream`, which must belong there."""
+    if dev is None:
+        dev = torch.cuda.current_device()
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device}, not of the current GPU")
+    return stream.cuda_stream
+
+
 def _ptrs(tensors, R):
     out = []
     for r in range(R):
@@ -383,7 +396,7 @@ class _MoeRows:
             self.handle, _ptrs(d_ys, R), _ptrs(zs, R) if d_weights is not None else None,
             _ptrs(d_zs, R) if d_zs is not None else None,
             weights.data_ptr() if weights is not None else None,
-            d_weights.data_ptr() if d_weights is not None else None, _stream(stream)),
+            d_weights.data_ptr() if d_weights is not None else None, _raw_stream(stream)),
             "rrb_moe_combine_backward")
 
 

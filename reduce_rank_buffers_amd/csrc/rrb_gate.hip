@@ -42,23 +42,30 @@ __device__ __forceinline__ void store_score(uint16_t *p, float v) { *p = f32_to_
 // NaN above +inf (so a row with a NaN has it among its experts and shows it
 // in its weights).  Always above 0.
 __device__ __forceinline__ uint32_t score_key(float f) {
-  if (f != f) return 0xffffffffu;
-  const uint32_t u = __float_as_uint(f == 0.f ? 0.f : f);
-  return u >> 31 ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(f + 0.f);  // -0 + 0 is +0
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return f != f ? 0xffffffffu : k;
 }
 __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);  // NaN keeps being one
 }
 
 // e^(l - m), where an expert masked out by -inf has no share (also where all
-// are) and scores of +inf share equally.
+// are) and scores of +inf share equally.  e^x = 2^t (1 + r ln 2) with
+// t = fl(x log2 e) and r what t lost of x log2 e, so the product's rounding
+// does not grow with |x|: 2 ulp, and 0 below 2^-126.
 __device__ __forceinline__ float share(float l, float m) {
-  if (l == -INFINITY) return 0.f;
-  return l == m ? 1.f : expf(l - m);
+  const float x = l - m;
+  const float t = x * 1.4426950408889634f;
+  const float r = __builtin_fmaf(x, 1.4426950408889634f, -t) + x * 1.925963033500e-8f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float v = __builtin_fmaf(e, r * 0.6931471805599453f, e);
+  return l == -INFINITY ? 0.f : l == m ? 1.f : e == 0.f ? 0.f : v;
 }
 
 // All-reduce over the L = 16 or 64 lanes of a token: within 16 lanes by DPP
-// (two quad permutations, two row rotations), across rows by shuffles.
+// (two quad permutations, two row rotations), across rows through scalar
+// registers.
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) {
   return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, false);
@@ -70,8 +77,9 @@ __device__ __forceinline__ int across(int v, F f) {
   v = f(v, dpp<0x124>(v));  // row_ror:4
   v = f(v, dpp<0x128>(v));  // row_ror:8
   if (L == 64) {
-    v = f(v, __shfl_xor(v, 16, 64));
-    v = f(v, __shfl_xor(v, 32, 64));
+    const int a = f(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16));
+    const int b = f(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48));
+    v = f(a, b);
   }
   return v;
 }
@@ -146,22 +154,26 @@ __global__ void __launch_bounds__(256) gate_kernel(GateArgs a) {
   for (int i = 0; i < V; ++i) sum += share(l[i], m);
   float mine = 0.f;
   int chosen = 0;
+  uint32_t best = 0;
   for (int j = 0; j < a.topk; ++j) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) best = max(best, key[i]);
-    best = most<L>(best);
     int e;
     float le;
     if (kShort) {
-      e = static_cast<int>(0xffffu - (best & 0xffffu));
-      le = key_score(best | 0xffffu);
-      // the key of a negative score is complemented: its lower half is ones
-      if (best >> 31) le = key_score(best & 0xffff0000u);
-      if (best >= 0xff810000u) le = NAN;
+      // Keys differ, so the next one is the largest below the last: as
+      // key - best wraps, the keys below best come out above the others, in
+      // their order.  (At first best is 0 and every key above it.)
+      uint32_t d = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = key[i] == best ? 0 : key[i];
+      for (int i = 0; i < V; ++i) d = max(d, key[i] - best);
+      best += most<L>(d);
+      e = static_cast<int>(0xffffu - (best & 0xffffu));
+      // the key of a negative score is complemented: its lower half is ones
+      le = best >= 0xff810000u ? NAN : key_score(best >> 31 ? best & 0xffff0000u : best | 0xffffu);
     } else {
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) best = max(best, key[i]);
+      best = most<L>(best);
       uint32_t low = 0xffffffffu;
 #pragma unroll
       for (int i = 0; i < V; ++i) {

@@ -15,7 +15,7 @@ import ctypes
 import torch
 
 from . import _lib as L
-from .api import _BF16_TYPES, _F32_TYPES, _dtype_of, _on_gpu
+from .api import _BF16_TYPES, _F32_TYPES, _dtype_of, _on_gpu, _raw_stream
 
 ACTIVATIONS = {"none": L.RRB_ACT_NONE, "silu": L.RRB_ACT_SILU, "gelu": L.RRB_ACT_GELU,
                "gelu_tanh": L.RRB_ACT_GELU_TANH, "relu": L.RRB_ACT_RELU}
@@ -52,16 +52,6 @@ def _addresses(named, optional=()):
             dev = t.get_device()
         out.append(t.data_ptr())
     return out, dev
-
-
-def _raw_stream(stream, dev):
-    """The HIP stream to launch on, without a Stream object where it is the
-    current one (building one takes as long as the rest of a call)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    if stream.device.index != dev:
-        raise ValueError(f"stream of {stream.device}, not of the current GPU")
-    return stream.cuda_stream
 
 
 # ---- the gate ----------------------------------------------------------------
