@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstring>
+#include <type_traits>
 #include <cstdlib>
 
 #include "rrb_internal.h"
@@ -254,10 +255,11 @@ __device__ __forceinline__ void store_cols(uint16_t *dst, int have, bool whole, 
 // blocks were dealt together (WIDE), the first or second half of eight at
 // 8 (l / 16).  Gated: blocks are gate and up by turns.
 // `whole`: rows start on 8-byte boundaries and all of the wave's columns exist.
+// The second FM / 2 blocks of rows begin `half` rows behind the first.
 template <int ACT, bool GATED, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (&acc)[FM][FN], uint16_t *c,
                                            uint16_t *save0, uint16_t *save1, const uint16_t *bias,
-                                           const uint16_t *residual, int m0, int mvalid, int n0, bool whole) {
+                                           const uint16_t *residual, int m0, int half, int mvalid, int n0, bool whole) {
   constexpr int W = WIDE ? 8 : 4;                       // consecutive columns per lane
   constexpr int BLOCKS = (GATED ? 2 : 1) * (WIDE ? 2 : 1);  // blocks that make them
   const int lane = threadIdx.x & 63;
@@ -269,7 +271,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (
     if (!GATED && bias && have > 0) load_cols<W>(bias + n, have, whole, b);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int m = m0 + i * 16 + (lane & 15);
+      const int m = m0 + (i >= FM / 2 ? half + (i - FM / 2) * 16 : i * 16) + (lane & 15);
       if (m >= mvalid || have <= 0) continue;
       const int64_t at = m * p.ldc + n;
       float v[W];
@@ -373,11 +375,12 @@ __device__ __forceinline__ Place place_tile(const ProductArgs &p) {
   return t;
 }
 
-// Stores a wave's part of the tile, at rows wm and output columns wn of it.
-// DEALT: row regions were dealt for eight columns per lane.
+// Stores a wave's part of the tile, at output columns wn and rows wm of it, the
+// second half of these `half` rows on.  DEALT: row regions were dealt for eight
+// columns per lane.
 template <int FORM, bool GATED, bool DEALT, int FM, int FN>
 __device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t, const f32x4_t (&acc)[FM][FN], int wm,
-                                            int wn) {
+                                            int half, int wn) {
   constexpr bool WIDE = DEALT && FORM == kForward;
   constexpr int COLS = FN * 16 / (GATED ? 2 : 1);
   const int n = t.n0 + wn;
@@ -390,7 +393,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t
     if (p.bias) bias = p.bias + static_cast<int64_t>(t.e) * p.n;
     if (p.residual) res = p.residual + t.row0 * p.ldc;
   }
-#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, wm, t.mvalid, n, whole);
+#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, wm, half, t.mvalid, n, whole);
   if (FORM != kForward) {
     RRB_STORE(RRB_ACT_NONE)
     return;
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
     }
     if (s + 1 < steps) commit((s + 1) & 1);
   }
-  finish_tile<FORM, GATED, false>(p, t, acc, wm, GATED ? wn / 2 : wn);
+  finish_tile<FORM, GATED, false>(p, t, acc, wm, FM * 8, GATED ? wn / 2 : wn);
 }
 
 // ---- the tiled product, loads straight to LDS -----------------------------------
@@ -546,14 +549,14 @@ __device__ __forceinline__ void load_to_lds(u32x4_t d, int at, int voffset, int 
                : "memory");
 }
 
-template <int BM, int BN, int WR, int WC, int FORM, bool GATED>
+template <int BM, int BN, int WR, int WC, int STAGES, int FORM, bool GATED>
 __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs p) {
   constexpr int NT = WR * WC * 64;
   constexpr int FM = BM / WR / 16, FN = BN / WC / 16;
   constexpr int A_BYTES = BM * kStep * 2, B_BYTES = BN * kStep * 2;
   constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT, NCOLS = GATED ? BN / 2 : BN;
   constexpr bool A_COL = FORM == kGradW, B_COL = FORM != kForward;
-  __shared__ __align__(16) unsigned char lds[2 * (A_BYTES + B_BYTES)];
+  __shared__ __align__(16) unsigned char lds[STAGES * (A_BYTES + B_BYTES)];
 
   const int tid = threadIdx.x;
   const int wave = uniform(tid >> 6);
@@ -590,21 +593,23 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
     }
   }
 
-  // Starts one step's loads into buffer `buf`.
+  // Starts one step's loads into buffer `buf`; past the end through an empty
+  // descriptor, so that every step counts the same.
   auto issue = [&](int step, int buf) {
     const int h = FORM == kGradX && step >= per ? 1 : 0;
     const int kstep = step - h * per;
     const int k0 = kstep * kStep;
     const int left = klen - k0;
+    const bool live = step < steps;
     const int rows = left < kStep ? left : kStep;  // of the column tiles
     const int ta = lds_address(lds) + buf * (A_BYTES + B_BYTES) + wave * 1024, tb = ta + A_BYTES;
     if (A_COL) {
-      const auto d = descriptor(t.a[0] + k0 * p.lda, rows * lda2 - t.m0 * 2);
+      const auto d = descriptor(t.a[0] + k0 * p.lda, live ? rows * lda2 - t.m0 * 2 : 0);
 #pragma unroll
       for (int i = 0; i < CA; ++i)
         load_to_lds(d, ta + i * NT * 16, va[i], 0);
     } else {
-      const auto d = descriptor(t.a[h], t.mvalid * lda2);
+      const auto d = descriptor(t.a[h], live ? t.mvalid * lda2 : 0);
 #pragma unroll
       for (int i = 0; i < CA; ++i) {
         int v = va[i];
@@ -616,12 +621,12 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
       }
     }
     if (B_COL) {
-      const auto d = descriptor(t.b[h] + k0 * p.ldb, rows * ldb2 - t.n0 * 2);
+      const auto d = descriptor(t.b[h] + k0 * p.ldb, live ? rows * ldb2 - t.n0 * 2 : 0);
 #pragma unroll
       for (int i = 0; i < CB; ++i)
         load_to_lds(d, tb + i * NT * 16, vb[i], 0);
     } else {
-      const int bytes = (p.n - t.n0 < NCOLS ? p.n - t.n0 : NCOLS) * ldb2;
+      const int bytes = live ? (p.n - t.n0 < NCOLS ? p.n - t.n0 : NCOLS) * ldb2 : 0;
       const auto d0 = descriptor(t.b[0], bytes);
       const auto d1 = descriptor(GATED ? t.b[1] : t.b[0], bytes);
 #pragma unroll
@@ -641,13 +646,19 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
   const int wm = wave / WC * (BM / WR), wn = wave % WC * (BN / WC);
   f32x4_t acc[FM][FN];
   clear_tile(acc);
-  if (steps > 0) issue(0, 0);
+  if (steps > 0) {
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+  }
+  int buf = 0, free = STAGES - 1;
   for (int s = 0; s < steps; ++s) {
-    // This step's loads have landed, and every wave is done with the other
-    // buffer.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (s + 1 < steps) issue(s + 1, (s + 1) & 1);
-    const unsigned char *ta = lds + (s & 1) * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;
+    // This step's loads have landed, and every wave is done with the buffer
+    // that is loaded next.
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (CA + CB)) : "memory");
+    issue(s + STAGES - 1, free);
+    free = buf;
+    const unsigned char *ta = lds + buf * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;
+    buf = buf + 1 == STAGES ? 0 : buf + 1;
 #pragma unroll
     for (int kk = 0; kk < kStep / 32; ++kk) {
       bf16x8_t fa[FM], fb[FN];
@@ -664,7 +675,8 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
   }
-  finish_tile<FORM, GATED, false>(p, t, acc, wm, GATED ? wn / 2 : wn);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  finish_tile<FORM, GATED, false>(p, t, acc, wm, FM * 8, GATED ? wn / 2 : wn);
 }
 
 // ---- the tiled product, two wave groups by turns -----------------------------------
@@ -674,7 +686,8 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 // group issues 16 matrix instructions (a quarter of its step) the other reads
 // fragments and starts loads, so a SIMD's matrix core and the LDS work at the
 // same time.  A step's tiles are kept as four regions of 16 KiB, the first and
-// second halves of each wave's rows (A0, A1) and columns (B0, B1), two steps
+// second 128 rows (A0, A1; a group has 64 of each) and the first and second
+// halves of each wave's columns (B0, B1), two steps
 // deep.  In phase p a group reads and starts
 //   0  reads B0, half of A1;            starts A1 of step s + 1;    A0 x B0
 //   1  reads the rest of A1;                                        A0 x B1
@@ -687,7 +700,9 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 // six of its loads be in flight when it passes phase 1, 2 or 3, which leaves
 // what the next phase reads (A0; B1; A1 and B0) complete in every wave before
 // the barrier between.  Steps past the end load through an empty descriptor
-// (zeros, no memory access), so the count holds to the last step.
+// (zeros, no memory access), so the count holds to the last step.  A tile of at
+// most 128 valid rows loads nothing for A1 and leaves out its reads and
+// products, so it costs half the matrix instructions of a whole one.
 
 // Row of B (column of the output) that sits at row r of half h of a row region.
 // Sixteen rows make a fragment and a lane holds four consecutive ones of each;
@@ -724,10 +739,10 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
       const int kr = id >> 4, c = (id & 15) ^ (col_swizzle(kr) << 1);
       const int r = id >> 3;
       if (A_COL) {
-        va[h][i] = kr * lda2 + ((c >> 3) * 128 + h * 64 + (c & 7) * 8) * 2;
+        va[h][i] = kr * lda2 + (h * 128 + c * 8) * 2;
       } else {
-        const int m = (r >> 6) * 128 + h * 64 + (r & 63);
-        va[h][i] = (m < t.mvalid ? m : t.mvalid - 1) * lda2 + ch * 16;
+        const int m = h * 128 + r;
+        va[h][i] = m < t.mvalid ? m * lda2 + ch * 16 : kOutside;
       }
       if (B_COL) {
         vb[h][i] = kr * ldb2 + ((c >> 2) * 64 + h * 32 + (c & 3) * 8) * 2;
@@ -738,6 +753,7 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
     }
   }
   const int to = lds_address(lds) + wave * 1024;
+  const bool both = t.mvalid > 128;  // rows in A1
 
   auto start_a = [&](int step, int h) {
     const int ph = FORM == kGradX && step >= per ? 1 : 0;
@@ -747,11 +763,11 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
     const int dst = to + (step & 1) * BUFFER + h * REGION;
     const bool live = step < steps;
     if (A_COL) {
-      const auto d = descriptor(t.a[0] + k0 * p.lda, live ? rows * lda2 - t.m0 * 2 : 0);
+      const auto d = descriptor(t.a[0] + k0 * p.lda, live && (h == 0 || both) ? rows * lda2 - t.m0 * 2 : 0);
       load_to_lds(d, dst, va[h][0], 0);
       load_to_lds(d, dst + 8192, va[h][1], 0);
     } else {
-      const auto d = descriptor(t.a[ph], live ? t.mvalid * lda2 : 0);
+      const auto d = descriptor(t.a[ph], live && (h == 0 || both) ? t.mvalid * lda2 : 0);
       const bool out = left < kStep && ch * 8 >= left;
       load_to_lds(d, dst, out ? kOutside : va[h][0], ks * 128);
       load_to_lds(d, dst + 8192, out ? kOutside : va[h][1], ks * 128);
@@ -858,41 +874,49 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
     if (wr) {
       RRB_BARRIER();
     }
-    for (int s = 0; s < steps; ++s) {
-      const unsigned char *buf = lds + (s & 1) * BUFFER, *next = lds + (~s & 1) * BUFFER;
-      read_b(buf, 0);
-      read_a(buf, 1, 0);
-      start_a(s + 1, 1);
-      RRB_BARRIER();
-      multiply(0, 0);
-      RRB_BARRIER();
-      read_a(buf, 1, 1);
-      asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-      RRB_BARRIER();
-      multiply(0, 1);
-      RRB_BARRIER();
-      read_a(next, 0, 0);
-      start_a(s + 2, 0);
-      start_b(s + 2, 0);
-      asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-      RRB_BARRIER();
-      multiply(1, 1);
-      RRB_BARRIER();
-      read_a(next, 0, 1);
-      read_b(next, 1);
-      start_b(s + 2, 1);
-      asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-      RRB_BARRIER();
-      multiply(1, 0);
-      RRB_BARRIER();
-    }
+    // Two loops, so that each one's waits count the reads it makes.
+    auto run = [&](auto whole) {
+      constexpr bool BOTH = decltype(whole)::value;
+      for (int s = 0; s < steps; ++s) {
+        const unsigned char *buf = lds + (s & 1) * BUFFER, *next = lds + (~s & 1) * BUFFER;
+        read_b(buf, 0);
+        if (BOTH) read_a(buf, 1, 0);
+        start_a(s + 1, 1);
+        RRB_BARRIER();
+        multiply(0, 0);
+        RRB_BARRIER();
+        if (BOTH) read_a(buf, 1, 1);
+        asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+        RRB_BARRIER();
+        multiply(0, 1);
+        RRB_BARRIER();
+        read_a(next, 0, 0);
+        start_a(s + 2, 0);
+        start_b(s + 2, 0);
+        asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+        RRB_BARRIER();
+        if (BOTH) multiply(1, 1);
+        RRB_BARRIER();
+        read_a(next, 0, 1);
+        read_b(next, 1);
+        start_b(s + 2, 1);
+        asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+        RRB_BARRIER();
+        if (BOTH) multiply(1, 0);
+        RRB_BARRIER();
+      }
+    };
+    if (both)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
     if (!wr) {
       RRB_BARRIER();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 #undef RRB_BARRIER
-  finish_tile<FORM, GATED, true>(p, t, acc, wr * 128, GATED ? wc * 32 : wc * 64);
+  finish_tile<FORM, GATED, true>(p, t, acc, wr * 64, 128, GATED ? wc * 32 : wc * 64);
 }
 
 // ---- gradients before the activation -------------------------------------------
@@ -1015,7 +1039,23 @@ rrb_status launch_product(const ProductArgs &p, hipStream_t s) {
   bool direct = p.lda % 8 == 0 && p.ldb % 8 == 0;
   for (int h = 0; h < 2; ++h) direct = direct && aligned(p.a[h], 16) && aligned(p.b[h], 16);
   if (!direct) return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
-  if (getenv("RRB_T128")) return launch_tiles<128, 128, FORM, GATED>(product_direct_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
+  if (const char *v = getenv("RRB_T")) {
+    switch (atoi(v)) {
+#define T(i, M, N, R, C, S) case i: return launch_tiles<M, N, FORM, GATED>(product_direct_kernel<M, N, R, C, S, FORM, GATED>, R * C * 64, p, s);
+      T(1, 128, 128, 2, 2, 2)
+      T(2, 32, 64, 1, 2, 4)
+      T(3, 32, 128, 1, 4, 4)
+      T(4, 32, 128, 1, 4, 3)
+      T(5, 64, 128, 1, 4, 2)
+      T(6, 64, 128, 1, 4, 3)
+      T(7, 128, 128, 2, 2, 4)
+      T(8, 128, 256, 2, 4, 2)
+      T(9, 128, 256, 2, 4, 3)
+      T(10, 64, 256, 1, 4, 3)
+      T(11, 64, 256, 2, 4, 3)
+      T(12, 256, 128, 4, 2, 3)
+    }
+  }
   return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED>, 512, p, s);
 }
 
