@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstring>
+#include <initializer_list>
 #include <type_traits>
 #include <cstdlib>
 
@@ -123,7 +124,7 @@ struct ProductArgs {
   int32_t bm, bn;         // tiles of one XCD's block: bm slots x bn column tiles
   int32_t halves;         // kGradX: phases; kGradW: outputs
   int32_t act;
-  int32_t cvec;           // every output row starts on an 8-byte boundary
+  int32_t cvec, lines;    // every output row starts on an 8-, a 16-byte boundary
 };
 
 // Offsets as the kernels read them: inside the arena whatever the array
@@ -255,14 +256,61 @@ __device__ __forceinline__ void store_cols(uint16_t *dst, int have, bool whole, 
 // blocks were dealt together (WIDE), the first or second half of eight at
 // 8 (l / 16).  Gated: blocks are gate and up by turns.
 // `whole`: rows start on 8-byte boundaries and all of the wave's columns exist.
+// `stage` (not gated; 64 columns, rows on 16-byte boundaries): 16 KiB of LDS of
+// the wave's own, through which results leave as whole 128-byte lines instead
+// of 32- or 64-byte pieces: a row of 64 columns is eight 16-byte chunks, stored
+// at chunk ^ row / 2 % 8, so that neither side meets its own banks.
 // The second FM / 2 blocks of rows begin `half` rows behind the first.
 template <int ACT, bool GATED, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (&acc)[FM][FN], uint16_t *c,
                                            uint16_t *save0, uint16_t *save1, const uint16_t *bias,
-                                           const uint16_t *residual, int m0, int half, int mvalid, int n0, bool whole) {
+                                           const uint16_t *residual, int m0, int half, int mvalid, int n0, bool whole,
+                                           unsigned char *stage) {
   constexpr int W = WIDE ? 8 : 4;                       // consecutive columns per lane
   constexpr int BLOCKS = (GATED ? 2 : 1) * (WIDE ? 2 : 1);  // blocks that make them
   const int lane = threadIdx.x & 63;
+  // To `to` directly, or into the stage.
+  auto put = [&](uint16_t *to, int64_t at, int i, int j, int have, const float (&v)[W]) {
+    if (!GATED && stage) {
+      const int r = i * 16 + (lane & 15);
+      const int col = j * 16 + (lane >> 4) * W;
+      unsigned char *q = stage + r * 128 + ((col >> 3) ^ row_swizzle(r)) * 16 + (col & 7) * 2;
+      *reinterpret_cast<uint2 *>(q) = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+      if (W == 8)
+        *reinterpret_cast<uint2 *>(q + 8) = make_uint2(cvt_pk_bf16(v[W - 4], v[W - 3]), cvt_pk_bf16(v[W - 2], v[W - 1]));
+    } else if (have > 0) {
+      store_cols<W>(to + at, have, whole, v);
+    }
+  };
+  // The staged tile to `to`.
+  auto flush = [&](uint16_t *to) {
+    if (GATED || !stage) return;
+    const int n = n0 + (lane & 7) * 8;
+#pragma unroll
+    for (int b = 0; b < FM * 2; ++b) {
+      const int r = b * 8 + (lane >> 3);
+      const int m = m0 + (r >= FM * 8 ? half + r - FM * 8 : r);
+      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(stage + r * 128 + ((lane & 7) ^ row_swizzle(r)) * 16);
+      if (m < mvalid && n < p.n) *reinterpret_cast<u32x4_t *>(to + m * p.ldc + n) = v;
+    }
+  };
+  if (!GATED && save0 && stage) {
+    // The pre-activation first: the stage holds one output at a time.
+#pragma unroll
+    for (int j = 0; j < FN; j += BLOCKS) {
+      const int n = n0 + j / BLOCKS * W * 4 + (lane >> 4) * W;
+      float b[W];
+      if (bias) load_cols<W>(bias + n, p.n - n, whole, b);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        float v[W];
+#pragma unroll
+        for (int q = 0; q < W; ++q) v[q] = acc[i][j + (q >> 2)][q & 3] + (bias ? b[q] : 0.f);
+        put(nullptr, 0, i, j, 0, v);
+      }
+    }
+    flush(save0);
+  }
 #pragma unroll
   for (int j = 0; j < FN; j += BLOCKS) {
     const int n = n0 + j / BLOCKS * W * 4 + (lane >> 4) * W;
@@ -272,7 +320,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int m = m0 + (i >= FM / 2 ? half + (i - FM / 2) * 16 : i * 16) + (lane & 15);
-      if (m >= mvalid || have <= 0) continue;
+      if (m >= mvalid || (have <= 0 && !stage)) continue;
       const int64_t at = m * p.ldc + n;
       float v[W];
       if (GATED) {
@@ -295,7 +343,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (
 #pragma unroll
           for (int q = 0; q < W; ++q) v[q] += b[q];
         }
-        if (save0) store_cols<W>(save0 + at, have, whole, v);
+        if (save0 && !stage) store_cols<W>(save0 + at, have, whole, v);
 #pragma unroll
         for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]);
         if (residual) {
@@ -305,9 +353,10 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (
           for (int q = 0; q < W; ++q) v[q] += r[q];
         }
       }
-      store_cols<W>(c + at, have, whole, v);
+      put(c, at, i, j, have, v);
     }
   }
+  flush(c);
 }
 
 // ---- the tiled product ------------------------------------------------------------
@@ -380,7 +429,7 @@ __device__ __forceinline__ Place place_tile(const ProductArgs &p) {
 // columns per lane.
 template <int FORM, bool GATED, bool DEALT, int FM, int FN>
 __device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t, const f32x4_t (&acc)[FM][FN], int wm,
-                                            int half, int wn) {
+                                            int half, int wn, unsigned char *stage) {
   constexpr bool WIDE = DEALT && FORM == kForward;
   constexpr int COLS = FN * 16 / (GATED ? 2 : 1);
   const int n = t.n0 + wn;
@@ -393,7 +442,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t
     if (p.bias) bias = p.bias + static_cast<int64_t>(t.e) * p.n;
     if (p.residual) res = p.residual + t.row0 * p.ldc;
   }
-#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, wm, half, t.mvalid, n, whole);
+#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, wm, half, t.mvalid, n, whole, p.lines ? stage : nullptr);
   if (FORM != kForward) {
     RRB_STORE(RRB_ACT_NONE)
     return;
@@ -513,7 +562,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
     }
     if (s + 1 < steps) commit((s + 1) & 1);
   }
-  finish_tile<FORM, GATED, false>(p, t, acc, wm, FM * 8, GATED ? wn / 2 : wn);
+  finish_tile<FORM, GATED, false>(p, t, acc, wm, FM * 8, GATED ? wn / 2 : wn, nullptr);
 }
 
 // ---- the tiled product, loads straight to LDS -----------------------------------
@@ -676,7 +725,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  finish_tile<FORM, GATED, false>(p, t, acc, wm, FM * 8, GATED ? wn / 2 : wn);
+  finish_tile<FORM, GATED, false>(p, t, acc, wm, FM * 8, GATED ? wn / 2 : wn, nullptr);
 }
 
 // ---- the tiled product, two wave groups by turns -----------------------------------
@@ -913,10 +962,13 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
     if (!wr) {
       RRB_BARRIER();
     }
+    // The last loads (of steps past the end) have landed in every wave: the
+    // epilogue takes the LDS over.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    RRB_BARRIER();
   }
 #undef RRB_BARRIER
-  finish_tile<FORM, GATED, true>(p, t, acc, wr * 64, 128, GATED ? wc * 32 : wc * 64);
+  finish_tile<FORM, GATED, true>(p, t, acc, wr * 64, 128, GATED ? wc * 32 : wc * 64, GATED ? nullptr : lds + wave * 16384);
 }
 
 // ---- gradients before the activation -------------------------------------------
@@ -1134,6 +1186,13 @@ rrb_status launch_act_grad(const ActGradArgs &a, int act, hipStream_t s) {
   return launched("activation gradient");
 }
 
+void set_output_alignment(ProductArgs &p, std::initializer_list<const void *> arrays) {
+  uintptr_t bits = static_cast<uintptr_t>(p.ldc * 2);
+  for (const void *a : arrays) bits |= reinterpret_cast<uintptr_t>(a);
+  p.cvec = bits % 8 == 0;
+  p.lines = bits % 16 == 0;
+}
+
 const uint16_t *u16(const void *p) { return static_cast<const uint16_t *>(p); }
 uint16_t *u16(void *p) { return static_cast<uint16_t *>(p); }
 
@@ -1171,7 +1230,7 @@ rrb_status rrb_expert_gated(const rrb_expert_spec *spec, const void *d_x, const 
   p.n = static_cast<int32_t>(spec->out);
   p.k = static_cast<int32_t>(spec->in);
   p.act = spec->activation;
-  p.cvec = p.ldc % 4 == 0 && aligned(d_out, 8) && aligned(d_save_gate, 8) && aligned(d_save_up, 8);
+  set_output_alignment(p, {d_out, d_save_gate, d_save_up});
   return launch_product<kForward, true>(p, static_cast<hipStream_t>(stream));
 }
 
@@ -1203,8 +1262,7 @@ rrb_status rrb_expert_linear(const rrb_expert_spec *spec, const void *d_x, const
   p.n = static_cast<int32_t>(spec->out);
   p.k = static_cast<int32_t>(spec->in);
   p.act = spec->activation;
-  p.cvec = p.ldc % 4 == 0 && aligned(d_out, 8) && aligned(d_save_pre, 8) && aligned(d_bias, 8) &&
-           aligned(d_residual, 8);
+  set_output_alignment(p, {d_out, d_save_pre, d_bias, d_residual});
   return launch_product<kForward, false>(p, static_cast<hipStream_t>(stream));
 }
 
@@ -1238,7 +1296,8 @@ rrb_status rrb_expert_gated_backward(const rrb_expert_spec *spec, const void *d_
   clear_error();
   rrb_status st = check_spec(spec, d_offsets);
   if (st != RRB_OK) return st;
-  if (!d_dx && !d_dw_gate) return fail(RRB_EINVAL, "no gradient asked for");
+  // (Without rows dx is empty, and its address may be NULL.)
+  if (spec->rows > 0 && !d_dx && !d_dw_gate) return fail(RRB_EINVAL, "no gradient asked for");
   if (!d_dw_gate != !d_dw_up) return fail(RRB_EINVAL, "dw_gate and dw_up go together");
   size_t need = 0;
   st = rrb_expert_gated_backward_workspace(spec, &need);
@@ -1286,7 +1345,7 @@ rrb_status rrb_expert_gated_backward(const rrb_expert_spec *spec, const void *d_
     q.c[0] = u16(d_dx);
     q.ldb = q.ldc = spec->in;
     q.k = static_cast<int32_t>(spec->out);
-    q.cvec = q.ldc % 4 == 0 && aligned(d_dx, 8);
+    set_output_alignment(q, {d_dx});
     if ((st = launch_product<kGradX, false>(q, s)) != RRB_OK) return st;
   }
   if (d_dw_gate) {
@@ -1295,7 +1354,7 @@ rrb_status rrb_expert_gated_backward(const rrb_expert_spec *spec, const void *d_
     p.c[1] = u16(d_dw_up);
     p.ldb = p.ldc = spec->in;
     p.m = static_cast<int32_t>(spec->out);
-    p.cvec = p.ldc % 4 == 0 && aligned(d_dw_gate, 8) && aligned(d_dw_up, 8);
+    set_output_alignment(p, {d_dw_gate, d_dw_up});
     if ((st = launch_product<kGradW, false>(p, s)) != RRB_OK) return st;
   }
   return RRB_OK;
@@ -1308,7 +1367,7 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
   clear_error();
   rrb_status st = check_spec(spec, d_offsets);
   if (st != RRB_OK) return st;
-  if (!d_dx && !d_dw && !d_dbias) return fail(RRB_EINVAL, "no gradient asked for");
+  if (spec->rows > 0 && !d_dx && !d_dw && !d_dbias) return fail(RRB_EINVAL, "no gradient asked for");
   size_t need = 0;
   st = rrb_expert_linear_backward_workspace(spec, &need);
   if (st != RRB_OK) return st;
@@ -1355,7 +1414,7 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
     q.c[0] = u16(d_dx);
     q.ldb = q.ldc = spec->in;
     q.k = static_cast<int32_t>(spec->out);
-    q.cvec = q.ldc % 4 == 0 && aligned(d_dx, 8);
+    set_output_alignment(q, {d_dx});
     if ((st = launch_product<kGradX, false>(q, s)) != RRB_OK) return st;
   }
   if (d_dw) {
@@ -1364,7 +1423,7 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
     q.c[0] = q.c[1] = u16(d_dw);
     q.ldb = q.ldc = spec->in;
     q.m = static_cast<int32_t>(spec->out);
-    q.cvec = q.ldc % 4 == 0 && aligned(d_dw, 8);
+    set_output_alignment(q, {d_dw});
     if ((st = launch_product<kGradW, false>(q, s)) != RRB_OK) return st;
   }
   if (d_dbias) {

@@ -404,6 +404,8 @@ def test_no_rows():
     g.fill_(1)
     rrb.expert_linear_backward(y, x, off, w, d_x=x, d_w=g, d_bias=b)
     assert not g.any() and not b.any()
+    rrb.expert_linear_backward(y, x, off, w, d_x=x)
+    rrb.expert_gated_backward(y, x, off, w, w, y, y, d_x=x)
 
 
 def test_partial_gradients():
