@@ -121,7 +121,7 @@ struct ProductArgs {
   int32_t m, n, k;        // m: kGradW only; k: kForward, kGradX only
   int32_t slots;          // kForward, kGradX: row-tile slots; kGradW: m tiles of both outputs
   int32_t ntiles;
-  int32_t bm, bn;         // tiles of one XCD's block: bm slots x bn column tiles
+  int32_t bm, bn;         // tiles of one XCD's block: bm slots x bn column tiles, or bm in a row
   int32_t halves;         // kGradX: phases; kGradW: outputs
   int32_t act;
   int32_t cvec, lines;    // every output row starts on an 8-, a 16-byte boundary
@@ -371,57 +371,119 @@ struct Place {
   bool empty;
 };
 
-// BM x NCOLS outputs per tile.
+// Tile (mt, nt) of group e, whose rows are first .. last - 1; BM x NCOLS
+// outputs.  kGradW: mt counts the tiles of both outputs.
 template <int BM, int NCOLS, int FORM>
-__device__ __forceinline__ Place place_tile(const ProductArgs &p) {
+__device__ __forceinline__ Place place_at(const ProductArgs &p, int e, int first, int last, int mt, int nt) {
   Place t;
-  // Workgroup i runs on XCD i % 8.  Each XCD takes blocks of bm x bn tiles,
-  // every eighth block, so that the tiles that share operand rows at the same
-  // time share an L2.
-  const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
-  const int size = p.bm * p.bn;
-  int block = at / size * 8 + xcd;
-  const int in = at % size;
-  const int down = (p.slots + p.bm - 1) / p.bm, across = (p.ntiles + p.bn - 1) / p.bn;
-  t.e = 0;
-  if (FORM == kGradW) {
-    t.e = block / (down * across);
-    block -= t.e * (down * across);
-  }
-  const int slot = block / across * p.bm + in % p.bm;
-  const int nt = block % across * p.bn + in / p.bm;
-  t.row0 = 0;
-  t.m0 = 0;
+  t.e = e;
   t.n0 = nt * NCOLS;
-  t.empty = slot >= p.slots || nt >= p.ntiles || t.e >= p.groups;
-  if (t.empty) return t;
+  t.empty = false;
   if (FORM == kGradW) {
-    const int mt = p.slots / p.halves;
-    const int half = slot / mt;
-    t.m0 = (slot - half * mt) * BM;
-    const int32_t first = uniform(offset_at(p, t.e)), last = uniform(offset_at(p, t.e + 1));
+    const int tiles = p.slots / p.halves;
+    const int half = mt / tiles;
+    t.row0 = 0;
+    t.m0 = (mt - half * tiles) * BM;
     t.klen = last > first ? last - first : 0;
     t.mvalid = p.m - t.m0;
     t.a[0] = t.a[1] = uniform(p.a[half] + first * p.lda + t.m0);
     t.b[0] = t.b[1] = uniform(p.b[0] + first * p.ldb + t.n0);
-    t.c = p.c[half] + t.e * p.bstride + t.m0 * p.ldc;
+    t.c = p.c[half] + e * p.bstride + t.m0 * p.ldc;
   } else {
-    t.e = uniform(group_of_slot<BM>(p, slot));
-    const int32_t first = uniform(offset_at(p, t.e)), last = uniform(offset_at(p, t.e + 1));
-    const int32_t mt = slot - (first / BM + t.e);
-    // A slot of a later group's numbering may lie past this one's rows.
-    t.empty = mt < 0 || mt >= (last - first + BM - 1) / BM;
-    t.row0 = t.empty ? 0 : first + mt * BM;
+    t.m0 = 0;
+    t.row0 = first + mt * BM;
     t.mvalid = uniform(last - t.row0 < BM ? last - t.row0 : BM);
     t.klen = p.k;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       t.a[h] = uniform(p.a[FORM == kGradX ? h : 0] + t.row0 * p.lda);
-      t.b[h] = uniform(p.b[h] + t.e * p.bstride + (FORM == kForward ? t.n0 * p.ldb : t.n0));
+      t.b[h] = uniform(p.b[h] + e * p.bstride + (FORM == kForward ? t.n0 * p.ldb : t.n0));
     }
     t.c = p.c[0] + t.row0 * p.ldc;
   }
   return t;
+}
+
+// The tile of a workgroup that computes one.  Workgroup i runs on XCD i % 8.
+// Each XCD takes blocks of bm x bn tiles, every eighth block, so that the tiles
+// that share operand rows at the same time share an L2.
+template <int BM, int NCOLS, int FORM>
+__device__ __forceinline__ Place place_tile(const ProductArgs &p) {
+  Place none;
+  none.empty = true;
+  const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+  const int size = p.bm * p.bn;
+  int block = at / size * 8 + xcd;
+  const int in = at % size;
+  const int down = (p.slots + p.bm - 1) / p.bm, across = (p.ntiles + p.bn - 1) / p.bn;
+  int e = 0;
+  if (FORM == kGradW) {
+    e = block / (down * across);
+    block -= e * (down * across);
+  }
+  const int slot = block / across * p.bm + in % p.bm;
+  const int nt = block % across * p.bn + in / p.bm;
+  if (slot >= p.slots || nt >= p.ntiles || e >= p.groups) return none;
+  if (FORM != kGradW) e = uniform(group_of_slot<BM>(p, slot));
+  const int32_t first = uniform(offset_at(p, e)), last = uniform(offset_at(p, e + 1));
+  int mt = slot;
+  if (FORM != kGradW) {
+    mt = slot - (first / BM + e);
+    // A slot of a later group's numbering may lie past this one's rows.
+    if (mt < 0 || mt >= (last - first + BM - 1) / BM) return none;
+  }
+  return place_at<BM, NCOLS, FORM>(p, e, first, last, mt, nt);
+}
+
+// The same for workgroups that fill a CU: the row tiles are counted, so that
+// the tiles come without gaps (workgroups that only exit would take turns on
+// the CUs and leave others two tiles to do: 512 rows in each of 16 groups, one
+// tile per CU, 185 -> 134 us).  Every wave counts by itself, 64 groups at a
+// time.  Tiles are ordered in bands of four row tiles, columns in turn, and
+// dealt to the XCDs in runs of p.bm.
+template <int BM, int NCOLS, int FORM>
+__device__ __forceinline__ Place place_counted(const ProductArgs &p) {
+  Place none;
+  none.empty = true;
+  const int lane = threadIdx.x & 63;
+  auto tiles_of = [&](int e, int &first, int &last) {
+    first = last = 0;
+    if (e < p.groups) {
+      first = offset_at(p, e);
+      last = offset_at(p, e + 1);
+    }
+    return last > first ? (last - first + BM - 1) / BM : 0;
+  };
+  int first, last, all = 0;
+  for (int e = lane; e < p.groups; e += 64) all += tiles_of(e, first, last);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) all += __shfl_xor(all, d, 64);
+  all = uniform(all);
+  const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3;
+  const int at = (turn / p.bm * 8 + xcd) * p.bm + turn % p.bm;
+  const int band = at / (4 * p.ntiles) * 4;
+  if (band >= all) return none;
+  const int high = all - band < 4 ? all - band : 4;
+  const int in = at - band * p.ntiles;
+  if (in >= high * p.ntiles) return none;
+  const int row = band + in % high, nt = in / high;
+  for (int base = 0, done = 0; base < p.groups; base += 64) {
+    const int n = tiles_of(base + lane, first, last);
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += v;
+    }
+    // The group whose tiles include this one: lanes below it end before.
+    const int l = __popcll(__ballot(done + upto <= row));
+    if (l < 64) {
+      const int mt = row - done - (uniform(__shfl(upto, l, 64)) - uniform(__shfl(n, l, 64)));
+      return place_at<BM, NCOLS, FORM>(p, base + l, uniform(__shfl(first, l, 64)), uniform(__shfl(last, l, 64)), mt, nt);
+    }
+    done += uniform(__shfl(upto, 63, 64));
+  }
+  return none;
 }
 
 // Stores a wave's part of the tile, at output columns wn and rows wm of it, the
@@ -763,15 +825,11 @@ __device__ __forceinline__ int dealt_row(int r, int h) {
 }
 
 template <int FORM, bool GATED>
-__global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
+__device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const Place &t, unsigned char *lds) {
   constexpr int REGION = 16384, BUFFER = 4 * REGION, NCOLS = GATED ? 128 : 256;
   constexpr bool A_COL = FORM == kGradW, B_COL = FORM != kForward;
-  __shared__ __align__(16) unsigned char lds[2 * BUFFER];
-
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
-  const Place t = place_tile<256, NCOLS, FORM>(p);
-  if (t.empty) return;
   const int klen = t.klen;
   const int per = (klen + kStep - 1) / kStep;
   const int steps = FORM == kGradX ? per * p.halves : per;
@@ -968,7 +1026,16 @@ __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
     RRB_BARRIER();
   }
 #undef RRB_BARRIER
-  finish_tile<FORM, GATED, true>(p, t, acc, wr * 64, 128, GATED ? wc * 32 : wc * 64, GATED ? nullptr : lds + wave * 16384);
+  finish_tile<FORM, GATED, true>(p, t, acc, wr * 64, 128, GATED ? wc * 32 : wc * 64,
+                                 GATED ? nullptr : lds + wave * 16384);
+}
+
+template <int FORM, bool GATED>
+__global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
+  __shared__ __align__(16) unsigned char lds[131072];
+  const Place t = FORM == kGradW ? place_tile<256, GATED ? 128 : 256, FORM>(p) : place_counted<256, GATED ? 128 : 256, FORM>(p);
+  if (t.empty) return;
+  product_turns_tile<FORM, GATED>(p, t, lds);
 }
 
 // ---- gradients before the activation -------------------------------------------
@@ -1074,15 +1141,34 @@ rrb_status launch_tiles(void (*kernel)(ProductArgs), int threads, ProductArgs p,
   p.ntiles = (p.n + cols - 1) / cols;
   const int64_t each = FORM == kGradW ? p.groups : 1;
   p.slots = FORM == kGradW ? (p.m + BM - 1) / BM * p.halves : static_cast<int32_t>(p.rows / BM) + p.groups;
-  // Blocks of 4 x 8 tiles (one per CU of an XCD) where there are enough of
-  // them to go round, single tiles otherwise.
-  const bool many = static_cast<int64_t>(p.slots) * p.ntiles * each >= 1024;
-  p.bm = many ? 4 : 1;
-  p.bn = many ? 8 : 1;
+  // Blocks of 4 x 8 tiles (one per CU of an XCD) where there are enough to go
+  // round, smaller ones for fewer tiles.
+  const int64_t tiles = static_cast<int64_t>(p.slots) * p.ntiles * each;
+  p.bm = tiles >= 512 ? 4 : tiles >= 128 ? 2 : 1;
+  p.bn = tiles >= 1024 ? 8 : tiles >= 256 ? 4 : tiles >= 128 ? 2 : 1;
   const int64_t blocks = static_cast<int64_t>((p.slots + p.bm - 1) / p.bm) * ((p.ntiles + p.bn - 1) / p.bn) * each;
   const int64_t grid = (blocks + 7) / 8 * 8 * p.bm * p.bn;
   if (grid > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, p);
+  return launched("expert product");
+}
+
+// Launches the form over 256 x 256 tiles, one workgroup per tile and CU.
+template <int FORM, bool GATED>
+rrb_status launch_turns(ProductArgs p, hipStream_t s) {
+  if (FORM == kGradW)
+    return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED>, 512, p, s);
+  constexpr int cols = GATED ? 128 : 256;
+  p.ntiles = (p.n + cols - 1) / cols;
+  // Row tiles at most (each group can add a partial one, but no more than rows).
+  const int64_t rows = p.rows / 256 + (p.groups < p.rows ? p.groups : p.rows);
+  const int64_t tiles = rows * p.ntiles;
+  // Runs of 32 tiles (an XCD's CUs) where there are many, shorter ones so that
+  // few tiles spread over the XCDs.
+  p.bm = tiles >= 4096 ? 32 : tiles >= 1024 ? 16 : tiles >= 256 ? 8 : 1;
+  const int64_t grid = (tiles + 8 * p.bm - 1) / (8 * p.bm) * (8 * p.bm);
+  if (grid > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
+  hipLaunchKernelGGL((product_turns_kernel<FORM, GATED>), dim3(static_cast<unsigned>(grid)), dim3(512), 0, s, p);
   return launched("expert product");
 }
 
@@ -1108,7 +1194,7 @@ rrb_status launch_product(const ProductArgs &p, hipStream_t s) {
       T(12, 256, 128, 4, 2, 3)
     }
   }
-  return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED>, 512, p, s);
+  return launch_turns<FORM, GATED>(p, s);
 }
 
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
