@@ -13,10 +13,11 @@
 // contiguous in memory.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <initializer_list>
 #include <type_traits>
-#include <cstdlib>
 
 #include "rrb_internal.h"
 #include "rrb_kernels.h"
@@ -29,7 +30,7 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
-// Groups that one wave's two ballots can search.
+// Groups that a wave counts, 64 at a time, before it starts on its tile.
 constexpr int kMaxGroups = 4096;
 // Row widths whose tile offsets fit 32 bits.
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
@@ -119,7 +120,7 @@ struct ProductArgs {
   int64_t bstride;        // kForward, kGradX: weight elements per group (kGradW: dW's)
   int32_t groups;
   int32_t m, n, k;        // m: kGradW only; k: kForward, kGradX only
-  int32_t slots;          // kForward, kGradX: row-tile slots; kGradW: m tiles of both outputs
+  int32_t mtiles;         // kGradW: m tiles of both outputs
   int32_t ntiles;
   int32_t bm, bn;         // tiles of one XCD's block: bm slots x bn column tiles, or bm in a row
   int32_t halves;         // kGradX: phases; kGradW: outputs
@@ -133,27 +134,6 @@ __device__ __forceinline__ int32_t offset_at(const ProductArgs &p, int e) {
   if (!p.offsets) return e == 0 ? 0 : p.rows;
   const int32_t v = p.offsets[e];
   return v < 0 ? 0 : v > p.rows ? p.rows : v;
-}
-
-// Row tiles are numbered without knowing the group sizes on the host: group
-// e's tiles start at slot floor(offsets[e] / BM) + e, which leaves each group
-// room for its ceil(rows / BM) tiles, so rows / BM + groups slots hold any
-// grouping; a slot without a tile exits.  The group of a slot is the last one
-// that starts at or before it: two steps of a 64-way search by ballot, with
-// no map to build beforehand.
-template <int BM>
-__device__ __forceinline__ int group_of_slot(const ProductArgs &p, int slot) {
-  const int lane = threadIdx.x & 63;
-  const int stride = (p.groups + 63) >> 6;
-  const int e0 = lane * stride;
-  const bool at0 = e0 < p.groups && offset_at(p, e0) / BM + e0 <= slot;
-  const int block = __popcll(__ballot(at0)) - 1;
-  if (stride == 1) return block < 0 ? 0 : block;
-  const int first = (block < 0 ? 0 : block) * stride;
-  const int e1 = first + lane;
-  const bool at1 = lane < stride && e1 < p.groups && offset_at(p, e1) / BM + e1 <= slot;
-  const int in = __popcll(__ballot(at1)) - 1;
-  return first + (in < 0 ? 0 : in);
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -175,7 +155,12 @@ __device__ __forceinline__ const uint16_t *uniform(const uint16_t *q) {
 constexpr int kStep = 64;
 
 __device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
-__device__ __forceinline__ int col_swizzle(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+template <int COLS>
+__device__ __forceinline__ int col_swizzle(int k) {
+  // 64 columns are four slots, and two rows span the banks.
+  if (COLS == 64) return ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+  return (k & 3) | ((k >> 3) & 1) << 2;
+}
 
 // Fragment of 16 rows x 32 k from a row tile: lane l holds row l % 16, k =
 // 8 (l / 16) .. + 7.
@@ -192,7 +177,7 @@ template <int COLS>
 __device__ __forceinline__ bf16x8_t col_fragment(const unsigned char *tile, int col, int kk) {
   const int lane = threadIdx.x & 63;
   const int k = kk * 32 + (lane >> 4) * 8 + ((lane >> 2) & 3);
-  const int at = k * (COLS * 2) + (((col >> 4) ^ col_swizzle(k)) << 5) + (lane & 3) * 8;
+  const int at = k * (COLS * 2) + (((col >> 4) ^ col_swizzle<COLS>(k)) << 5) + (lane & 3) * 8;
   typedef __attribute__((address_space(3))) s16x4_t *lds_ptr;
   const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at));
   const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at + 4 * COLS * 2));
@@ -380,7 +365,7 @@ __device__ __forceinline__ Place place_at(const ProductArgs &p, int e, int first
   t.n0 = nt * NCOLS;
   t.empty = false;
   if (FORM == kGradW) {
-    const int tiles = p.slots / p.halves;
+    const int tiles = p.mtiles / p.halves;
     const int half = mt / tiles;
     t.row0 = 0;
     t.m0 = (mt - half * tiles) * BM;
@@ -404,43 +389,33 @@ __device__ __forceinline__ Place place_at(const ProductArgs &p, int e, int first
   return t;
 }
 
-// The tile of a workgroup that computes one.  Workgroup i runs on XCD i % 8.
-// Each XCD takes blocks of bm x bn tiles, every eighth block, so that the tiles
-// that share operand rows at the same time share an L2.
-template <int BM, int NCOLS, int FORM>
-__device__ __forceinline__ Place place_tile(const ProductArgs &p) {
+// Workgroup i runs on XCD i % 8.  A weight gradient's tiles: every group has
+// the same ones, and each XCD takes blocks of bm x bn of them, every eighth
+// block, so that tiles that share operand rows at the same time share an L2.
+template <int BM, int NCOLS>
+__device__ __forceinline__ Place place_weight(const ProductArgs &p) {
   Place none;
   none.empty = true;
   const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
   const int size = p.bm * p.bn;
   int block = at / size * 8 + xcd;
   const int in = at % size;
-  const int down = (p.slots + p.bm - 1) / p.bm, across = (p.ntiles + p.bn - 1) / p.bn;
-  int e = 0;
-  if (FORM == kGradW) {
-    e = block / (down * across);
-    block -= e * (down * across);
-  }
-  const int slot = block / across * p.bm + in % p.bm;
+  const int down = (p.mtiles + p.bm - 1) / p.bm, across = (p.ntiles + p.bn - 1) / p.bn;
+  const int e = block / (down * across);
+  block -= e * (down * across);
+  const int mt = block / across * p.bm + in % p.bm;
   const int nt = block % across * p.bn + in / p.bm;
-  if (slot >= p.slots || nt >= p.ntiles || e >= p.groups) return none;
-  if (FORM != kGradW) e = uniform(group_of_slot<BM>(p, slot));
-  const int32_t first = uniform(offset_at(p, e)), last = uniform(offset_at(p, e + 1));
-  int mt = slot;
-  if (FORM != kGradW) {
-    mt = slot - (first / BM + e);
-    // A slot of a later group's numbering may lie past this one's rows.
-    if (mt < 0 || mt >= (last - first + BM - 1) / BM) return none;
-  }
-  return place_at<BM, NCOLS, FORM>(p, e, first, last, mt, nt);
+  if (mt >= p.mtiles || nt >= p.ntiles || e >= p.groups) return none;
+  return place_at<BM, NCOLS, kGradW>(p, e, uniform(offset_at(p, e)), uniform(offset_at(p, e + 1)), mt, nt);
 }
 
-// The same for workgroups that fill a CU: the row tiles are counted, so that
-// the tiles come without gaps (workgroups that only exit would take turns on
-// the CUs and leave others two tiles to do: 512 rows in each of 16 groups, one
-// tile per CU, 185 -> 134 us).  Every wave counts by itself, 64 groups at a
-// time.  Tiles are ordered in bands of four row tiles, columns in turn, and
-// dealt to the XCDs in runs of p.bm.
+// The other forms' tiles.  How many row tiles a group has is known on the
+// device alone: they are counted, so that the tiles come without gaps (with
+// workgroups that only exit between them, taking their turns on the CUs, other
+// CUs got two tiles to do: 512 rows in each of 16 groups, one tile per CU, 185
+// -> 105 us).  Every wave counts by itself, 64 groups at a time.  Tiles are
+// ordered in bands of four row tiles, columns in turn, and dealt to the XCDs in
+// runs of p.bm.
 template <int BM, int NCOLS, int FORM>
 __device__ __forceinline__ Place place_counted(const ProductArgs &p) {
   Place none;
@@ -484,6 +459,12 @@ __device__ __forceinline__ Place place_counted(const ProductArgs &p) {
     done += uniform(__shfl(upto, 63, 64));
   }
   return none;
+}
+
+template <int BM, int NCOLS, int FORM>
+__device__ __forceinline__ Place place_tile(const ProductArgs &p) {
+  if (FORM == kGradW) return place_weight<BM, NCOLS>(p);
+  return place_counted<BM, NCOLS, FORM>(p);
 }
 
 // Stores a wave's part of the tile, at output columns wn and rows wm of it, the
@@ -564,7 +545,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
       const int id = i * NT + tid;
       if (A_COL) {
         const int kr = id / (BM / 8), pos = id % (BM / 8);
-        const int ch = pos ^ (col_swizzle(kr) << 1);
+        const int ch = pos ^ (col_swizzle<BM>(kr) << 1);
         ra[i] = load_chunk(t.a[0] + (k0 + kr) * p.lda + ch * 8, k0 + kr < klen ? p.m - t.m0 - ch * 8 : 0);
       } else {
         const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
@@ -577,7 +558,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
       const int id = i * NT + tid;
       if (B_COL) {
         const int kr = id / (BN / 8), pos = id % (BN / 8);
-        const int ch = pos ^ (col_swizzle(kr) << 1);
+        const int ch = pos ^ (col_swizzle<BN>(kr) << 1);
         rb[i] = load_chunk(t.b[h] + (k0 + kr) * p.ldb + ch * 8, k0 + kr < klen ? p.n - t.n0 - ch * 8 : 0);
       } else {
         const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
@@ -685,7 +666,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
     const int id = i * NT + tid;
     if (A_COL) {
       const int kr = id / (BM / 8), pos = id % (BM / 8);
-      va[i] = kr * lda2 + (pos ^ (col_swizzle(kr) << 1)) * 16;
+      va[i] = kr * lda2 + (pos ^ (col_swizzle<BM>(kr) << 1)) * 16;
     } else {
       const int r = id >> 3;
       va[i] = (r < t.mvalid ? r : t.mvalid - 1) * lda2 + ((id & 7) ^ row_swizzle(r)) * 16;
@@ -696,7 +677,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
     const int id = i * NT + tid;
     if (B_COL) {
       const int kr = id / (BN / 8), pos = id % (BN / 8);
-      vb[i] = kr * ldb2 + (pos ^ (col_swizzle(kr) << 1)) * 16;
+      vb[i] = kr * ldb2 + (pos ^ (col_swizzle<BN>(kr) << 1)) * 16;
     } else {
       const int r = id >> 3;
       const int n = GATED ? gated_row(r) : r;
@@ -792,7 +773,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 
 // ---- the tiled product, two wave groups by turns -----------------------------------
 //
-// 256 x 256 tiles for products that are bound by the matrix cores.  Eight waves
+// 256 x 256 tiles, for products that are bound by the matrix cores.  Eight waves
 // (2 x 4, 128 x 64 outputs each) in two groups of one wave per SIMD: while one
 // group issues 16 matrix instructions (a quarter of its step) the other reads
 // fragments and starts loads, so a SIMD's matrix core and the LDS work at the
@@ -843,7 +824,7 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int id = i * 512 + tid;
-      const int kr = id >> 4, c = (id & 15) ^ (col_swizzle(kr) << 1);
+      const int kr = id >> 4, c = (id & 15) ^ (col_swizzle<128>(kr) << 1);
       const int r = id >> 3;
       if (A_COL) {
         va[h][i] = kr * lda2 + (h * 128 + c * 8) * 2;
@@ -909,7 +890,7 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
   if (A_COL) {
     const int k = (lane >> 4) * 8 + ((lane >> 2) & 3);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fa_at[i] = k * 256 + (((wr * 4 + i) ^ col_swizzle(k)) << 5) + (lane & 3) * 8;
+    for (int i = 0; i < 4; ++i) fa_at[i] = k * 256 + (((wr * 4 + i) ^ col_swizzle<128>(k)) << 5) + (lane & 3) * 8;
   } else {
     const int r = wr * 64 + (lane & 15);
 #pragma unroll
@@ -918,7 +899,7 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
   if (B_COL) {
     const int k = (lane >> 4) * 8 + ((lane >> 2) & 3);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) fb_at[j] = k * 256 + (((wc * 2 + j) ^ col_swizzle(k)) << 5) + (lane & 3) * 8;
+    for (int j = 0; j < 2; ++j) fb_at[j] = k * 256 + (((wc * 2 + j) ^ col_swizzle<128>(k)) << 5) + (lane & 3) * 8;
   } else {
     const int r = wc * 32 + (lane & 15);
 #pragma unroll
@@ -1033,7 +1014,7 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
 template <int FORM, bool GATED>
 __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
   __shared__ __align__(16) unsigned char lds[131072];
-  const Place t = FORM == kGradW ? place_tile<256, GATED ? 128 : 256, FORM>(p) : place_counted<256, GATED ? 128 : 256, FORM>(p);
+  const Place t = place_tile<256, GATED ? 128 : 256, FORM>(p);
   if (t.empty) return;
   product_turns_tile<FORM, GATED>(p, t, lds);
 }
@@ -1134,67 +1115,97 @@ rrb_status launched(const char *what) {
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// Row tiles that the groups' rows can make at most: each group that has rows
+// adds at most one partial tile.
+int64_t most_row_tiles(const ProductArgs &p, int bm) {
+  return p.rows / bm + (p.groups < p.rows ? p.groups : p.rows);
+}
+
 // Launches the form over BM x BN tiles with the given kernel.
 template <int BM, int BN, int FORM, bool GATED>
 rrb_status launch_tiles(void (*kernel)(ProductArgs), int threads, ProductArgs p, hipStream_t s) {
   constexpr int cols = GATED ? BN / 2 : BN;
   p.ntiles = (p.n + cols - 1) / cols;
-  const int64_t each = FORM == kGradW ? p.groups : 1;
-  p.slots = FORM == kGradW ? (p.m + BM - 1) / BM * p.halves : static_cast<int32_t>(p.rows / BM) + p.groups;
-  // Blocks of 4 x 8 tiles (one per CU of an XCD) where there are enough to go
-  // round, smaller ones for fewer tiles.
-  const int64_t tiles = static_cast<int64_t>(p.slots) * p.ntiles * each;
-  p.bm = tiles >= 512 ? 4 : tiles >= 128 ? 2 : 1;
-  p.bn = tiles >= 1024 ? 8 : tiles >= 256 ? 4 : tiles >= 128 ? 2 : 1;
-  const int64_t blocks = static_cast<int64_t>((p.slots + p.bm - 1) / p.bm) * ((p.ntiles + p.bn - 1) / p.bn) * each;
-  const int64_t grid = (blocks + 7) / 8 * 8 * p.bm * p.bn;
+  int64_t grid;
+  if (FORM == kGradW) {
+    p.mtiles = (p.m + BM - 1) / BM * p.halves;
+    // Blocks of 4 x 8 tiles (one per CU of an XCD) where there are enough to
+    // go round, smaller ones for fewer tiles.
+    const int64_t tiles = static_cast<int64_t>(p.mtiles) * p.ntiles * p.groups;
+    p.bm = tiles >= 512 ? 4 : tiles >= 128 ? 2 : 1;
+    p.bn = tiles >= 1024 ? 8 : tiles >= 256 ? 4 : tiles >= 128 ? 2 : 1;
+    const int64_t blocks =
+        static_cast<int64_t>((p.mtiles + p.bm - 1) / p.bm) * ((p.ntiles + p.bn - 1) / p.bn) * p.groups;
+    grid = (blocks + 7) / 8 * 8 * p.bm * p.bn;
+  } else {
+    // Runs of 32 tiles (an XCD's CUs) where there are many, shorter ones so
+    // that few tiles spread over the XCDs.
+    const int64_t tiles = most_row_tiles(p, BM) * p.ntiles;
+    p.bm = tiles >= 4096 ? 32 : tiles >= 1024 ? 16 : tiles >= 256 ? 8 : 1;
+    grid = (tiles + 8 * p.bm - 1) / (8 * p.bm) * (8 * p.bm);
+  }
   if (grid > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, p);
   return launched("expert product");
 }
 
-// Launches the form over 256 x 256 tiles, one workgroup per tile and CU.
+// Estimated time (us) of the form over BM x BN tiles, `resident` of them per CU
+// at a time: rounds of tiles of so many steps, `step` each, and `rest` per tile
+// (first loads, results); no less than moving the operands from the L2s takes
+// at 10 TB/s, nor than moving the weights (or their gradients) from or to HBM
+// at 5.5 TB/s.  The rates are measured; what counts is which
+// shape comes out first.
 template <int FORM, bool GATED>
-rrb_status launch_turns(ProductArgs p, hipStream_t s) {
-  if (FORM == kGradW)
-    return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED>, 512, p, s);
-  constexpr int cols = GATED ? 128 : 256;
-  p.ntiles = (p.n + cols - 1) / cols;
-  // Row tiles at most (each group can add a partial one, but no more than rows).
-  const int64_t rows = p.rows / 256 + (p.groups < p.rows ? p.groups : p.rows);
-  const int64_t tiles = rows * p.ntiles;
-  // Runs of 32 tiles (an XCD's CUs) where there are many, shorter ones so that
-  // few tiles spread over the XCDs.
-  p.bm = tiles >= 4096 ? 32 : tiles >= 1024 ? 16 : tiles >= 256 ? 8 : 1;
-  const int64_t grid = (tiles + 8 * p.bm - 1) / (8 * p.bm) * (8 * p.bm);
-  if (grid > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
-  hipLaunchKernelGGL((product_turns_kernel<FORM, GATED>), dim3(static_cast<unsigned>(grid)), dim3(512), 0, s, p);
-  return launched("expert product");
+double estimate(const ProductArgs &p, int bm, int bn, int resident, double step, double rest) {
+  constexpr double kCus = 256;
+  const double live = p.groups < p.rows ? p.groups : p.rows;
+  const int cols = GATED ? bn / 2 : bn;
+  const double across = (p.n + cols - 1) / cols;
+  const double weights = 2.0 * p.n * (GATED ? 2 : 1) * p.halves * (FORM == kGradW ? p.groups : live) *
+                         (FORM == kGradW ? p.m : p.k);
+  double down, steps, moved;
+  if (FORM == kGradW) {
+    down = static_cast<double>((p.m + bm - 1) / bm) * p.halves * p.groups;
+    steps = live > 0 ? p.rows / live / kStep : 0;
+    moved = down * across * steps * (bm + bn);
+  } else {
+    down = static_cast<double>(p.rows) / bm + live / 2;
+    if (down < live) down = live;
+    steps = static_cast<double>((p.k + kStep - 1) / kStep) * (FORM == kGradX ? p.halves : 1);
+    moved = across * steps * (down * bn + p.rows);
+  }
+  const double rounds = down * across / (kCus * resident);
+  // Rounds that are not whole: about half a one more where tiles come and go
+  // by themselves, up to a whole one where one fills a CU.
+  const double more = rounds <= 1 ? 1 : rounds + 0.5;
+  const double whole = rounds <= 1 ? 1 : (resident > 1 ? more : std::ceil(rounds)) / rounds;
+  const double matrix = more * (steps * step + rest);
+  return std::max(matrix, std::max(moved * kStep * 2 / 10e6, weights / 5.5e6 * whole));
 }
 
+// Three tile shapes.  256 x 256 is the fastest by far where there are enough
+// tiles to fill the CUs (1.3 PFLOP/s; 64 x 256 reaches 0.7, 64 x 64 0.5), but
+// few tiles leave CUs idle, and few rows leave a tile empty.  Measured (us;
+// 256 x 256, 64 x 256, 64 x 64), products of `rows` in each of G groups:
+//   G 1, 1 row, 4096 x 4096: 61, 41, 20     G 16, 64, 4096 x 2048: 74, 58, 79
+//   G 1, 512, 8192 x 1024: 147, 76, 37      G 1, 2048, 4096 x 2048: 85, 50, 57
+//   G 32, 1, 7168 x 2048: 158, 155, 152     G 8, 512, 2048 x 2048: 57, 69, 63
+//   G 2, 1024, 4096 x 4096: 94, 132, 121    G 32, 160, 2048 x 1024: 46, 51, 51
 template <int FORM, bool GATED>
 rrb_status launch_product(const ProductArgs &p, hipStream_t s) {
   bool direct = p.lda % 8 == 0 && p.ldb % 8 == 0;
   for (int h = 0; h < 2; ++h) direct = direct && aligned(p.a[h], 16) && aligned(p.b[h], 16);
   if (!direct) return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
-  if (const char *v = getenv("RRB_T")) {
-    switch (atoi(v)) {
-#define T(i, M, N, R, C, S) case i: return launch_tiles<M, N, FORM, GATED>(product_direct_kernel<M, N, R, C, S, FORM, GATED>, R * C * 64, p, s);
-      T(1, 128, 128, 2, 2, 2)
-      T(2, 32, 64, 1, 2, 4)
-      T(3, 32, 128, 1, 4, 4)
-      T(4, 32, 128, 1, 4, 3)
-      T(5, 64, 128, 1, 4, 2)
-      T(6, 64, 128, 1, 4, 3)
-      T(7, 128, 128, 2, 2, 4)
-      T(8, 128, 256, 2, 4, 2)
-      T(9, 128, 256, 2, 4, 3)
-      T(10, 64, 256, 1, 4, 3)
-      T(11, 64, 256, 2, 4, 3)
-      T(12, 256, 128, 4, 2, 3)
-    }
-  }
-  return launch_turns<FORM, GATED>(p, s);
+  // A tile of at most 128 valid rows takes about half a 256-row step.
+  const bool half = FORM != kGradW && static_cast<int64_t>(p.groups) * 128 >= p.rows;
+  const double big = estimate<FORM, GATED>(p, 256, 256, 1, half ? 0.9 : 1.55, 8);
+  const double mid = estimate<FORM, GATED>(p, 64, 256, 1, 0.66, 4);
+  const double low = estimate<FORM, GATED>(p, 64, 64, 2, 0.42, 2);
+  if (big <= mid && big <= low)
+    return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED>, 512, p, s);
+  if (mid <= low)
+    return launch_tiles<64, 256, FORM, GATED>(product_direct_kernel<64, 256, 2, 4, 3, FORM, GATED>, 512, p, s);
+  return launch_tiles<64, 64, FORM, GATED>(product_direct_kernel<64, 64, 2, 2, 5, FORM, GATED>, 256, p, s);
 }
 
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
