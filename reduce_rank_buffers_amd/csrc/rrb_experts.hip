@@ -240,108 +240,107 @@ __device__ __forceinline__ void store_cols(uint16_t *dst, int have, bool whole, 
 // consecutive columns of each 16 x 16 block: 4 (l / 16) .. + 3, or, where two
 // blocks were dealt together (WIDE), the first or second half of eight at
 // 8 (l / 16).  Gated: blocks are gate and up by turns.
-// `whole`: rows start on 8-byte boundaries and all of the wave's columns exist.
-// `stage` (not gated; 64 columns, rows on 16-byte boundaries): 16 KiB of LDS of
-// the wave's own, through which results leave as whole 128-byte lines instead
-// of 32- or 64-byte pieces: a row of 64 columns is eight 16-byte chunks, stored
-// at chunk ^ row / 2 % 8, so that neither side meets its own banks.
-// The second FM / 2 blocks of rows begin `half` rows behind the first.
+// The second half of a wave's blocks of rows begins `down` rows behind the first
+// block, and of columns `right` columns.  `whole`: rows start on 8-byte
+// boundaries and all of the wave's columns exist.  `stage` (256 x 256 tiles, not
+// gated, rows on 16-byte boundaries): 128 KiB of LDS through which results
+// leave as whole rows of the tile instead of 32- or 64-byte pieces (a weight
+// gradient's 268 MB of zeros: 77 -> 56 us); 16-byte chunk c of row r is kept
+// at c ^ r % 16, so that neither side meets its own banks.
+struct Spot {
+  int m, n;         // the wave's first row and output column in the tile
+  int down, right;
+};
+
 template <int ACT, bool GATED, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (&acc)[FM][FN], uint16_t *c,
                                            uint16_t *save0, uint16_t *save1, const uint16_t *bias,
-                                           const uint16_t *residual, int m0, int half, int mvalid, int n0, bool whole,
+                                           const uint16_t *residual, Spot spot, int mvalid, int n0, bool whole,
                                            unsigned char *stage) {
-  constexpr int W = WIDE ? 8 : 4;                       // consecutive columns per lane
+  constexpr int W = WIDE ? 8 : 4;                           // consecutive columns per lane
   constexpr int BLOCKS = (GATED ? 2 : 1) * (WIDE ? 2 : 1);  // blocks that make them
   const int lane = threadIdx.x & 63;
+  auto row_at = [&](int i) { return spot.m + (i >= FM / 2 ? spot.down + (i - FM / 2) * 16 : i * 16) + (lane & 15); };
+  auto col_at = [&](int j) {
+    const int g = j / BLOCKS, halves = FN / BLOCKS / 2;
+    return spot.n + (halves && g >= halves ? spot.right + (g - halves) * W * 4 : g * W * 4) + (lane >> 4) * W;
+  };
   // To `to` directly, or into the stage.
-  auto put = [&](uint16_t *to, int64_t at, int i, int j, int have, const float (&v)[W]) {
+  auto put = [&](uint16_t *to, int m, int n, const float (&v)[W]) {
     if (!GATED && stage) {
-      const int r = i * 16 + (lane & 15);
-      const int col = j * 16 + (lane >> 4) * W;
-      unsigned char *q = stage + r * 128 + ((col >> 3) ^ row_swizzle(r)) * 16 + (col & 7) * 2;
+      unsigned char *q = stage + m * 512 + ((n >> 3) ^ (m & 15)) * 16 + (n & 7) * 2;
       *reinterpret_cast<uint2 *>(q) = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
       if (W == 8)
         *reinterpret_cast<uint2 *>(q + 8) = make_uint2(cvt_pk_bf16(v[W - 4], v[W - 3]), cvt_pk_bf16(v[W - 2], v[W - 1]));
-    } else if (have > 0) {
-      store_cols<W>(to + at, have, whole, v);
+    } else {
+      store_cols<W>(to + m * p.ldc + n0 + n, p.n - n0 - n, whole, v);
     }
   };
-  // The staged tile to `to`.
+  // The staged tile to `to`, 32 rows per wave.
   auto flush = [&](uint16_t *to) {
     if (GATED || !stage) return;
-    const int n = n0 + (lane & 7) * 8;
+    __syncthreads();
+    const int n = n0 + (lane & 31) * 8;
 #pragma unroll
-    for (int b = 0; b < FM * 2; ++b) {
-      const int r = b * 8 + (lane >> 3);
-      const int m = m0 + (r >= FM * 8 ? half + r - FM * 8 : r);
-      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(stage + r * 128 + ((lane & 7) ^ row_swizzle(r)) * 16);
+    for (int b = 0; b < 16; ++b) {
+      const int m = (threadIdx.x >> 6) * 32 + b * 2 + (lane >> 5);
+      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(stage + m * 512 + ((lane & 31) ^ (m & 15)) * 16);
       if (m < mvalid && n < p.n) *reinterpret_cast<u32x4_t *>(to + m * p.ldc + n) = v;
     }
+    __syncthreads();
   };
-  if (!GATED && save0 && stage) {
-    // The pre-activation first: the stage holds one output at a time.
+  // Staged, the pre-activation goes first: the stage holds one output at a
+  // time.
+  const bool ahead = !GATED && save0 && stage;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 0 && !ahead) continue;
 #pragma unroll
     for (int j = 0; j < FN; j += BLOCKS) {
-      const int n = n0 + j / BLOCKS * W * 4 + (lane >> 4) * W;
+      const int n = col_at(j), have = p.n - n0 - n;
+      if (have <= 0) continue;
       float b[W];
-      if (bias) load_cols<W>(bias + n, p.n - n, whole, b);
+      if (!GATED && bias) load_cols<W>(bias + n0 + n, have, whole, b);
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
+        const int m = row_at(i);
+        if (m >= mvalid) continue;
         float v[W];
+        if (GATED) {
+          float u[W];
 #pragma unroll
-        for (int q = 0; q < W; ++q) v[q] = acc[i][j + (q >> 2)][q & 3] + (bias ? b[q] : 0.f);
-        put(nullptr, 0, i, j, 0, v);
+          for (int q = 0; q < W; ++q) {
+            v[q] = acc[i][j + (q >> 2) * 2][q & 3];
+            u[q] = acc[i][j + (q >> 2) * 2 + (GATED ? 1 : 0)][q & 3];
+          }
+          if (save0) {
+            put(save0, m, n, v);
+            put(save1, m, n, u);
+          }
+#pragma unroll
+          for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]) * u[q];
+        } else {
+#pragma unroll
+          for (int q = 0; q < W; ++q) v[q] = acc[i][j + (q >> 2)][q & 3] + (bias ? b[q] : 0.f);
+          if (pass == 0) {
+            put(save0, m, n, v);
+            continue;
+          }
+          if (save0 && !ahead) put(save0, m, n, v);
+#pragma unroll
+          for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]);
+          if (residual) {
+            float r[W];
+            load_cols<W>(residual + m * p.ldc + n0 + n, have, whole, r);
+#pragma unroll
+            for (int q = 0; q < W; ++q) v[q] += r[q];
+          }
+        }
+        put(c, m, n, v);
       }
     }
-    flush(save0);
+    flush(pass == 0 ? save0 : c);
   }
-#pragma unroll
-  for (int j = 0; j < FN; j += BLOCKS) {
-    const int n = n0 + j / BLOCKS * W * 4 + (lane >> 4) * W;
-    const int have = p.n - n;
-    float b[W];
-    if (!GATED && bias && have > 0) load_cols<W>(bias + n, have, whole, b);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int m = m0 + (i >= FM / 2 ? half + (i - FM / 2) * 16 : i * 16) + (lane & 15);
-      if (m >= mvalid || (have <= 0 && !stage)) continue;
-      const int64_t at = m * p.ldc + n;
-      float v[W];
-      if (GATED) {
-        float u[W];
-#pragma unroll
-        for (int q = 0; q < W; ++q) {
-          v[q] = acc[i][j + (q >> 2) * 2][q & 3];
-          u[q] = acc[i][j + (q >> 2) * 2 + (GATED ? 1 : 0)][q & 3];
-        }
-        if (save0) {
-          store_cols<W>(save0 + at, have, whole, v);
-          store_cols<W>(save1 + at, have, whole, u);
-        }
-#pragma unroll
-        for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]) * u[q];
-      } else {
-#pragma unroll
-        for (int q = 0; q < W; ++q) v[q] = acc[i][j + (q >> 2)][q & 3];
-        if (bias) {
-#pragma unroll
-          for (int q = 0; q < W; ++q) v[q] += b[q];
-        }
-        if (save0 && !stage) store_cols<W>(save0 + at, have, whole, v);
-#pragma unroll
-        for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]);
-        if (residual) {
-          float r[W];
-          load_cols<W>(residual + at, have, whole, r);
-#pragma unroll
-          for (int q = 0; q < W; ++q) v[q] += r[q];
-        }
-      }
-      put(c, at, i, j, have, v);
-    }
-  }
-  flush(c);
 }
 
 // ---- the tiled product ------------------------------------------------------------
@@ -413,26 +412,42 @@ __device__ __forceinline__ Place place_weight(const ProductArgs &p) {
 // device alone: they are counted, so that the tiles come without gaps (with
 // workgroups that only exit between them, taking their turns on the CUs, other
 // CUs got two tiles to do: 512 rows in each of 16 groups, one tile per CU, 185
-// -> 105 us).  Every wave counts by itself, 64 groups at a time.  Tiles are
-// ordered in bands of four row tiles, columns in turn, and dealt to the XCDs in
-// runs of p.bm.
-template <int BM, int NCOLS, int FORM>
+// -> 105 us).  Every wave counts by itself, 64 groups at a time.  LIGHT: tiles
+// of at most so many rows cost half of a whole one and come last, where they
+// fill the CUs that the whole ones leave (304 tiles of 112 steps on 256 CUs,
+// two fifths of them light: 351 -> 250 us).  Tiles are ordered in bands of four
+// row tiles, columns in turn, and dealt to the XCDs in runs of p.bm.
+template <int BM, int NCOLS, int LIGHT, int FORM>
 __device__ __forceinline__ Place place_counted(const ProductArgs &p) {
   Place none;
   none.empty = true;
   const int lane = threadIdx.x & 63;
-  auto tiles_of = [&](int e, int &first, int &last) {
-    first = last = 0;
-    if (e < p.groups) {
-      first = offset_at(p, e);
-      last = offset_at(p, e + 1);
-    }
-    return last > first ? (last - first + BM - 1) / BM : 0;
+  struct Group {
+    int first, last, whole, all;  // rows; tiles that are not light, and all
   };
-  int first, last, all = 0;
-  for (int e = lane; e < p.groups; e += 64) all += tiles_of(e, first, last);
+  auto group = [&](int e) {
+    Group g = {0, 0, 0, 0};
+    if (e < p.groups) {
+      g.first = offset_at(p, e);
+      g.last = offset_at(p, e + 1);
+      const int n = g.last > g.first ? g.last - g.first : 0;
+      g.all = (n + BM - 1) / BM;
+      g.whole = n == 0 ? 0 : (n - 1) / BM + ((n - 1) % BM >= LIGHT ? 1 : 0);
+    }
+    return g;
+  };
+  int whole = 0, all = 0;
+  for (int e = lane; e < p.groups; e += 64) {
+    const Group g = group(e);
+    whole += g.whole;
+    all += g.all;
+  }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) all += __shfl_xor(all, d, 64);
+  for (int d = 32; d; d >>= 1) {
+    whole += __shfl_xor(whole, d, 64);
+    all += __shfl_xor(all, d, 64);
+  }
+  whole = uniform(whole);
   all = uniform(all);
   const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3;
   const int at = (turn / p.bm * 8 + xcd) * p.bm + turn % p.bm;
@@ -441,42 +456,46 @@ __device__ __forceinline__ Place place_counted(const ProductArgs &p) {
   const int high = all - band < 4 ? all - band : 4;
   const int in = at - band * p.ntiles;
   if (in >= high * p.ntiles) return none;
-  const int row = band + in % high, nt = in / high;
+  int row = band + in % high;
+  const int nt = in / high;
+  const bool light = row >= whole;
+  if (light) row -= whole;
   for (int base = 0, done = 0; base < p.groups; base += 64) {
-    const int n = tiles_of(base + lane, first, last);
+    const Group g = group(base + lane);
+    const int n = light ? g.all - g.whole : g.whole;
     int upto = n;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(upto, d, 64);
       if (lane >= d) upto += v;
     }
-    // The group whose tiles include this one: lanes below it end before.
+    // The group whose tiles include this one: those below it end before.
     const int l = __popcll(__ballot(done + upto <= row));
     if (l < 64) {
-      const int mt = row - done - (uniform(__shfl(upto, l, 64)) - uniform(__shfl(n, l, 64)));
-      return place_at<BM, NCOLS, FORM>(p, base + l, uniform(__shfl(first, l, 64)), uniform(__shfl(last, l, 64)), mt, nt);
+      const int before = done + __shfl(upto - n, l, 64);
+      const int mt = row - before + (light ? __shfl(g.whole, l, 64) : 0);
+      return place_at<BM, NCOLS, FORM>(p, base + l, uniform(__shfl(g.first, l, 64)), uniform(__shfl(g.last, l, 64)),
+                                       uniform(mt), nt);
     }
     done += uniform(__shfl(upto, 63, 64));
   }
   return none;
 }
 
-template <int BM, int NCOLS, int FORM>
+template <int BM, int NCOLS, int LIGHT, int FORM>
 __device__ __forceinline__ Place place_tile(const ProductArgs &p) {
   if (FORM == kGradW) return place_weight<BM, NCOLS>(p);
-  return place_counted<BM, NCOLS, FORM>(p);
+  return place_counted<BM, NCOLS, LIGHT, FORM>(p);
 }
 
-// Stores a wave's part of the tile, at output columns wn and rows wm of it, the
-// second half of these `half` rows on.  DEALT: row regions were dealt for eight
+// Stores a wave's part of the tile.  DEALT: row regions were dealt for eight
 // columns per lane.
 template <int FORM, bool GATED, bool DEALT, int FM, int FN>
-__device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t, const f32x4_t (&acc)[FM][FN], int wm,
-                                            int half, int wn, unsigned char *stage) {
+__device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t, const f32x4_t (&acc)[FM][FN],
+                                            Spot spot, unsigned char *stage) {
   constexpr bool WIDE = DEALT && FORM == kForward;
   constexpr int COLS = FN * 16 / (GATED ? 2 : 1);
-  const int n = t.n0 + wn;
-  const bool whole = p.cvec && n + COLS <= p.n;
+  const bool whole = p.cvec && t.n0 + spot.n + COLS / 2 + (COLS / 2 > spot.right ? COLS / 2 : spot.right) <= p.n;
   uint16_t *s0 = nullptr, *s1 = nullptr;
   const uint16_t *bias = nullptr, *res = nullptr;
   if (FORM == kForward) {
@@ -485,7 +504,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t
     if (p.bias) bias = p.bias + static_cast<int64_t>(t.e) * p.n;
     if (p.residual) res = p.residual + t.row0 * p.ldc;
   }
-#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, wm, half, t.mvalid, n, whole, p.lines ? stage : nullptr);
+#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, spot, t.mvalid, t.n0, whole, p.lines ? stage : nullptr);
   if (FORM != kForward) {
     RRB_STORE(RRB_ACT_NONE)
     return;
@@ -529,7 +548,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
 
   const int tid = threadIdx.x;
   const int wave = uniform(tid >> 6);
-  const Place t = place_tile<BM, GATED ? BN / 2 : BN, FORM>(p);
+  const Place t = place_tile<BM, GATED ? BN / 2 : BN, 0, FORM>(p);
   if (t.empty) return;
   const int klen = t.klen;
   const int per = (klen + kStep - 1) / kStep;  // steps per phase
@@ -605,7 +624,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
     }
     if (s + 1 < steps) commit((s + 1) & 1);
   }
-  finish_tile<FORM, GATED, false>(p, t, acc, wm, FM * 8, GATED ? wn / 2 : wn, nullptr);
+  finish_tile<FORM, GATED, false>(p, t, acc, Spot{wm, GATED ? wn / 2 : wn, FM * 8, FN * (GATED ? 4 : 8)}, nullptr);
 }
 
 // ---- the tiled product, loads straight to LDS -----------------------------------
@@ -652,7 +671,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 
   const int tid = threadIdx.x;
   const int wave = uniform(tid >> 6);
-  const Place t = place_tile<BM, GATED ? BN / 2 : BN, FORM>(p);
+  const Place t = place_tile<BM, GATED ? BN / 2 : BN, 0, FORM>(p);
   if (t.empty) return;
   const int klen = t.klen;
   const int per = (klen + kStep - 1) / kStep;  // steps per phase
@@ -768,7 +787,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  finish_tile<FORM, GATED, false>(p, t, acc, wm, FM * 8, GATED ? wn / 2 : wn, nullptr);
+  finish_tile<FORM, GATED, false>(p, t, acc, Spot{wm, GATED ? wn / 2 : wn, FM * 8, FN * (GATED ? 4 : 8)}, nullptr);
 }
 
 // ---- the tiled product, two wave groups by turns -----------------------------------
@@ -778,8 +797,8 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 // group issues 16 matrix instructions (a quarter of its step) the other reads
 // fragments and starts loads, so a SIMD's matrix core and the LDS work at the
 // same time.  A step's tiles are kept as four regions of 16 KiB, the first and
-// second 128 rows (A0, A1; a group has 64 of each) and the first and second
-// halves of each wave's columns (B0, B1), two steps
+// second 128 rows (A0, A1; a group has 64 of each) and columns (B0, B1; a wave
+// has 32 of each, gated: half of the rows dealt to its 32 outputs), two steps
 // deep.  In phase p a group reads and starts
 //   0  reads B0, half of A1;            starts A1 of step s + 1;    A0 x B0
 //   1  reads the rest of A1;                                        A0 x B1
@@ -802,7 +821,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 template <bool GATED>
 __device__ __forceinline__ int dealt_row(int r, int h) {
   if (GATED) return (r >> 5) * 32 + ((r >> 2) & 3) * 8 + h * 4 + (r & 3);  // gate and up rows of the same outputs
-  return (r >> 5) * 64 + h * 32 + ((r >> 2) & 3) * 8 + ((r >> 4) & 1) * 4 + (r & 3);
+  return h * 128 + (r >> 5) * 32 + ((r >> 2) & 3) * 8 + ((r >> 4) & 1) * 4 + (r & 3);
 }
 
 template <int FORM, bool GATED>
@@ -833,7 +852,7 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
         va[h][i] = m < t.mvalid ? m * lda2 + ch * 16 : kOutside;
       }
       if (B_COL) {
-        vb[h][i] = kr * ldb2 + ((c >> 2) * 64 + h * 32 + (c & 3) * 8) * 2;
+        vb[h][i] = kr * ldb2 + (h * 128 + c * 8) * 2;
       } else {
         const int n = dealt_row<GATED>(r, h);
         vb[h][i] = (t.n0 + n < p.n ? n : p.n - 1 - t.n0) * ldb2 + ch * 16;
@@ -1007,14 +1026,13 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
     RRB_BARRIER();
   }
 #undef RRB_BARRIER
-  finish_tile<FORM, GATED, true>(p, t, acc, wr * 64, 128, GATED ? wc * 32 : wc * 64,
-                                 GATED ? nullptr : lds + wave * 16384);
+  finish_tile<FORM, GATED, true>(p, t, acc, Spot{wr * 64, wc * 32, 128, GATED ? 16 : 128}, GATED ? nullptr : lds);
 }
 
 template <int FORM, bool GATED>
 __global__ void __launch_bounds__(512, 2) product_turns_kernel(ProductArgs p) {
   __shared__ __align__(16) unsigned char lds[131072];
-  const Place t = place_tile<256, GATED ? 128 : 256, FORM>(p);
+  const Place t = place_tile<256, GATED ? 128 : 256, 128, FORM>(p);
   if (t.empty) return;
   product_turns_tile<FORM, GATED>(p, t, lds);
 }
