@@ -140,7 +140,10 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 __device__ __forceinline__ const uint16_t *uniform(const uint16_t *q) {
   const uint64_t v = reinterpret_cast<uint64_t>(q);
   const uint32_t lo = uniform(static_cast<int>(v)), hi = uniform(static_cast<int>(v >> 32));
-  return reinterpret_cast<const uint16_t *>(static_cast<uint64_t>(hi) << 32 | lo);
+  // As a global address: through a plain one the loads would be flat, which
+  // wait with the LDS's.
+  typedef __attribute__((address_space(1))) const uint16_t *global;
+  return (const uint16_t *)(global)(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 // ---- operand tiles in LDS -----------------------------------------------------
@@ -184,17 +187,19 @@ __device__ __forceinline__ bf16x8_t col_fragment(const unsigned char *tile, int 
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Eight bf16 from `src`, of which the first `have` exist (the others are 0).
+// Eight bf16 from `src`, of which the first `have` exist (the others are 0).  A
+// partial chunk is read as eight single elements, the last one again for those
+// that are not there, so that its loads go out together.
 __device__ __forceinline__ u32x4_t load_chunk(const uint16_t *src, int64_t have) {
   u32x4_t v = {0, 0, 0, 0};
   if (have >= 8) {
     __builtin_memcpy(&v, src, 16);
   } else if (have > 0) {
-    uint32_t w[4] = {0, 0, 0, 0};
+    uint32_t e[8];
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < have) w[i >> 1] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
-    v = u32x4_t{w[0], w[1], w[2], w[3]};
+    for (int i = 0; i < 8; ++i) e[i] = src[i < have ? i : have - 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (2 * i < have ? e[2 * i] : 0) | (2 * i + 1 < have ? e[2 * i + 1] << 16 : 0);
   }
   return v;
 }
@@ -555,6 +560,14 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
   const int steps = FORM == kGradX ? per * p.halves : per;
 
   u32x4_t ra[CA], rb[CB];
+  // Elements of a column tile's chunk to read in row k, of whose `cols` columns
+  // `have` are left there.  A chunk over the row's end is read whole, into the
+  // next rows, while the group's matrix has that many elements left: its
+  // columns past the end are of outputs that are not stored.
+  auto there = [&](int64_t k, int have, int cols, int64_t ld) {
+    if (k >= klen) return 0;
+    return have > 0 && (klen - k) * ld - (cols - have) >= 8 ? 8 : have;
+  };
   // Loads of one step's chunks into registers.
   auto fetch = [&](int step) {
     const int h = FORM == kGradX && step >= per ? 1 : 0;
@@ -565,7 +578,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
       if (A_COL) {
         const int kr = id / (BM / 8), pos = id % (BM / 8);
         const int ch = pos ^ (col_swizzle<BM>(kr) << 1);
-        ra[i] = load_chunk(t.a[0] + (k0 + kr) * p.lda + ch * 8, k0 + kr < klen ? p.m - t.m0 - ch * 8 : 0);
+        ra[i] = load_chunk(t.a[0] + (k0 + kr) * p.lda + ch * 8, there(k0 + kr, p.m - t.m0 - ch * 8, p.m, p.lda));
       } else {
         const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
         const int64_t have = klen - k0 - ch * 8;
@@ -578,7 +591,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
       if (B_COL) {
         const int kr = id / (BN / 8), pos = id % (BN / 8);
         const int ch = pos ^ (col_swizzle<BN>(kr) << 1);
-        rb[i] = load_chunk(t.b[h] + (k0 + kr) * p.ldb + ch * 8, k0 + kr < klen ? p.n - t.n0 - ch * 8 : 0);
+        rb[i] = load_chunk(t.b[h] + (k0 + kr) * p.ldb + ch * 8, there(k0 + kr, p.n - t.n0 - ch * 8, p.n, p.ldb));
       } else {
         const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
         const int64_t have = klen - k0 - ch * 8;
@@ -1213,7 +1226,11 @@ template <int FORM, bool GATED>
 rrb_status launch_product(const ProductArgs &p, hipStream_t s) {
   bool direct = p.lda % 8 == 0 && p.ldb % 8 == 0;
   for (int h = 0; h < 2; ++h) direct = direct && aligned(p.a[h], 16) && aligned(p.b[h], 16);
-  if (!direct) return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
+  if (!direct) {
+    if (estimate<FORM, GATED>(p, 128, 128, 2, 1.7, 2) <= estimate<FORM, GATED>(p, 64, 64, 4, 1.1, 1))
+      return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED>, 256, p, s);
+    return launch_tiles<64, 64, FORM, GATED>(product_kernel<64, 64, 2, 2, FORM, GATED>, 256, p, s);
+  }
   // A tile of at most 128 valid rows takes about half a 256-row step.
   const bool half = FORM != kGradW && static_cast<int64_t>(p.groups) * 128 >= p.rows;
   const double big = estimate<FORM, GATED>(p, 256, 256, 1, half ? 0.9 : 1.55, 8);
