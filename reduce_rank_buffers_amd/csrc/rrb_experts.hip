@@ -16,7 +16,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <initializer_list>
 #include <type_traits>
 
 #include "rrb_internal.h"
@@ -125,7 +124,6 @@ struct ProductArgs {
   int32_t bm, bn;         // tiles of one XCD's block: bm slots x bn column tiles, or bm in a row
   int32_t halves;         // kGradX: phases; kGradW: outputs
   int32_t act;
-  int32_t cvec, lines;    // every output row starts on an 8-, a 16-byte boundary
 };
 
 // Offsets as the kernels read them: inside the arena whatever the array
@@ -204,34 +202,26 @@ __device__ __forceinline__ u32x4_t load_chunk(const uint16_t *src, int64_t have)
   return v;
 }
 
-// W consecutive columns of one row, W = 4 or 8, as fp32.
+// W consecutive columns of one row, W = 4 or 8, as fp32; `have` of them exist.
 template <int W>
-__device__ __forceinline__ void load_cols(const uint16_t *src, int have, bool whole, float (&v)[W]) {
-  if (whole) {
+__device__ __forceinline__ void load_cols(const uint16_t *src, int have, float (&v)[W]) {
+  if (have >= W) {
+    uint32_t w[W / 2];
+    __builtin_memcpy(w, src, sizeof w);
 #pragma unroll
-    for (int q = 0; q < W; q += 4) {
-      const uint2 w = *reinterpret_cast<const uint2 *>(src + q);
-      v[q] = bf16_lo(w.x); v[q + 1] = bf16_hi(w.x); v[q + 2] = bf16_lo(w.y); v[q + 3] = bf16_hi(w.y);
-    }
+    for (int q = 0; q < W; ++q) v[q] = q & 1 ? bf16_hi(w[q >> 1]) : bf16_lo(w[q >> 1]);
   } else {
 #pragma unroll
     for (int q = 0; q < W; ++q) v[q] = q < have ? bf16_to_f32(src[q]) : 0.f;
   }
 }
 template <int W>
-__device__ __forceinline__ void store_cols(uint16_t *dst, int have, bool whole, const float (&v)[W]) {
+__device__ __forceinline__ void store_cols(uint16_t *dst, int have, const float (&v)[W]) {
   uint32_t w[W / 2];
 #pragma unroll
   for (int q = 0; q < W / 2; ++q) w[q] = cvt_pk_bf16(v[2 * q], v[2 * q + 1]);
-  if (whole) {
-    if (W == 8) {
-      // The pair of stores becomes one of 16 bytes where the pitch allows;
-      // rows are known to start on 8-byte boundaries only.
-      typedef uint32_t __attribute__((ext_vector_type(4), aligned(8))) quad;
-      *reinterpret_cast<quad *>(dst) = quad{w[0], w[1], w[W / 2 - 2], w[W / 2 - 1]};
-    } else {
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-    }
+  if (have >= W) {
+    __builtin_memcpy(dst, w, sizeof w);
   } else {
 #pragma unroll
     for (int q = 0; q < W; ++q)
@@ -246,12 +236,12 @@ __device__ __forceinline__ void store_cols(uint16_t *dst, int have, bool whole, 
 // blocks were dealt together (WIDE), the first or second half of eight at
 // 8 (l / 16).  Gated: blocks are gate and up by turns.
 // The second half of a wave's blocks of rows begins `down` rows behind the first
-// block, and of columns `right` columns.  `whole`: rows start on 8-byte
-// boundaries and all of the wave's columns exist.  `stage` (256 x 256 tiles, not
-// gated, rows on 16-byte boundaries): 128 KiB of LDS through which results
-// leave as whole rows of the tile instead of 32- or 64-byte pieces (a weight
-// gradient's 268 MB of zeros: 77 -> 56 us); 16-byte chunk c of row r is kept
-// at c ^ r % 16, so that neither side meets its own banks.
+// block, and of columns `right` columns.  Rows may start at any element: vector
+// loads and stores need no alignment.  `stage` (256 x 256 tiles, not gated): 128
+// KiB of LDS through which results leave as whole rows of the tile instead of
+// 32- or 64-byte pieces (a weight gradient's 268 MB of zeros: 77 -> 56 us);
+// 16-byte chunk c of row r is kept at c ^ r % 16, so that neither side meets its
+// own banks.  Then save0 is NULL: the stage holds one output at a time.
 struct Spot {
   int m, n;         // the wave's first row and output column in the tile
   int down, right;
@@ -260,7 +250,7 @@ struct Spot {
 template <int ACT, bool GATED, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (&acc)[FM][FN], uint16_t *c,
                                            uint16_t *save0, uint16_t *save1, const uint16_t *bias,
-                                           const uint16_t *residual, Spot spot, int mvalid, int n0, bool whole,
+                                           const uint16_t *residual, Spot spot, int mvalid, int n0,
                                            unsigned char *stage) {
   constexpr int W = WIDE ? 8 : 4;                           // consecutive columns per lane
   constexpr int BLOCKS = (GATED ? 2 : 1) * (WIDE ? 2 : 1);  // blocks that make them
@@ -278,7 +268,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (
       if (W == 8)
         *reinterpret_cast<uint2 *>(q + 8) = make_uint2(cvt_pk_bf16(v[W - 4], v[W - 3]), cvt_pk_bf16(v[W - 2], v[W - 1]));
     } else {
-      store_cols<W>(to + m * p.ldc + n0 + n, p.n - n0 - n, whole, v);
+      store_cols<W>(to + m * p.ldc + n0 + n, p.n - n0 - n, v);
     }
   };
   // The staged tile to `to`, 32 rows per wave.
@@ -290,62 +280,58 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, const f32x4_t (
     for (int b = 0; b < 16; ++b) {
       const int m = (threadIdx.x >> 6) * 32 + b * 2 + (lane >> 5);
       const u32x4_t v = *reinterpret_cast<const u32x4_t *>(stage + m * 512 + ((lane & 31) ^ (m & 15)) * 16);
-      if (m < mvalid && n < p.n) *reinterpret_cast<u32x4_t *>(to + m * p.ldc + n) = v;
+      if (m >= mvalid) continue;
+      if (n + 8 <= p.n) {
+        __builtin_memcpy(to + m * p.ldc + n, &v, 16);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 7; ++q)
+          if (n + q < p.n) to[m * p.ldc + n + q] = static_cast<uint16_t>(v[q >> 1] >> (16 * (q & 1)));
+      }
     }
     __syncthreads();
   };
-  // Staged, the pre-activation goes first: the stage holds one output at a
-  // time.
-  const bool ahead = !GATED && save0 && stage;
 #pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 0 && !ahead) continue;
+  for (int j = 0; j < FN; j += BLOCKS) {
+    const int n = col_at(j), have = p.n - n0 - n;
+    if (have <= 0) continue;
+    float b[W];
+    if (!GATED && bias) load_cols<W>(bias + n0 + n, have, b);
 #pragma unroll
-    for (int j = 0; j < FN; j += BLOCKS) {
-      const int n = col_at(j), have = p.n - n0 - n;
-      if (have <= 0) continue;
-      float b[W];
-      if (!GATED && bias) load_cols<W>(bias + n0 + n, have, whole, b);
+    for (int i = 0; i < FM; ++i) {
+      const int m = row_at(i);
+      if (m >= mvalid) continue;
+      float v[W];
+      if (GATED) {
+        float u[W];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int m = row_at(i);
-        if (m >= mvalid) continue;
-        float v[W];
-        if (GATED) {
-          float u[W];
-#pragma unroll
-          for (int q = 0; q < W; ++q) {
-            v[q] = acc[i][j + (q >> 2) * 2][q & 3];
-            u[q] = acc[i][j + (q >> 2) * 2 + (GATED ? 1 : 0)][q & 3];
-          }
-          if (save0) {
-            put(save0, m, n, v);
-            put(save1, m, n, u);
-          }
-#pragma unroll
-          for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]) * u[q];
-        } else {
-#pragma unroll
-          for (int q = 0; q < W; ++q) v[q] = acc[i][j + (q >> 2)][q & 3] + (bias ? b[q] : 0.f);
-          if (pass == 0) {
-            put(save0, m, n, v);
-            continue;
-          }
-          if (save0 && !ahead) put(save0, m, n, v);
-#pragma unroll
-          for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]);
-          if (residual) {
-            float r[W];
-            load_cols<W>(residual + m * p.ldc + n0 + n, have, whole, r);
-#pragma unroll
-            for (int q = 0; q < W; ++q) v[q] += r[q];
-          }
+        for (int q = 0; q < W; ++q) {
+          v[q] = acc[i][j + (q >> 2) * 2][q & 3];
+          u[q] = acc[i][j + (q >> 2) * 2 + (GATED ? 1 : 0)][q & 3];
         }
-        put(c, m, n, v);
+        if (save0) {
+          put(save0, m, n, v);
+          put(save1, m, n, u);
+        }
+#pragma unroll
+        for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]) * u[q];
+      } else {
+#pragma unroll
+        for (int q = 0; q < W; ++q) v[q] = acc[i][j + (q >> 2)][q & 3] + (bias ? b[q] : 0.f);
+        if (save0) put(save0, m, n, v);
+#pragma unroll
+        for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]);
+        if (residual) {
+          float r[W];
+          load_cols<W>(residual + m * p.ldc + n0 + n, have, r);
+#pragma unroll
+          for (int q = 0; q < W; ++q) v[q] += r[q];
+        }
       }
+      put(c, m, n, v);
     }
-    flush(pass == 0 ? save0 : c);
   }
+  flush(c);
 }
 
 // ---- the tiled product ------------------------------------------------------------
@@ -499,8 +485,6 @@ template <int FORM, bool GATED, bool DEALT, int FM, int FN>
 __device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t, const f32x4_t (&acc)[FM][FN],
                                             Spot spot, unsigned char *stage) {
   constexpr bool WIDE = DEALT && FORM == kForward;
-  constexpr int COLS = FN * 16 / (GATED ? 2 : 1);
-  const bool whole = p.cvec && t.n0 + spot.n + COLS / 2 + (COLS / 2 > spot.right ? COLS / 2 : spot.right) <= p.n;
   uint16_t *s0 = nullptr, *s1 = nullptr;
   const uint16_t *bias = nullptr, *res = nullptr;
   if (FORM == kForward) {
@@ -509,10 +493,15 @@ __device__ __forceinline__ void finish_tile(const ProductArgs &p, const Place &t
     if (p.bias) bias = p.bias + static_cast<int64_t>(t.e) * p.n;
     if (p.residual) res = p.residual + t.row0 * p.ldc;
   }
-#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, spot, t.mvalid, t.n0, whole, p.lines ? stage : nullptr);
+#define RRB_STORE(A) store_tile<A, GATED, WIDE>(p, acc, t.c, s0, s1, bias, res, spot, t.mvalid, t.n0, stage);
   if (FORM != kForward) {
     RRB_STORE(RRB_ACT_NONE)
     return;
+  }
+  // Staged, the pre-activation goes by itself: the stage holds one output.
+  if (!GATED && stage && s0) {
+    store_tile<RRB_ACT_NONE, GATED, WIDE>(p, acc, s0, nullptr, nullptr, bias, nullptr, spot, t.mvalid, t.n0, stage);
+    s0 = nullptr;
   }
   switch (p.act) {
 #define RRB_CASE(A)  \
@@ -1318,13 +1307,6 @@ rrb_status launch_act_grad(const ActGradArgs &a, int act, hipStream_t s) {
   return launched("activation gradient");
 }
 
-void set_output_alignment(ProductArgs &p, std::initializer_list<const void *> arrays) {
-  uintptr_t bits = static_cast<uintptr_t>(p.ldc * 2);
-  for (const void *a : arrays) bits |= reinterpret_cast<uintptr_t>(a);
-  p.cvec = bits % 8 == 0;
-  p.lines = bits % 16 == 0;
-}
-
 const uint16_t *u16(const void *p) { return static_cast<const uint16_t *>(p); }
 uint16_t *u16(void *p) { return static_cast<uint16_t *>(p); }
 
@@ -1362,7 +1344,6 @@ rrb_status rrb_expert_gated(const rrb_expert_spec *spec, const void *d_x, const 
   p.n = static_cast<int32_t>(spec->out);
   p.k = static_cast<int32_t>(spec->in);
   p.act = spec->activation;
-  set_output_alignment(p, {d_out, d_save_gate, d_save_up});
   return launch_product<kForward, true>(p, static_cast<hipStream_t>(stream));
 }
 
@@ -1375,8 +1356,8 @@ rrb_status rrb_expert_linear(const rrb_expert_spec *spec, const void *d_x, const
   if (spec->rows == 0) return RRB_OK;
   if (!d_x || !d_w || !d_out) return fail(RRB_EINVAL, "NULL x, w or out");
   const Bytes z(*spec);
-  // The residual is read where the output is written, by the same lane: it
-  // may be the output itself.
+  // A tile's residual is read before any of the tile is written, and by no
+  // other workgroup: it may be the output itself.
   const Span spans[] = {{d_x, z.x, "x", false}, {d_offsets, z.offsets, "offsets", false}, {d_w, z.w, "w", false},
                         {d_bias, z.bias, "bias", false},
                         {d_residual == d_out ? nullptr : d_residual, z.y, "residual", false},
@@ -1394,7 +1375,6 @@ rrb_status rrb_expert_linear(const rrb_expert_spec *spec, const void *d_x, const
   p.n = static_cast<int32_t>(spec->out);
   p.k = static_cast<int32_t>(spec->in);
   p.act = spec->activation;
-  set_output_alignment(p, {d_out, d_save_pre, d_bias, d_residual});
   return launch_product<kForward, false>(p, static_cast<hipStream_t>(stream));
 }
 
@@ -1477,7 +1457,6 @@ rrb_status rrb_expert_gated_backward(const rrb_expert_spec *spec, const void *d_
     q.c[0] = u16(d_dx);
     q.ldb = q.ldc = spec->in;
     q.k = static_cast<int32_t>(spec->out);
-    set_output_alignment(q, {d_dx});
     if ((st = launch_product<kGradX, false>(q, s)) != RRB_OK) return st;
   }
   if (d_dw_gate) {
@@ -1486,7 +1465,6 @@ rrb_status rrb_expert_gated_backward(const rrb_expert_spec *spec, const void *d_
     p.c[1] = u16(d_dw_up);
     p.ldb = p.ldc = spec->in;
     p.m = static_cast<int32_t>(spec->out);
-    set_output_alignment(p, {d_dw_gate, d_dw_up});
     if ((st = launch_product<kGradW, false>(p, s)) != RRB_OK) return st;
   }
   return RRB_OK;
@@ -1546,7 +1524,6 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
     q.c[0] = u16(d_dx);
     q.ldb = q.ldc = spec->in;
     q.k = static_cast<int32_t>(spec->out);
-    set_output_alignment(q, {d_dx});
     if ((st = launch_product<kGradX, false>(q, s)) != RRB_OK) return st;
   }
   if (d_dw) {
@@ -1555,7 +1532,6 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
     q.c[0] = q.c[1] = u16(d_dw);
     q.ldb = q.ldc = spec->in;
     q.m = static_cast<int32_t>(spec->out);
-    set_output_alignment(q, {d_dw});
     if ((st = launch_product<kGradW, false>(q, s)) != RRB_OK) return st;
   }
   if (d_dbias) {
