@@ -297,8 +297,8 @@ rrb_status rrb_empty_kernel(rrb_stream_t stream);
  * masks an expert: it has weight 0 and is chosen only where too few others
  * are left (a row of -inf alone: experts 0..topk-1 with weight 0).  Scores of
  * +inf share the weight equally.  NaN ranks above every number and makes the
- * row's weights NaN; the experts stay distinct and in range.  experts <= 1024
- * and topk <= 16 (RRB_EUNSUPPORTED).  Asynchronous on `stream`.
+ * row's weights NaN; the experts stay distinct and in range.  experts <= 1024,
+ * topk <= 16, tokens < 2^26 (RRB_EUNSUPPORTED otherwise).  Asynchronous on `stream`.
  */
 #define RRB_GATE_RENORMALIZE 1u
 rrb_status rrb_moe_gate(int64_t tokens, int32_t experts, int32_t topk, int32_t dtype,

@@ -1164,7 +1164,8 @@ rrb_status launch_tiles(void (*kernel)(ProductArgs), int threads, ProductArgs p,
     p.bm = tiles >= 4096 ? 32 : tiles >= 1024 ? 16 : tiles >= 256 ? 8 : 1;
     grid = (tiles + 8 * p.bm - 1) / (8 * p.bm) * (8 * p.bm);
   }
-  if (grid > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
+  // A launch's threads are counted in 32 bits.
+  if (grid * threads > 0xffffffffLL) return fail(RRB_EUNSUPPORTED, "too many tiles for one launch");
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, p);
   return launched("expert product");
 }

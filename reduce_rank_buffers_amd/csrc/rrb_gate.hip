@@ -287,7 +287,7 @@ rrb_status gate(const GateArgs &a, int32_t dtype, uint32_t flags, bool back, rrb
   if (a.experts > kRouteMaxExperts || a.topk > kRouteMaxTopk)
     return fail(RRB_EUNSUPPORTED, "experts %d, topk %d: at most %d and %d", a.experts, a.topk, kRouteMaxExperts,
                 kRouteMaxTopk);
-  if (a.tokens > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tokens for one launch");
+  if (a.tokens >= 1LL << 26) return fail(RRB_EUNSUPPORTED, "tokens %lld >= 2^26", (long long)a.tokens);
   if (a.tokens == 0) return RRB_OK;
   if (!a.logits || !a.idx || (back ? !a.dw || !a.dlogits : !a.w)) return fail(RRB_EINVAL, "NULL array");
   // Whole 16-byte loads where every row starts on such a boundary.

@@ -310,6 +310,7 @@ struct BackArgs {
   unsigned char *dz[RRB_MAX_RANKS];
   float *dw;  // [T][k] in routing order, or NULL: z is not read
   bool has_dz;
+  uint32_t first;  // token of workgroup 0
   RowArgs r;  // maps, weights, sizes
 };
 
@@ -344,7 +345,7 @@ __device__ __forceinline__ void store_dots(float (&dot)[K], float *dw, const int
 template <int K>
 __global__ void __launch_bounds__(kBackBlock) moe_combine_backward_kernel(BackArgs b) {
   const RowArgs &a = b.r;
-  const uint32_t t = blockIdx.x;
+  const uint32_t t = b.first + blockIdx.x;
   const int64_t tk = static_cast<int64_t>(t) * K;
   const int32_t status = route_status_word(a);
   int32_t s[K];
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kBackBlock) moe_combine_backward_kernel(BackAr
 __global__ void __launch_bounds__(kBackBlock) moe_combine_backward_any_kernel(BackArgs b) {
   const RowArgs &a = b.r;
   if (route_failed(a)) return;
-  const int64_t t = blockIdx.x;
+  const int64_t t = static_cast<int64_t>(b.first) + blockIdx.x;
   const int64_t rank = t / a.tokens_per_rank;
   const uint16_t *dy = reinterpret_cast<const uint16_t *>(b.dy[rank] + (t - rank * a.tokens_per_rank) * a.row_bytes);
   for (int j = 0; j < a.k; ++j) {
@@ -1159,7 +1160,6 @@ rrb_status launch_combine_backward(const Plan &p, const void *const *dy, const v
                                    const float *d_weights, float *d_dweights, void *stream) {
   const RowMaps &m = p.rows;
   if (m.tokens == 0) return RRB_OK;
-  if (m.tokens > 0x7fffffffLL) return fail(RRB_EUNSUPPORTED, "too many tokens for one launch");
   BackArgs b;
   std::memset(&b, 0, sizeof b);
   for (int32_t r = 0; r < p.nranks; ++r) {
@@ -1187,9 +1187,17 @@ rrb_status launch_combine_backward(const Plan &p, const void *const *dy, const v
             reinterpret_cast<uintptr_t>(b.dz[r]);
   BackFn kern = (bits & 15) == 0 ? combine_backward_for(m.topk) : nullptr;
   if (!kern) kern = moe_combine_backward_any_kernel;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(m.tokens)), dim3(kBackBlock), 0,
-                     static_cast<hipStream_t>(stream), b);
-  return route_launch_check("combine backward");
+  // A launch's threads are counted in 32 bits: 2^23 tokens at a time (the row
+  // plans hold up to 2^26).
+  constexpr int64_t kMost = 1 << 23;
+  for (int64_t first = 0; first < m.tokens; first += kMost) {
+    b.first = static_cast<uint32_t>(first);
+    const int64_t n = m.tokens - first < kMost ? m.tokens - first : kMost;
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(n)), dim3(kBackBlock), 0, static_cast<hipStream_t>(stream), b);
+    const rrb_status st = route_launch_check("combine backward");
+    if (st != RRB_OK) return st;
+  }
+  return RRB_OK;
 }
 
 rrb_status launch_expert_offsets(const Plan &p, int32_t *d_offsets, void *stream) {

@@ -191,9 +191,12 @@ def test_linear_in_place_residual():
 def test_gated(shape, lead, tail, shift):
     require_gpu()
     k = SHAPES.index(shape) + lead + shift
-    p, name = Problem(4, *shape, lead=lead, tail=tail, shift=shift), ACTS[k % 5]
+    _forward_gated(Problem(4, *shape, lead=lead, tail=tail, shift=shift), ACTS[k % 5], k % 2)
+
+
+def _forward_gated(p, name, save):
     h = p.out(p.N, p.o)
-    g, u = (p.out(p.N, p.o), p.out(p.N, p.o)) if k % 2 else (None, None)
+    g, u = (p.out(p.N, p.o), p.out(p.N, p.o)) if save else (None, None)
     rrb.expert_gated(p.x, p.d_off, p.w, p.w2, h, activation=name, save_gate=g, save_up=u)
     torch.cuda.synchronize()
     x, wg, wu = _np(p.x), _np(p.w), _np(p.w2)
@@ -224,8 +227,10 @@ def _grad_bounds(p, d, d_err, x, w):
 def test_linear_backward(shape, lead, tail, shift):
     require_gpu()
     k = SHAPES.index(shape) + lead + shift
-    name = ACTS[k % 5]
-    p = Problem(5, *shape, lead=lead, tail=tail, shift=shift)
+    _backward_linear(Problem(5, *shape, lead=lead, tail=tail, shift=shift), ACTS[k % 5])
+
+
+def _backward_linear(p, name):
     d, pre = p.rows(p.o), p.rows(p.o) if name != "none" else None
     d_x, d_w, d_b = p.out(p.N, p.i), p.out(p.G, p.o, p.i), p.out(p.G, p.o)
     rrb.expert_linear_backward(d, p.x, p.d_off, p.w, pre=pre, activation=name, d_x=d_x, d_w=d_w, d_bias=d_b)
@@ -250,8 +255,10 @@ def test_linear_backward(shape, lead, tail, shift):
 def test_gated_backward(shape, lead, tail, shift):
     require_gpu()
     k = SHAPES.index(shape) + lead + shift
-    name = ACTS[(k + 1) % 5]
-    p = Problem(6, *shape, lead=lead, tail=tail, shift=shift)
+    _backward_gated(Problem(6, *shape, lead=lead, tail=tail, shift=shift), ACTS[(k + 1) % 5])
+
+
+def _backward_gated(p, name):
     d, g, u = p.rows(p.o), p.rows(p.o), p.rows(p.o)
     d_x, d_wg, d_wu = p.out(p.N, p.i), p.out(p.G, p.o, p.i), p.out(p.G, p.o, p.i)
     rrb.expert_gated_backward(d, p.x, p.d_off, p.w, p.w2, g, u, activation=name, d_x=d_x, d_w_gate=d_wg, d_w_up=d_wu)
@@ -268,6 +275,81 @@ def test_gated_backward(shape, lead, tail, shift):
     _check("d_w_gate", d_wg, wwg, bwg, 2 * HALF)
     _check("d_w_up", d_wu, wwu, bwu, 2 * HALF)
     p.untouched("d_x", d_x)
+
+
+# Enough tiles for the larger tile shapes: whole tiles, tiles of at most 128
+# rows, one row, empty groups; a reduction that ends inside a step and outputs
+# that end inside a tile.
+RAGGED = [2500, 0, 100, 1300, 129, 1, 2900, 256, 128, 700]
+
+
+@pytest.mark.parametrize("i,o", [(200, 4104), (64, 4104), (136, 8200), (2056, 1032)])
+@pytest.mark.parametrize("lead,tail", [(0, 0), (7, 9)])
+def test_large_forward(i, o, lead, tail):
+    require_gpu()
+    _say(f"large forward {i} -> {o}")
+    _forward_linear(Problem(50, RAGGED, i, o, lead, tail), ACTS[i % 5], True, True, lead == 0)
+    _forward_gated(Problem(51, RAGGED, i, o // 2, lead, tail), ACTS[(i + 2) % 5], lead == 0)
+
+
+@pytest.mark.parametrize("i,o", [(4104, 200), (4104, 201), (8200, 64), (2056, 1027)])
+@pytest.mark.parametrize("lead,tail", [(0, 0), (7, 9)])
+def test_large_backward(i, o, lead, tail):
+    require_gpu()
+    _say(f"large backward {i} <- {o}")
+    _backward_linear(Problem(52, RAGGED, i, o, lead, tail), ACTS[o % 5])
+    _backward_gated(Problem(53, RAGGED, i, o, lead, tail), ACTS[(o + 2) % 5])
+
+
+@pytest.mark.parametrize("sizes,i,o", [([1, 0, 3, 1, 2, 60, 1, 9], 2048, 4096), ([64] * 32, 1024, 1024),
+                                       ([40, 100] * 16, 512, 2048), ([1] * 300, 256, 512)])
+def test_few_rows(sizes, i, o):
+    """Shapes where the smaller tiles are taken: decode and short batches."""
+    require_gpu()
+    _forward_linear(Problem(54, sizes, i, o), "silu", True, False, True)
+    _forward_gated(Problem(55, sizes, i, o), "gelu", False)
+    _backward_gated(Problem(56, sizes, i, o // 4), "silu")
+
+
+def test_arena_past_4_gib():
+    """Rows and weights whose byte offsets pass 2^32: the last rows' outputs
+    and the last group's gradient against the oracle on those alone."""
+    require_gpu()
+    N, i, o = 280000, 8192, 64
+    _say(f"arena of {N * i * 2 >> 20} MiB")
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.empty(N, i, dtype=BF, device=DEV)
+    for a in range(0, N, 40000):
+        x[a:a + 40000] = torch.randn(min(40000, N - a), i, generator=gen, device=DEV).to(BF)
+    off = torch.tensor([0, N - 100, N], dtype=torch.int32, device=DEV)
+    w = (torch.randn(2, o, i, generator=gen, device=DEV) * i ** -0.5).to(BF)
+    y, d_w = torch.empty(N, o, dtype=BF, device=DEV), torch.empty_like(w)
+    rrb.expert_linear(x, off, w, y)
+    at = slice(N - 300, N)
+    nx, nw = _np(x[at]), _np(w)
+    want = np.concatenate([nx[:200] @ nw[0].T, nx[200:] @ nw[1].T])
+    scale = np.concatenate([np.abs(nx[:200]) @ np.abs(nw[0]).T, np.abs(nx[200:]) @ np.abs(nw[1]).T])
+    _check("out", y[at], want, i * ADD * scale, HALF * 1.01)
+    rrb.expert_linear_backward(y, x, off, w, d_w=d_w)
+    ny = _np(y[N - 100:])
+    _check("d_w", d_w[1], ny.T @ nx[200:], 101 * ADD * (np.abs(ny).T @ np.abs(nx[200:])), HALF * 1.01)
+    d_x = x  # in place of the inputs, which nothing reads any more
+    rrb.expert_linear_backward(y, torch.empty_like(x), off, w, d_x=d_x)
+    ny = _np(y[at])
+    want = np.concatenate([ny[:200] @ nw[0], ny[200:] @ nw[1]])
+    scale = np.concatenate([np.abs(ny[:200]) @ np.abs(nw[0]), np.abs(ny[200:]) @ np.abs(nw[1])])
+    _check("d_x", d_x[at], want, (o + 1) * ADD * scale, HALF * 1.01)
+    del x, d_x, y
+    G, i, o = 40, 8192, 8192
+    w = torch.empty(G, o, i, dtype=BF, device=DEV)
+    for e in range(G):
+        w[e] = (torch.randn(o, i, generator=gen, device=DEV) * i ** -0.5).to(BF)
+    x = torch.randn(2 * G, i, generator=gen, device=DEV).to(BF)
+    off = torch.arange(0, 2 * G + 1, 2, dtype=torch.int32, device=DEV)
+    y = torch.empty(2 * G, o, dtype=BF, device=DEV)
+    rrb.expert_linear(x, off, w, y)
+    nx, nw = _np(x[-2:]), _np(w[-1])
+    _check("out", y[-2:], nx @ nw.T, i * ADD * (np.abs(nx) @ np.abs(nw).T), HALF * 1.01)
 
 
 def test_gradients_against_differences():
