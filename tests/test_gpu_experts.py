@@ -283,7 +283,7 @@ def _backward_gated(p, name):
 RAGGED = [2500, 0, 100, 1300, 129, 1, 2900, 256, 128, 700]
 
 
-@pytest.mark.parametrize("i,o", [(200, 4104), (64, 4104), (136, 8200), (2056, 1032)])
+@pytest.mark.parametrize("i,o", [(200, 4104), (64, 4104), (136, 8200), (2056, 1032), (1029, 2050)])
 @pytest.mark.parametrize("lead,tail", [(0, 0), (7, 9)])
 def test_large_forward(i, o, lead, tail):
     require_gpu()
@@ -292,7 +292,7 @@ def test_large_forward(i, o, lead, tail):
     _forward_gated(Problem(51, RAGGED, i, o // 2, lead, tail), ACTS[(i + 2) % 5], lead == 0)
 
 
-@pytest.mark.parametrize("i,o", [(4104, 200), (4104, 201), (8200, 64), (2056, 1027)])
+@pytest.mark.parametrize("i,o", [(4104, 200), (4104, 201), (8200, 64), (2056, 1027), (4099, 1031)])
 @pytest.mark.parametrize("lead,tail", [(0, 0), (7, 9)])
 def test_large_backward(i, o, lead, tail):
     require_gpu()
