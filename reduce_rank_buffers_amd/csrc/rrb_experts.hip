@@ -405,9 +405,9 @@ __device__ __forceinline__ Place place_weight(const ProductArgs &p) {
 // CUs got two tiles to do: 512 rows in each of 16 groups, one tile per CU, 185
 // -> 105 us).  Every wave counts by itself, 64 groups at a time.  LIGHT: tiles
 // of at most so many rows cost half of a whole one and come last, where they
-// fill the CUs that the whole ones leave (304 tiles of 112 steps on 256 CUs,
-// two fifths of them light: 351 -> 250 us).  Tiles are ordered in bands of four
-// row tiles, columns in turn, and dealt to the XCDs in runs of p.bm.
+// fill the CUs that the whole ones leave (an input gradient of 12007 rows in
+// seven groups: 522 -> 498 us).  Tiles are ordered in bands of four row tiles,
+// columns in turn, and dealt to the XCDs in runs of p.bm.
 template <int BM, int NCOLS, int LIGHT, int FORM>
 __device__ __forceinline__ Place place_counted(const ProductArgs &p) {
   Place none;
@@ -530,7 +530,9 @@ __device__ __forceinline__ bool gated_up(int j) { return j & 16; }
 
 // Operands whose rows do not start on 16-byte boundaries: tiles go through
 // registers, with 16-byte loads that need no alignment and the last, partial
-// chunk of a row read element by element.
+// chunk of a row read element by element.  Bound by those loads and the one
+// step that they are ahead: 0.5 PFLOP/s on 8 groups of 1024 rows, 4095 x 4096
+// (1.2 where rows are aligned).
 template <int BM, int BN, int WR, int WC, int FORM, bool GATED>
 __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
   constexpr int NT = WR * WC * 64;
@@ -638,6 +640,14 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
 // results are not stored); chunks past the reduction's end, and rows of a
 // column tile past it, lie outside the descriptor and arrive as zeros, on both
 // sides, so that nothing behind a group reaches its sums.
+//
+// Small tiles, for few rows or few tiles: STAGES - 1 steps of loads in flight
+// and one barrier a step.  64 x 64 in five stages (two workgroups a CU) streams
+// the weights of 24 single-row groups at 6.1 TB/s (7168 -> 2048 gated, 231 us;
+// the 256 x 256 kernel 335); 64 x 256 in three stages covers 64 rows in each of
+// 16 groups, 4096 -> 2048, in 58 us (64 x 64 79, 256 x 256 74).  Four stages of
+// 32 x 128, eight to twelve of 32 x 64 and 128 x 256 in three were within 10% of
+// these or behind.
 
 __device__ __forceinline__ u32x4_t descriptor(const uint16_t *base, int bytes) {
   const uint64_t v = reinterpret_cast<uint64_t>(uniform(base));
@@ -654,7 +664,8 @@ __device__ __forceinline__ int lds_address(const unsigned char *lds) {
 // 16 bytes per lane from `d` at voffset + soffset to LDS address `at` (the
 // wave's first byte, uniform) + 16 * lane.  As assembly, because the compiler
 // would wait for every such load in flight before it reads any LDS
-// transposed; the kernels wait themselves, by count.
+// transposed; the kernels wait themselves, by count.  (m0 is reserved: the
+// compiler keeps nothing in it from one use to the next.)
 __device__ __forceinline__ void load_to_lds(u32x4_t d, int at, int voffset, int soffset) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
@@ -816,6 +827,10 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 // (zeros, no memory access), so the count holds to the last step.  A tile of at
 // most 128 valid rows loads nothing for A1 and leaves out its reads and
 // products, so it costs half the matrix instructions of a whole one.
+// Measured: 1.24 to 1.34 PFLOP/s (8192 x 8192 outputs, 8192 and 4096 deep, random
+// data; 1.74 on zeros: the clock falls to 2.0 GHz under load), matrix cores busy
+// 60% of the time in a 4096-deep gated forward; tiles of few steps are bound by
+// their first loads and results, about 13 us a tile together.
 
 // Row of B (column of the output) that sits at row r of half h of a row region.
 // Sixteen rows make a fragment and a lane holds four consecutive ones of each;
@@ -1050,8 +1065,9 @@ struct ActGradArgs {
 };
 
 // dG = dH * U * act'(G), dU = dH * act(G) (linear: dZ = dY * act'(pre)), one
-// 8-column chunk per thread, rows of groups only.  Memory-bound; the results
-// are rounded to bf16, as the matrix instructions take them.  Columns up to
+// 8-column chunk per thread, rows of groups only.  Memory-bound: 12007 x 2001
+// gated, 240 MB in 48 us (5.0 TB/s).  The results are rounded to bf16, as the
+// matrix instructions take them.  Columns up to
 // the pitch are written as 0, so the products that reduce over them read
 // zeros and not what the workspace held.
 template <int ACT, bool GATED>
@@ -1093,7 +1109,8 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs p) {
 }
 
 // db[e][n] = the sum of dZ's rows of group e: 64 columns per workgroup, eight
-// lanes wide and 32 rows deep, fp32.
+// lanes wide and 32 rows deep, fp32.  Bound by reading dZ: 8192 x 7168 in 16
+// groups, 117 MB in 31 us.
 struct BiasGradArgs {
   const uint16_t *dz;
   uint16_t *db;
@@ -1174,8 +1191,8 @@ rrb_status launch_tiles(void (*kernel)(ProductArgs), int threads, ProductArgs p,
 // at a time: rounds of tiles of so many steps, `step` each, and `rest` per tile
 // (first loads, results); no less than moving the operands from the L2s takes
 // at 10 TB/s, nor than moving the weights (or their gradients) from or to HBM
-// at 5.5 TB/s.  The rates are measured; what counts is which
-// shape comes out first.
+// at 5.5 TB/s.  The rates are measured; what counts is which shape comes out
+// first.
 template <int FORM, bool GATED>
 double estimate(const ProductArgs &p, int bm, int bn, int resident, double step, double rest) {
   constexpr double kCus = 256;
