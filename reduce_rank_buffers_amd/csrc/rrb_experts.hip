@@ -665,12 +665,25 @@ __device__ __forceinline__ int lds_address(const unsigned char *lds) {
 // wave's first byte, uniform) + 16 * lane.  As assembly, because the compiler
 // would wait for every such load in flight before it reads any LDS
 // transposed; the kernels wait themselves, by count.  (m0 is reserved: the
-// compiler keeps nothing in it from one use to the next.)
+// compiler keeps nothing in it from one use to the next.  The five wait states
+// stand between a vector instruction that may just have written the scalar
+// operands and the load that reads them; the compiler sees to that only for
+// instructions of its own.)
 __device__ __forceinline__ void load_to_lds(u32x4_t d, int at, int voffset, int soffset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(uniform(at)), "v"(voffset), "s"(d), "s"(uniform(soffset))
                : "memory");
+}
+
+// Two such loads, 8 KiB apart in LDS, behind one set of wait states.
+__device__ __forceinline__ void load_two_to_lds(u32x4_t d, int at, int voffset0, int voffset1, int soffset) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %4, %5 offen lds\n\t"
+      "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %4, %5 offen lds"
+      :
+      : "s"(uniform(at)), "s"(uniform(at + 8192)), "v"(voffset0), "v"(voffset1), "s"(d), "s"(uniform(soffset))
+      : "memory");
 }
 
 template <int BM, int BN, int WR, int WC, int STAGES, int FORM, bool GATED>
@@ -888,13 +901,11 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
     const bool live = step < steps;
     if (A_COL) {
       const auto d = descriptor(t.a[0] + k0 * p.lda, live && (h == 0 || both) ? rows * lda2 - t.m0 * 2 : 0);
-      load_to_lds(d, dst, va[h][0], 0);
-      load_to_lds(d, dst + 8192, va[h][1], 0);
+      load_two_to_lds(d, dst, va[h][0], va[h][1], 0);
     } else {
       const auto d = descriptor(t.a[ph], live && (h == 0 || both) ? t.mvalid * lda2 : 0);
       const bool out = left < kStep && ch * 8 >= left;
-      load_to_lds(d, dst, out ? kOutside : va[h][0], ks * 128);
-      load_to_lds(d, dst + 8192, out ? kOutside : va[h][1], ks * 128);
+      load_two_to_lds(d, dst, out ? kOutside : va[h][0], out ? kOutside : va[h][1], ks * 128);
     }
   };
   auto start_b = [&](int step, int h) {
@@ -906,16 +917,14 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
     const bool live = step < steps;
     if (B_COL) {
       const auto d = descriptor(t.b[ph] + k0 * p.ldb, live ? rows * ldb2 - t.n0 * 2 : 0);
-      load_to_lds(d, dst, vb[h][0], 0);
-      load_to_lds(d, dst + 8192, vb[h][1], 0);
+      load_two_to_lds(d, dst, vb[h][0], vb[h][1], 0);
     } else {
       // The wave's eight rows are all gate rows or all up rows.
       const bool up = GATED && (wave & 2);
       const int cols = p.n - t.n0 < NCOLS ? p.n - t.n0 : NCOLS;
       const auto d = descriptor(up ? t.b[1] : t.b[0], live ? cols * ldb2 : 0);
       const bool out = left < kStep && ch * 8 >= left;
-      load_to_lds(d, dst, out ? kOutside : vb[h][0], ks * 128);
-      load_to_lds(d, dst + 8192, out ? kOutside : vb[h][1], ks * 128);
+      load_two_to_lds(d, dst, out ? kOutside : vb[h][0], out ? kOutside : vb[h][1], ks * 128);
     }
   };
 
