@@ -639,7 +639,10 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs p) {
 // lane reads.  Rows past a tile's last valid one read that row again (their
 // results are not stored); chunks past the reduction's end, and rows of a
 // column tile past it, lie outside the descriptor and arrive as zeros, on both
-// sides, so that nothing behind a group reaches its sums.
+// sides, so that nothing behind a group reaches its sums.  The range check is of
+// a lane's own offset, the scalar offset left out or taken off the descriptor's
+// size first; so that an empty descriptor holds either way (0 less an offset
+// must not wrap to a large size), loads through one have a scalar offset of 0.
 //
 // Small tiles, for few rows or few tiles: STAGES - 1 steps of loads in flight
 // and one barrier a step.  64 x 64 in five stages (two workgroups a CU) streams
@@ -738,6 +741,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
     const int k0 = kstep * kStep;
     const int left = klen - k0;
     const bool live = step < steps;
+    const int along = live ? kstep * 128 : 0;
     const int rows = left < kStep ? left : kStep;  // of the column tiles
     const int ta = lds_address(lds) + buf * (A_BYTES + B_BYTES) + wave * 1024, tb = ta + A_BYTES;
     if (A_COL) {
@@ -754,7 +758,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
           const int id = i * NT + tid;
           if (((id & 7) ^ row_swizzle(id >> 3)) * 8 >= left) v = kOutside;
         }
-        load_to_lds(d, ta + i * NT * 16, v, kstep * 128);
+        load_to_lds(d, ta + i * NT * 16, v, along);
       }
     }
     if (B_COL) {
@@ -775,7 +779,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
         }
         // The wave's eight rows are all gate rows or all up rows.
         const bool up = GATED && gated_up((i * NT + wave * 64) >> 3);
-        load_to_lds(up ? d1 : d0, tb + i * NT * 16, v, kstep * 128);
+        load_to_lds(up ? d1 : d0, tb + i * NT * 16, v, along);
       }
     }
   };
@@ -903,9 +907,10 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
       const auto d = descriptor(t.a[0] + k0 * p.lda, live && (h == 0 || both) ? rows * lda2 - t.m0 * 2 : 0);
       load_two_to_lds(d, dst, va[h][0], va[h][1], 0);
     } else {
-      const auto d = descriptor(t.a[ph], live && (h == 0 || both) ? t.mvalid * lda2 : 0);
+      const bool any = live && (h == 0 || both);
+      const auto d = descriptor(t.a[ph], any ? t.mvalid * lda2 : 0);
       const bool out = left < kStep && ch * 8 >= left;
-      load_two_to_lds(d, dst, out ? kOutside : va[h][0], out ? kOutside : va[h][1], ks * 128);
+      load_two_to_lds(d, dst, out ? kOutside : va[h][0], out ? kOutside : va[h][1], any ? ks * 128 : 0);
     }
   };
   auto start_b = [&](int step, int h) {
@@ -924,7 +929,7 @@ __device__ __forceinline__ void product_turns_tile(const ProductArgs &p, const P
       const int cols = p.n - t.n0 < NCOLS ? p.n - t.n0 : NCOLS;
       const auto d = descriptor(up ? t.b[1] : t.b[0], live ? cols * ldb2 : 0);
       const bool out = left < kStep && ch * 8 >= left;
-      load_two_to_lds(d, dst, out ? kOutside : vb[h][0], out ? kOutside : vb[h][1], ks * 128);
+      load_two_to_lds(d, dst, out ? kOutside : vb[h][0], out ? kOutside : vb[h][1], live ? ks * 128 : 0);
     }
   };
 
