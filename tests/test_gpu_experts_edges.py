@@ -44,3 +44,24 @@ def test_short_reductions(sizes, o, i, monkeypatch):
     T._forward_gated(T.Problem(61, sizes, i, o // 2), "silu", True)
     T._backward_linear(T.Problem(62, sizes, o, i), "relu")
     T._backward_gated(T.Problem(63, sizes, o, i), "silu")
+
+
+def test_gelu_far_tail():
+    """x Phi(x) and its slope relative to themselves, for every bf16 from -12.5
+    to -1/16.  Phi within 1.1e-6 of the formula and z^2, z = |x| / sqrt 2 <= 8.9,
+    rounded to fp32 three times before e^(-z^2): 79 * 2^-22 and the
+    exponential's own argument, 114 * 2^-24, together below 2^-14; the slope's
+    two terms likewise, and one rounding to bf16 each."""
+    require_gpu()
+    bits = torch.arange(0xBD80, 0xC149, dtype=torch.int32).to(torch.int16)
+    x = bits.view(BF).reshape(-1, 1).to(DEV)
+    one = torch.ones(1, 1, 1, dtype=BF, device=DEV)
+    y, d_x = torch.empty_like(x), torch.empty_like(x)
+    T.rrb.expert_linear(x, None, one, y, activation="gelu")
+    T.rrb.expert_linear_backward(torch.ones_like(x), x, None, one, pre=x, activation="gelu", d_x=d_x)
+    nx = T._np(x)
+    assert nx.min() == -12.5 and nx.max() == -0.0625
+    want, slope = T.OE.act("gelu", nx), T.OE.act_grad("gelu", nx)
+    T._check("act", y, want, 2.0 ** -14 * np.abs(want))
+    phi = want / nx
+    T._check("slope", d_x, slope, 2.0 ** -14 * (phi + np.abs(slope - phi)))
