@@ -397,7 +397,8 @@ rrb_status rrb_expert_linear(const rrb_expert_spec *spec, const void *d_x, const
 /* Its gradients; each of d_dx, d_dw, d_dbias may be NULL (not computed), not
  * all.  d_pre is the saved pre-activation (not read without an activation).
  * The residual's gradient is d_dout itself.  dw and dbias of a group without
- * rows are written as 0.  Workspace as above. */
+ * rows are written as 0.  For dx and dw an activation's gradient d_dout * act'
+ * is held in bf16 in d_workspace (as above); dbias sums it in fp32. */
 rrb_status rrb_expert_linear_backward_workspace(const rrb_expert_spec *spec, size_t *bytes);
 rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d_dout, const void *d_x,
                                       const int32_t *d_offsets, const void *d_w, const void *d_pre,

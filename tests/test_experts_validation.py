@@ -293,3 +293,13 @@ def test_workspace_sizes(librrb):
     assert rrb.expert_gated_backward_workspace(10, 4, 13, 2) == 10 * 16 * 2 * 2
     assert rrb.expert_linear_backward_workspace(10, 4, 13, 2) >= 10 * 16 * 2
     assert rrb.expert_gated_backward_workspace(0, 4, 13, 2) == 0
+
+
+def test_linear_backward_workspace_holds_the_bias_sums(librrb):
+    """Where a bias gradient's rows are split, its fp32 sums have room behind
+    dZ, and a workspace without it is refused."""
+    n = rrb.expert_linear_backward_workspace(32768, 8, 64, 1)
+    assert n == 32768 * 64 * 2 + 64 * 64 * 4
+    a = at(9)
+    assert librrb.rrb_expert_linear_backward(_spec(rows=32768, o=64), *a, n - 1, None) == L.RRB_EINVAL
+    assert b"workspace of" in librrb.rrb_last_error()

@@ -65,3 +65,64 @@ def test_gelu_far_tail():
     T._check("act", y, want, 2.0 ** -14 * np.abs(want))
     phi = want / nx
     T._check("slope", d_x, slope, 2.0 ** -14 * (phi + np.abs(slope - phi)))
+
+
+@pytest.mark.parametrize("name", T.ACTS)
+@pytest.mark.parametrize("o", [64, 37])
+def test_bias_gradient_of_cancelling_rows(name, o):
+    """Column sums that nearly cancel: 100 rows of dZ = dY act'(pre), and three
+    more that take their sum back to 2^-20 of it.  dZ in fp32 is off by 2^-19
+    (1 + |pre|) |dY|, a sum of N terms by N 2^-24 of their magnitudes' in any
+    order; rounding each dZ to bf16 first would be off by 40 times as
+    much and more."""
+    require_gpu()
+    rng = T._rng(64, o)
+    rows, G = 100, 2
+    off = np.array([0, rows + 3, 2 * (rows + 3)], np.int32)
+    N = int(off[-1])
+    bf = lambda a: torch.from_numpy(a).to(BF).double().numpy()
+    d, pre = bf(rng.standard_normal((N, o))), bf(rng.standard_normal((N, o)))
+    slope = lambda: T.OE.act_grad(name, pre)
+    for e in range(G):
+        r = slice(int(off[e]), int(off[e + 1]))
+        pre[r][rows:] = 4.0
+        d[r][rows:] = 0.0
+        for q in range(3):
+            d[r][rows + q] = bf(-(d[r] * slope()[r]).sum(axis=0) / slope()[r][rows + q])
+    x, w = torch.ones(N, 8, dtype=BF, device=DEV), torch.ones(G, o, 8, dtype=BF, device=DEV)
+    put = lambda a: torch.from_numpy(a).to(BF).to(DEV)
+    d_b = torch.full((G, o), -7.25, dtype=BF, device=DEV)
+    T.rrb.expert_linear_backward(put(d), x, put_off(off), w, pre=put(pre), activation=name, d_bias=d_b)
+    dz = d * slope()
+    sums = lambda a: np.stack([a[int(off[e]):int(off[e + 1])].sum(axis=0) for e in range(G)])
+    assert (np.abs(sums(dz)) <= 2.0 ** -20 * sums(np.abs(dz))).all()
+    bound = 2.0 ** -19 * sums(np.abs(d) * (1 + np.abs(pre))) + (rows + 3) * 2.0 ** -24 * sums(np.abs(dz))
+    T._check("d_bias", d_b, sums(dz), bound)
+
+
+def put_off(off):
+    return torch.from_numpy(off).to(DEV)
+
+
+@pytest.mark.parametrize("name", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("sizes,o", [([20000, 0, 1, 3000], 64), ([5000], 37), ([300] * 12, 130), ([9000, 40], 8)])
+@pytest.mark.parametrize("lead,tail", [(0, 0), (3, 5)])
+def test_bias_gradient_of_long_groups(name, sizes, o, lead, tail):
+    """Groups whose rows are split over workgroups, alone and with the other
+    gradients: the same bits, from call to call too."""
+    require_gpu()
+    p = T.Problem(65, sizes, 8, o, lead=lead, tail=tail)
+    T._backward_linear(p, name)
+    d, pre = p.rows(o), p.rows(o)
+    got = [p.out(p.G, o) for _ in range(3)]
+    d_x, d_w = p.out(p.N, 8), p.out(p.G, o, 8)
+    for q, kw in zip(got, ({}, {"d_x": d_x, "d_w": d_w}, {})):
+        T.rrb.expert_linear_backward(d, p.x, p.d_off, p.w, pre=pre, activation=name, d_bias=q, **kw)
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    nd = T._np(d)
+    err = np.zeros_like(nd)
+    if name != "none":
+        err = np.abs(nd) * T.ACT * (1 + np.abs(T._np(pre)))
+        nd = nd * T.OE.act_grad(name, T._np(pre))
+    sums = lambda a: np.stack([np.nan_to_num(a[p.off[e]:p.off[e + 1]]).sum(axis=0) for e in range(p.G)])
+    T._check("d_bias", got[0], sums(nd), sums(err) + (np.diff(p.off).max() + 64) * 2.0 ** -24 * sums(np.abs(nd)))
