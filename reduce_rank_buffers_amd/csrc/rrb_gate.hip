@@ -304,10 +304,27 @@ rrb_status gate(const GateArgs &a, int32_t dtype, uint32_t flags, bool back, rrb
                                              : gate_pick<float, 1>(a, back, &lanes))
                                      : (wide ? gate_pick<uint16_t, kPerLoad<uint16_t>>(a, back, &lanes)
                                              : gate_pick<uint16_t, 1>(a, back, &lanes));
-  const int64_t blocks = (a.tokens + 256 / lanes - 1) / (256 / lanes);
-  hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? RRB_OK : fail(RRB_EHIP, "gate launch: %s", hipGetErrorString(e));
+  // A launch's threads are counted in 32 bits: 2^23 tokens (at most 2^29
+  // threads) at a time.
+  constexpr int64_t kMost = 1 << 23;
+  const int64_t row = a.experts * static_cast<int64_t>(dtype == RRB_F32 ? 4 : 2);
+  for (int64_t first = 0; first < a.tokens; first += kMost) {
+    GateArgs b = a;
+    b.tokens = a.tokens - first < kMost ? a.tokens - first : kMost;
+    b.logits = static_cast<const char *>(a.logits) + first * row;
+    b.idx += first * a.topk;
+    if (back) {
+      b.dw += first * a.topk;
+      b.dlogits = static_cast<char *>(a.dlogits) + first * row;
+    } else {
+      b.w += first * a.topk;
+    }
+    const int64_t blocks = (b.tokens + 256 / lanes - 1) / (256 / lanes);
+    hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream), b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(RRB_EHIP, "gate launch: %s", hipGetErrorString(e));
+  }
+  return RRB_OK;
 }
 
 }  // namespace

@@ -126,3 +126,33 @@ def test_bias_gradient_of_long_groups(name, sizes, o, lead, tail):
         nd = nd * T.OE.act_grad(name, T._np(pre))
     sums = lambda a: np.stack([np.nan_to_num(a[p.off[e]:p.off[e + 1]]).sum(axis=0) for e in range(p.G)])
     T._check("d_bias", got[0], sums(nd), sums(err) + (np.diff(p.off).max() + 64) * 2.0 ** -24 * sums(np.abs(nd)))
+
+
+def test_gate_of_the_most_tokens():
+    """2^26 - 1 tokens, the most that the gate takes, at a wave per token: a
+    score of 1 in a row of zeros, at a different expert for each token.  Weights
+    and gradients are then two values each, known to E 2^-23 relative (the bound
+    of tests/test_gpu_experts.py's gate); bf16 gradients add half a step."""
+    require_gpu()
+    N, E = (1 << 26) - 1, 264
+    T._say(f"gate of {N} tokens, {N * E * 2 >> 30} GiB of scores, twice")
+    hot = (torch.arange(N, dtype=torch.int32, device=DEV) * 7 % E).reshape(N, 1)
+    logits, d_logits = torch.zeros(N, E, dtype=BF, device=DEV), torch.empty(N, E, dtype=BF, device=DEV)
+    step = 1 << 22
+    for a in range(0, N, step):
+        logits[a:a + step].scatter_(1, hot[a:a + step].long(), 1.0)
+    idx, w = torch.full((N, 1), -1, dtype=torch.int32, device=DEV), torch.full((N, 1), -1.0, device=DEV)
+    T.rrb.moe_gate(logits, idx, w)
+    assert torch.equal(idx, hot)
+    p = np.e / (np.e + E - 1)
+    rel = (E + 10) * 2.0 ** -23
+    assert abs(w.min().item() - p) <= rel * p and abs(w.max().item() - p) <= rel * p
+    T.rrb.moe_gate_backward(logits, idx, torch.ones_like(w), d_logits)
+    other = p / np.e * -p
+    for a in range(0, N, step):
+        d, h = d_logits[a:a + step], hot[a:a + step].long()
+        for got, want in ((d.gather(1, h), p * (1 - p)), (d.scatter_(1, h, d[0, (h[0, 0] + 1) % E].item()), other)):
+            for v in (got.min().item(), got.max().item()):
+                assert abs(v - want) <= (T.HALF + 6 * rel) * abs(want), (a, v, want)
+    del logits, d_logits, d
+    torch.cuda.empty_cache()
