@@ -298,7 +298,8 @@ rrb_status rrb_empty_kernel(rrb_stream_t stream);
  * are left (a row of -inf alone: experts 0..topk-1 with weight 0).  Scores of
  * +inf share the weight equally.  NaN ranks above every number and makes the
  * row's weights NaN; the experts stay distinct and in range.  experts <= 1024,
- * topk <= 16, tokens < 2^26 (RRB_EUNSUPPORTED otherwise).  Asynchronous on `stream`.
+ * topk <= 16, tokens < 2^26 (RRB_EUNSUPPORTED otherwise).  Outputs must not overlap
+ * the scores or each other (RRB_EINVAL).  Asynchronous on `stream`.
  */
 #define RRB_GATE_RENORMALIZE 1u
 rrb_status rrb_moe_gate(int64_t tokens, int32_t experts, int32_t topk, int32_t dtype,
@@ -312,6 +313,8 @@ rrb_status rrb_moe_gate(int64_t tokens, int32_t experts, int32_t topk, int32_t d
  * RRB_GATE_RENORMALIZE dl_i = w_i (dw_i - sum w dw) for the chosen and 0 for the
  * others.  Masked experts get 0 and their dw is not used.  d_topk_idx holds
  * distinct experts per row; entries outside 0..experts-1 are passed over.
+ * d_dlogits must not overlap the inputs (RRB_EINVAL), except that it may be
+ * d_logits.
  */
 rrb_status rrb_moe_gate_backward(int64_t tokens, int32_t experts, int32_t topk, int32_t dtype,
                                  uint32_t flags, const void *d_logits, const int32_t *d_topk_idx,

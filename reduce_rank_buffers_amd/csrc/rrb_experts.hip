@@ -1322,27 +1322,6 @@ rrb_status check_spec(const rrb_expert_spec *s, const int32_t *offsets) {
   return RRB_OK;
 }
 
-// A buffer of a call: outputs must not share memory with any other.
-struct Span {
-  const void *at;
-  int64_t bytes;
-  const char *name;
-  bool out;
-};
-
-template <int N>
-rrb_status check_disjoint(const Span (&s)[N]) {
-  for (int i = 0; i < N; ++i) {
-    for (int j = 0; j < i; ++j) {
-      if ((!s[i].out && !s[j].out) || !s[i].at || !s[j].at) continue;
-      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].at), b = reinterpret_cast<uintptr_t>(s[j].at);
-      if (a < b + static_cast<uintptr_t>(s[j].bytes) && b < a + static_cast<uintptr_t>(s[i].bytes))
-        return fail(RRB_EINVAL, "%s overlaps %s", s[i].name, s[j].name);
-    }
-  }
-  return RRB_OK;
-}
-
 // Bytes of the arrays that the sizes name.
 struct Bytes {
   int64_t x, y, w, bias, offsets;

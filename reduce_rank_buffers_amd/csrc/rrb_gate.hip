@@ -295,6 +295,17 @@ rrb_status gate(const GateArgs &a, int32_t dtype, uint32_t flags, bool back, rrb
   if (a.tokens >= 1LL << 26) return fail(RRB_EUNSUPPORTED, "tokens %lld >= 2^26", (long long)a.tokens);
   if (a.tokens == 0) return RRB_OK;
   if (!a.logits || !a.idx || (back ? !a.dw || !a.dlogits : !a.w)) return fail(RRB_EINVAL, "NULL array");
+  const int64_t row = a.experts * static_cast<int64_t>(elem_size(dtype));
+  const int64_t scores = a.tokens * row, chosen = a.tokens * a.topk * 4;
+  // A token's scores are read before its gradients are written, by one wave:
+  // the gradients may take the scores' place.
+  const Span spans[] = {{a.dlogits == a.logits ? nullptr : a.logits, scores, "logits", false},
+                        {a.idx, chosen, "topk_idx", !back},
+                        {a.w, chosen, "topk_w", true},
+                        {a.dw, chosen, "dtopk_w", false},
+                        {a.dlogits, scores, "dlogits", true}};
+  const rrb_status st = check_disjoint(spans);
+  if (st != RRB_OK) return st;
   // Whole 16-byte loads where every row starts on such a boundary.
   const int per = dtype == RRB_F32 ? kPerLoad<float> : kPerLoad<uint16_t>;
   const bool wide = a.experts % per == 0 &&
@@ -307,7 +318,6 @@ rrb_status gate(const GateArgs &a, int32_t dtype, uint32_t flags, bool back, rrb
   // A launch's threads are counted in 32 bits: 2^23 tokens (at most 2^29
   // threads) at a time.
   constexpr int64_t kMost = 1 << 23;
-  const int64_t row = a.experts * static_cast<int64_t>(dtype == RRB_F32 ? 4 : 2);
   for (int64_t first = 0; first < a.tokens; first += kMost) {
     GateArgs b = a;
     b.tokens = a.tokens - first < kMost ? a.tokens - first : kMost;

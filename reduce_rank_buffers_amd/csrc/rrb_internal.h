@@ -17,6 +17,27 @@ rrb_status fail(rrb_status s, const char *fmt, ...);
 // Clears the thread's last-error text.
 void clear_error();
 
+// A buffer of a call: outputs must not share memory with any other.
+struct Span {
+  const void *at;  // NULL: not there
+  int64_t bytes;
+  const char *name;
+  bool out;
+};
+
+template <int N>
+rrb_status check_disjoint(const Span (&s)[N]) {
+  for (int i = 0; i < N; ++i) {
+    for (int j = 0; j < i; ++j) {
+      if ((!s[i].out && !s[j].out) || !s[i].at || !s[j].at) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].at), b = reinterpret_cast<uintptr_t>(s[j].at);
+      if (a < b + static_cast<uintptr_t>(s[j].bytes) && b < a + static_cast<uintptr_t>(s[i].bytes))
+        return fail(RRB_EINVAL, "%s overlaps %s", s[i].name, s[j].name);
+    }
+  }
+  return RRB_OK;
+}
+
 inline int elem_size(int32_t dtype) { return dtype == RRB_F32 ? 4 : 2; }
 
 // An index-map entry at element granularity (the same fields rrb_segment

@@ -84,7 +84,8 @@ def moe_gate(logits, topk_idx, topk_w, renormalize=False, stream=None):
 
 def moe_gate_backward(logits, topk_idx, d_topk_w, d_logits, renormalize=False, stream=None):
     """The scores' gradient from the weights': d_topk_w float32 [T, k] ->
-    d_logits [T, E] of the scores' type, for moe_gate's logits and topk_idx."""
+    d_logits [T, E] of the scores' type (may be logits itself), for moe_gate's
+    logits and topk_idx."""
     T, E, k = _gate_sizes(logits, topk_idx)
     dt = _dtype_of(logits)
     named = [_shaped(logits, "logits", (T, E), (logits.dtype,)),

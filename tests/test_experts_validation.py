@@ -303,3 +303,22 @@ def test_linear_backward_workspace_holds_the_bias_sums(librrb):
     a = at(9)
     assert librrb.rrb_expert_linear_backward(_spec(rows=32768, o=64), *a, n - 1, None) == L.RRB_EINVAL
     assert b"workspace of" in librrb.rrb_last_error()
+
+
+def test_abi_gate_refuses_overlaps(librrb):
+    """An output that shares its last or first byte with an input or the other
+    output."""
+    T, E, k = 5, 8, 2
+    for dt, scores in ((L.RRB_BF16, T * E * 2), (L.RRB_F32, T * E * 4)):
+        chosen = T * k * 4
+        for call, sizes, outs in ((librrb.rrb_moe_gate, [scores, chosen, chosen], (1, 2)),
+                                  (librrb.rrb_moe_gate_backward, [scores, chosen, chosen, scores], (3,))):
+            for o in outs:
+                for i in range(len(sizes)):
+                    if i == o:
+                        continue
+                    for shift in (sizes[i] - 1, 1 - sizes[o]):
+                        a = at(len(sizes))
+                        a[o] = a[i] + shift
+                        assert call(T, E, k, dt, 0, *a, None) == L.RRB_EINVAL
+                        assert b"overlaps" in librrb.rrb_last_error()

@@ -156,3 +156,31 @@ def test_gate_of_the_most_tokens():
                 assert abs(v - want) <= (T.HALF + 6 * rel) * abs(want), (a, v, want)
     del logits, d_logits, d
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gate_gradients_in_the_scores_place(dtype, renorm):
+    require_gpu()
+    for N, E, k in T.GATES:
+        logits = T._scores(N, E, "masked", dtype).to(DEV)
+        idx, w = torch.empty(N, k, dtype=torch.int32, device=DEV), torch.empty(N, k, device=DEV)
+        T.rrb.moe_gate(logits, idx, w, renormalize=renorm)
+        d_w = torch.from_numpy(T._rng(66, N, E).standard_normal((N, k)).astype(np.float32)).to(DEV)
+        want = torch.empty_like(logits)
+        T.rrb.moe_gate_backward(logits, idx, d_w, want, renormalize=renorm)
+        T.rrb.moe_gate_backward(logits, idx, d_w, logits, renormalize=renorm)
+        assert torch.equal(logits, want), (N, E, k)
+
+
+def test_gate_refuses_overlaps():
+    require_gpu()
+    buf = torch.zeros(4096, device=DEV)
+    logits = buf[:1024].reshape(16, 64)
+    idx, w = torch.zeros(16, 4, dtype=torch.int32, device=DEV), torch.zeros(16, 4, device=DEV)
+    for call in (lambda: T.rrb.moe_gate(logits, idx, buf[1000:1064].reshape(16, 4)),
+                 lambda: T.rrb.moe_gate(logits, idx, idx.view(torch.float32)),
+                 lambda: T.rrb.moe_gate_backward(logits, idx, w, buf[64:1088].reshape(16, 64))):
+        with pytest.raises(T.rrb.RrbError) as e:
+            call()
+        assert "overlaps" in str(e.value)
