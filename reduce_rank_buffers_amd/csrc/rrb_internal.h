@@ -20,7 +20,7 @@ void clear_error();
 // A buffer of a call: outputs must not share memory with any other.
 struct Span {
   const void *at;  // NULL: not there
-  int64_t bytes;
+  int64_t bytes;   // 0: shares nothing, wherever it is
   const char *name;
   bool out;
 };
@@ -29,7 +29,7 @@ template <int N>
 rrb_status check_disjoint(const Span (&s)[N]) {
   for (int i = 0; i < N; ++i) {
     for (int j = 0; j < i; ++j) {
-      if ((!s[i].out && !s[j].out) || !s[i].at || !s[j].at) continue;
+      if ((!s[i].out && !s[j].out) || !s[i].at || !s[j].at || !s[i].bytes || !s[j].bytes) continue;
       const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].at), b = reinterpret_cast<uintptr_t>(s[j].at);
       if (a < b + static_cast<uintptr_t>(s[j].bytes) && b < a + static_cast<uintptr_t>(s[i].bytes))
         return fail(RRB_EINVAL, "%s overlaps %s", s[i].name, s[j].name);

@@ -322,3 +322,10 @@ def test_abi_gate_refuses_overlaps(librrb):
                         a[o] = a[i] + shift
                         assert call(T, E, k, dt, 0, *a, None) == L.RRB_EINVAL
                         assert b"overlaps" in librrb.rrb_last_error()
+
+
+def test_abi_takes_empty_arrays_anywhere(librrb):
+    """Without rows x, dx and dout are empty: where they lie does not matter."""
+    s, w = _spec(rows=0, i=8, o=16, G=2), P + 64
+    assert librrb.rrb_expert_linear_backward(s, w, w, P << 20, P, w, w, None, None, None, 0, None) == L.RRB_OK
+    assert librrb.rrb_expert_gated_backward(s, w, w, P << 20, P, P << 8, w, w, w, None, None, None, 0, None) == L.RRB_OK
