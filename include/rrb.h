@@ -324,8 +324,9 @@ rrb_status rrb_moe_gate_backward(int64_t tokens, int32_t experts, int32_t topk, 
  * Offsets of the experts' rows in a device-routed plan's arena, for the calls
  * below: d_offsets[experts + 1] (device) receives the first arena row of each
  * expert as the last rrb_moe_route placed it, then tokens*topk.  After a
- * failed routing all of them are 0 (no rows).  Asynchronous on `stream`, after
- * the route on the same stream.
+ * failed routing all of them are 0 (no rows).  They must not lie in the plan's
+ * workspace (RRB_EINVAL).  Asynchronous on `stream`, after the route on the
+ * same stream.
  */
 rrb_status rrb_moe_expert_offsets(rrb_plan_t plan, int32_t *d_offsets, rrb_stream_t stream);
 
@@ -336,7 +337,8 @@ rrb_status rrb_moe_expert_offsets(rrb_plan_t plan, int32_t *d_offsets, rrb_strea
  * d_dz[R]: the expert rows (the plan's inputs) and their gradients; d_weights
  * as for rrb_reduce; d_dweights[tokens][topk] in the routing arrays' order.
  * d_dz may be NULL (not computed), and so may d_dweights (then d_z is not
- * read and may be NULL), not both.  dz must not overlap dy or z.  A
+ * read and may be NULL), not both.  dz and dweights must not overlap each
+ * other, what the call reads or the plan's workspace (RRB_EINVAL).  A
  * dispatch's gradient is its combine with per-call weights of 1.
  */
 rrb_status rrb_moe_combine_backward(rrb_plan_t plan, const void *const *d_dy, const void *const *d_z,

@@ -153,6 +153,10 @@ rrb_status rrb_moe_expert_offsets(rrb_plan_t plan, int32_t *d_offsets, rrb_strea
   const Plan &p = plan->p;
   if (p.kind != PlanKind::RowsDevice) return fail(RRB_EINVAL, "rrb_moe_expert_offsets needs a device row plan");
   if (!p.d_ws) return fail(RRB_EINVAL, "plan is not bound to a workspace");
+  const Span spans[] = {{p.d_ws, static_cast<int64_t>(p.ws_bytes), "the plan's workspace", false},
+                        {d_offsets, (p.rows.experts + 1ll) * 4, "offsets", true}};
+  const rrb_status st = check_disjoint(spans);
+  if (st != RRB_OK) return st;
   return launch_expert_offsets(p, d_offsets, stream);
 }
 
@@ -166,13 +170,26 @@ rrb_status rrb_moe_combine_backward(rrb_plan_t plan, const void *const *d_dy, co
     return fail(RRB_EINVAL, "rrb_moe_combine_backward needs an MoE combine plan");
   if (!d_dz && !d_dweights) return fail(RRB_EINVAL, "no gradient asked for");
   if (p.rows.tokens > 0) {
-    if (!p.d_ws) return fail(RRB_EINVAL, "row plan is not bound to a workspace");
     if (!d_dy || (d_dweights && !d_z)) return fail(RRB_EINVAL, "NULL dy or z");
     for (int32_t r = 0; r < p.nranks; ++r) {
       if (p.out_count[r] && !d_dy[r]) return fail(RRB_EINVAL, "dy[%d] is NULL", r);
       if (p.in_count[r] && ((d_dweights && !d_z[r]) || (d_dz && !d_dz[r])))
         return fail(RRB_EINVAL, "z[%d] or dz[%d] is NULL", r, r);
     }
+    const int64_t entries = p.rows.tokens * p.rows.topk * 4;
+    Span spans[3 * RRB_MAX_RANKS + 3];
+    int n = 0;
+    for (int32_t r = 0; r < p.nranks; ++r) {
+      spans[n++] = {d_dy[r], p.out_count[r] * 2, "dy", false};
+      if (d_dweights) spans[n++] = {d_z[r], p.in_count[r] * 2, "z", false};
+      if (d_dz) spans[n++] = {d_dz[r], p.in_count[r] * 2, "dz", true};
+    }
+    spans[n++] = {d_weights, entries, "weights", false};
+    spans[n++] = {d_dweights, entries, "dweights", true};
+    spans[n++] = {p.d_ws, static_cast<int64_t>(p.ws_bytes), "the plan's workspace", false};
+    const rrb_status st = check_disjoint(spans, n);
+    if (st != RRB_OK) return st;
+    if (!p.d_ws) return fail(RRB_EINVAL, "row plan is not bound to a workspace");
   }
   return launch_combine_backward(p, d_dy, d_dweights ? d_z : nullptr, d_dz, d_weights, d_dweights, stream);
 }

@@ -25,9 +25,8 @@ struct Span {
   bool out;
 };
 
-template <int N>
-rrb_status check_disjoint(const Span (&s)[N]) {
-  for (int i = 0; i < N; ++i) {
+inline rrb_status check_disjoint(const Span *s, int n) {
+  for (int i = 0; i < n; ++i) {
     for (int j = 0; j < i; ++j) {
       if ((!s[i].out && !s[j].out) || !s[i].at || !s[j].at || !s[i].bytes || !s[j].bytes) continue;
       const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].at), b = reinterpret_cast<uintptr_t>(s[j].at);
@@ -36,6 +35,10 @@ rrb_status check_disjoint(const Span (&s)[N]) {
     }
   }
   return RRB_OK;
+}
+template <int N>
+rrb_status check_disjoint(const Span (&s)[N]) {
+  return check_disjoint(s, N);
 }
 
 inline int elem_size(int32_t dtype) { return dtype == RRB_F32 ? 4 : 2; }

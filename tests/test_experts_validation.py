@@ -329,3 +329,33 @@ def test_abi_takes_empty_arrays_anywhere(librrb):
     s, w = _spec(rows=0, i=8, o=16, G=2), P + 64
     assert librrb.rrb_expert_linear_backward(s, w, w, P << 20, P, w, w, None, None, None, 0, None) == L.RRB_OK
     assert librrb.rrb_expert_gated_backward(s, w, w, P << 20, P, P << 8, w, w, w, None, None, None, 0, None) == L.RRB_OK
+
+
+def test_abi_combine_backward_refuses_overlaps(librrb):
+    """dz or dw over one byte of dy, z, the weights, each other or another
+    rank's dz (host plan of 2 ranks, each with rows; the addresses are compared
+    before the plan's maps are asked for)."""
+    T, k, E, h = 4, 2, 4, 24
+    idx = (ctypes.c_int32 * (T * k))(0, 2, 1, 3, 0, 3, 1, 2)
+    w = (ctypes.c_float * (T * k))(*[0.5] * (T * k))
+    plan = ctypes.c_void_p()
+    assert librrb.rrb_plan_create_rows(2, T, h, E, k, idx, w, L.RRB_MOE_COMBINE, ctypes.byref(plan)) == L.RRB_OK
+    rows = T * k // 2 * h * 2  # two tokens of each expert: four rows a rank
+    size = [T // 2 * h * 2] * 2 + [rows] * 4 + [T * k * 4] * 2  # dy dy, z z, dz dz, weights, dw
+
+    def call(a):
+        return librrb.rrb_moe_combine_backward(plan, L.ptr_array(a[:2]), L.ptr_array(a[2:4]), L.ptr_array(a[4:6]),
+                                               a[6], a[7], None)
+
+    assert call(at(8)) == L.RRB_EINVAL and b"not bound" in librrb.rrb_last_error()
+    for o in (4, 5, 7):
+        for i in range(8):
+            if i != o:
+                for shift in (size[i] - 1, 0, 1 - size[o]):
+                    a = at(8)
+                    a[o] = a[i] + shift
+                    assert call(a) == L.RRB_EINVAL and b"overlaps" in librrb.rrb_last_error(), (o, i, shift)
+    a = at(8)
+    a[0] = a[1]  # inputs may share
+    assert call(a) == L.RRB_EINVAL and b"not bound" in librrb.rrb_last_error()
+    librrb.rrb_plan_destroy(plan)

@@ -184,3 +184,32 @@ def test_gate_refuses_overlaps():
         with pytest.raises(T.rrb.RrbError) as e:
             call()
         assert "overlaps" in str(e.value)
+
+
+def test_plans_refuse_overlaps():
+    """Offsets in a plan's workspace, and the combine's gradient over its
+    inputs, its weights or the workspace; neither call then writes."""
+    require_gpu()
+    N, h, E, k = 32, 64, 8, 2
+    rng = T._rng(67)
+    idx, w = torch.from_numpy(T._choices(rng, N, E, k)).to(DEV), torch.rand(N, k, device=DEV)
+    comb = T.rrb.MoeDevicePlan(1, N, h, E, k, "combine")
+    comb.route(idx, w)
+    dy, z = T._bf16(rng, (N, h)).to(DEV), T._bf16(rng, (N * k, h)).to(DEV)
+    dz, dw = torch.zeros_like(z), torch.zeros(N, k, device=DEV)
+    ws = comb._ws.view(torch.int32)
+    keep = comb._ws.clone()
+    at = ws.numel() // 2
+    calls = [lambda: comb.expert_offsets(ws[at:at + E + 1]),
+             lambda: comb.backward([dy], [z], [z], d_weights=dw),
+             lambda: comb.backward([z], None, [z]),
+             lambda: comb.backward([dy], [z], [dz], d_weights=w, weights=w),
+             lambda: comb.backward([dy], [z], [dz], d_weights=ws[at:at + N * k].view(torch.float32))]
+    for call in calls:
+        with pytest.raises(T.rrb.RrbError) as e:
+            call()
+        assert "overlaps" in str(e.value)
+    assert torch.equal(comb._ws, keep)
+    comb.backward([dy], [z], [dz], d_weights=dw)
+    want_z, want_w = T.OE.combine_grad(T._np(dy), T._np(z), T._slots(idx.cpu().numpy(), E), T._np(w))
+    T._check("dz", dz, want_z, T.ADD * np.abs(want_z), T.HALF * 1.01)
