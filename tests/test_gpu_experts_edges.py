@@ -213,3 +213,27 @@ def test_plans_refuse_overlaps():
     comb.backward([dy], [z], [dz], d_weights=dw)
     want_z, want_w = T.OE.combine_grad(T._np(dy), T._np(z), T._slots(idx.cpu().numpy(), E), T._np(w))
     T._check("dz", dz, want_z, T.ADD * np.abs(want_z), T.HALF * 1.01)
+
+
+@pytest.mark.parametrize("h,shift", [(8, 0), (8, 1), (5, 0)])
+def test_combine_backward_of_more_tokens_than_a_launch(h, shift):
+    """More than 2^23 tokens, which a launch takes: both kernels' later slices
+    (whole 16-byte rows, and rows off those boundaries), every row and weight.
+    dz is one fp32 product rounded to bf16, so equal; dw sums h products."""
+    require_gpu()
+    N, E = (1 << 23) + 77, 4
+    T._say(f"combine gradient of {N} tokens, width {h}, shift {shift}")
+    gen = torch.Generator(device=DEV).manual_seed(68)
+    idx = torch.randint(0, E, (N, 1), generator=gen, dtype=torch.int32, device=DEV)
+    w = torch.rand(N, 1, generator=gen, device=DEV)
+    put = T.Shifted(shift)
+    dy, z = (put(torch.randn(N, h, generator=gen, device=DEV).to(BF)) for _ in range(2))
+    plan = T.rrb.MoeDevicePlan(1, N, h, E, 1, "combine")
+    plan.route(idx, w)
+    dz, dw = put(torch.full((N, h), -7.25, dtype=BF)), torch.full((N, 1), -7.0, device=DEV)
+    plan.backward([dy], [z], [dz], d_weights=dw)
+    order = torch.sort(idx[:, 0], stable=True).indices  # token of each arena row
+    assert torch.equal(dz, (w * dy.float()).to(BF)[order])
+    terms = dy.float()[order].double() * z.double()
+    got = dw[order, 0].double()
+    assert ((got - terms.sum(dim=1)).abs() <= (h + 2) * T.ADD * terms.abs().sum(dim=1)).all()
