@@ -237,3 +237,64 @@ def test_combine_backward_of_more_tokens_than_a_launch(h, shift):
     terms = dy.float()[order].double() * z.double()
     got = dw[order, 0].double()
     assert ((got - terms.sum(dim=1)).abs() <= (h + 2) * T.ADD * terms.abs().sum(dim=1)).all()
+
+
+@pytest.mark.parametrize("N,h,f,E,k,R", [(64, 64, 96, 8, 2, 2), (256, 136, 72, 16, 4, 4), (1, 48, 40, 16, 4, 1)])
+def test_moe_step_replayed_by_itself(N, h, f, E, k, R):
+    """The whole step captured, and replayed three times on new inputs with
+    every output, intermediate and the plan's routing made useless before: the
+    replay alone has to bring all of it back, equal to an eager step's."""
+    require_gpu()
+    rng = T._rng(69, N, h, f)
+    x, dy = T._bf16(rng, (N, h)).to(DEV), T._bf16(rng, (N, h)).to(DEV)
+    logits = torch.zeros(N, E, device=DEV)
+    wg, wu = (T._bf16(rng, (E, f, h), h ** -0.5).to(DEV) for _ in range(2))
+    wd = T._bf16(rng, (E, h, f), f ** -0.5).to(DEV)
+    n = N * k
+    new = lambda *s, dtype=BF: torch.zeros(s, dtype=dtype, device=DEV)
+    disp = T.rrb.MoeDevicePlan(R, N, h, E, k, "dispatch")
+    comb = T.rrb.MoeDevicePlan(R, N, h, E, k, "combine", share=disp)
+    shards = lambda t: list(t.reshape(R, N // R, h).unbind(0))
+    arena = lambda t: [t] + [None] * (R - 1)
+    idx, off = new(N, k, dtype=torch.int32), new(E + 1, dtype=torch.int32)
+    w, d_w, d_logits = (new(N, c, dtype=torch.float32) for c in (k, k, E))
+    xe, z, d_z, d_xe = (new(n, h) for _ in range(4))
+    g, u, hh, d_h = (new(n, f) for _ in range(4))
+    y, d_x, d_wg, d_wu, d_wd = new(N, h), new(N, h), new(E, f, h), new(E, f, h), new(E, h, f)
+    ones = torch.ones(N, k, device=DEV)
+
+    def step():
+        T.rrb.moe_gate(logits, idx, w, renormalize=True)
+        disp.route(idx, w)
+        disp.expert_offsets(off)
+        disp.run(shards(x), arena(xe))
+        T.rrb.expert_gated(xe, off, wg, wu, hh, save_gate=g, save_up=u)
+        T.rrb.expert_linear(hh, off, wd, z)
+        comb.run(arena(z), shards(y))
+        comb.backward(shards(dy), arena(z), arena(d_z), d_weights=d_w)
+        T.rrb.expert_linear_backward(d_z, hh, off, wd, d_x=d_h, d_w=d_wd)
+        T.rrb.expert_gated_backward(d_h, xe, off, wg, wu, g, u, d_x=d_xe, d_w_gate=d_wg, d_w_up=d_wu)
+        comb.run(arena(d_xe), shards(d_x), weights=ones)
+        T.rrb.moe_gate_backward(logits, idx, d_w, d_logits, renormalize=True)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    made = (idx, off, w, d_w, d_logits, xe, z, d_z, d_xe, g, u, hh, d_h, y, d_x, d_wg, d_wu, d_wd)
+    other = torch.arange(k, dtype=torch.int32, device=DEV).expand(N, k).contiguous()
+    for q in range(3):
+        x.copy_(T._bf16(T._rng(70, q), (N, h)))
+        logits.copy_(torch.from_numpy(T._rng(71, q).standard_normal((N, E)).astype(np.float32)))
+        step()
+        torch.cuda.synchronize()
+        eager = [t.clone() for t in made]
+        disp.route(other, torch.full((N, k), float("nan"), device=DEV))
+        for t in made:
+            t.fill_(float("nan") if t.is_floating_point() else 0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(eager, made)):
+            assert torch.equal(a, b), (q, i)
