@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(256) gate_backward_kernel(GateArgs a) {
     m = fmaxf(m, l[i]);
     mine[expert_of<L, W>(i, lane)] = 0.f;
   }
-  m = max_of<L>(m);
+  // Renormalised, the chosen ones' own largest: theirs need not be the row's.
+  m = max_of<L>(a.renorm ? le : m);
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) sum += l[i] = share(l[i], m);

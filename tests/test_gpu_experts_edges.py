@@ -298,3 +298,28 @@ def test_moe_step_replayed_by_itself(N, h, f, E, k, R):
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(eager, made)):
             assert torch.equal(a, b), (q, i)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_gate_gradient_of_experts_far_below_the_largest(dtype):
+    """Renormalised over chosen experts whose scores lie far below the row's
+    largest, which is not among them (its entry is passed over): the softmax
+    over the chosen alone, against the oracle with the others masked."""
+    require_gpu()
+    for E in (5, 300):
+        l = np.full((3, E), -1.0)
+        l[:, 0] = 200.0, 1000.0, 90.0
+        l[:, 1:4] = [1.0, 0.0, -2.0]
+        idx = np.array([[-1, 1, 2], [3, 99999, 1], [2, 3, 1]], np.int32)
+        d_w = T._rng(72, E).standard_normal((3, 3)).astype(np.float32)
+        logits = torch.from_numpy(l).to(dtype).to(DEV)
+        out = torch.full((3, E), -7.0, dtype=dtype, device=DEV)
+        T.rrb.moe_gate_backward(logits, torch.from_numpy(idx).to(DEV), torch.from_numpy(d_w).to(DEV), out,
+                                renormalize=True)
+        for t in range(3):
+            used = (idx[t] >= 0) & (idx[t] < E)
+            masked = np.full((1, E), -np.inf)
+            masked[0, idx[t][used]] = l[t, idx[t][used]]
+            want = T.OE.gate_grad(masked, idx[t:t + 1, used], d_w[t:t + 1, used].astype(np.float64), True)
+            # weights below 1 known to (k + |l - m| + 8) 2^-23 <= 2^-19, times two terms of |dw|
+            T._check("d_logits", out[t:t + 1], want, np.full_like(want, 2.0 ** -17 * np.abs(d_w[t]).max()))
