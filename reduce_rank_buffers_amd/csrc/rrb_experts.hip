@@ -1152,8 +1152,9 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(BiasGradArgs a) {
   const int e = blockIdx.y, lane8 = threadIdx.x & 7, deep = threadIdx.x >> 3;
   const int c0 = blockIdx.x * 64 + lane8 * 8;
   const int32_t first = offset_at(a.p, e), last = offset_at(a.p, e + 1);
-  const int64_t rows = last > first ? last - first : 0;
-  const int64_t s = first + rows * blockIdx.z / a.splits, t = first + rows * (blockIdx.z + 1) / a.splits;
+  const uint32_t rows = last > first ? last - first : 0, z = blockIdx.z;
+  const uint32_t each = a.splits == 1 ? rows : (rows + a.splits - 1) / static_cast<uint32_t>(a.splits);
+  const int64_t s = first + min(rows, each * z), t = first + min(rows, each * (z + 1));
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int64_t r = s + deep; r < t; r += 32) {
     const u32x4_t v = load_chunk(a.dout + r * a.n + c0, a.n - c0);
