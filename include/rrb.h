@@ -356,8 +356,10 @@ rrb_status rrb_moe_combine_backward(rrb_plan_t plan, const void *const *d_dy, co
  * clamped to 0..rows, so no access leaves the buffers; where they decrease the
  * outputs are unspecified.  Buffers need the alignment of their elements only
  * (16-byte aligned rows run faster); outputs must not overlap inputs or each
- * other (RRB_EINVAL), except that d_out may be d_residual.  Limits (RRB_EUNSUPPORTED): rows < 2^30, in and
- * out <= 2^20, groups <= 4096.  All calls are asynchronous on `stream`.
+ * other (RRB_EINVAL), except that d_out may be d_residual.  Limits
+ * (RRB_EUNSUPPORTED): rows < 2^30, in and out <= 2^20, groups <= 4096, and no more
+ * tiles than one launch holds (2^32 threads, 256 or 512 a tile of 64 x 64 to
+ * 256 x 256 outputs).  All calls are asynchronous on `stream`.
  */
 typedef enum {
   RRB_ACT_NONE = 0,
