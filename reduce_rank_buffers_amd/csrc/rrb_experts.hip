@@ -54,7 +54,8 @@ __device__ __forceinline__ float gelu_2u(float x) {
 // leaves fp32's normal range (a fit of the absolute error, 1.5e-7, was 0.4% off
 // at -6 and 1% at -8).  About 17 instructions where the library's erfc takes
 // some 100 (it was an eighth of a 4096-deep product's time).
-__device__ __forceinline__ float normal_cdf(float x) {
+// e receives e^(-x^2 / 2), of which the density is made.
+__device__ __forceinline__ float normal_cdf(float x, float &e) {
   const float z = 0.70710678118654752f * fabsf(x);
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.38f, z, 1.f));
   float q = __builtin_fmaf(-0.12530328f, t, 0.33559692f);
@@ -63,14 +64,18 @@ __device__ __forceinline__ float normal_cdf(float x) {
   q = __builtin_fmaf(q, t, 0.18082708f);
   q = __builtin_fmaf(q, t, 0.21652655f);
   q = __builtin_fmaf(q, t, 0.21429171f);
-  const float half = 0.5f * q * t * __expf(-z * z);
+  e = __expf(-z * z);
+  const float half = 0.5f * q * t * e;
   return x < 0.f ? half : 1.f - half;
 }
 
 template <int ACT>
 __device__ __forceinline__ float activate(float x) {
   if (ACT == RRB_ACT_SILU) return x * sigmoid(x);
-  if (ACT == RRB_ACT_GELU) return x * normal_cdf(x);
+  if (ACT == RRB_ACT_GELU) {
+    float e;
+    return x * normal_cdf(x, e);
+  }
   if (ACT == RRB_ACT_GELU_TANH) return x * sigmoid(gelu_2u(x));
   if (ACT == RRB_ACT_RELU) return x < 0.f ? 0.f : x;
   return x;
@@ -84,9 +89,10 @@ __device__ __forceinline__ void activate_grad(float x, float &f, float &df) {
     f = x * s;
     df = s * (1.f + x * (1.f - s));
   } else if (ACT == RRB_ACT_GELU) {
-    const float c = normal_cdf(x);
+    float e;
+    const float c = normal_cdf(x, e);
     f = x * c;
-    df = c + x * (0.3989422804014327f * __expf(-0.5f * x * x));
+    df = c + x * (0.3989422804014327f * e);
   } else if (ACT == RRB_ACT_GELU_TANH) {
     const float s = sigmoid(gelu_2u(x));
     const float t = s * (1.f - s);
@@ -1134,25 +1140,25 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs p) {
 // wide and 32 rows deep.  A group's rows are split over workgroups where the
 // columns alone make few; their sums are then joined in order by
 // bias_join_kernel.  8192 x 7168 in 16 groups (1792 workgroups): bound by reading
-// dY, 117 MB in 31 us.  32768 x 64 in one group: 196 us whole and 13.5 split;
+// dY, 117 MB in 31 us.  32768 x 64 in one group: 196 us whole and 12.5 split;
 // with silu's slope 590 and 14.
 struct BiasGradArgs {
   const uint16_t *dout, *pre;  // pre: NULL without an activation
   uint16_t *db;
   float *part;   // [splits][groups][n], or NULL: one split, straight to db
-  uint16_t *dz;  // NULL: not written; pitch ldo, columns n .. ldo padded with 0
+  uint16_t *dz;  // COPY; pitch ldo, columns n .. ldo padded with 0
   int64_t ldo;
   ProductArgs p;  // offsets, rows, groups
   int32_t n, splits;
 };
 
-template <int ACT>
+template <int ACT, bool COPY>
 __global__ void __launch_bounds__(256) bias_grad_kernel(BiasGradArgs a) {
   __shared__ float part[32][64 + 1];
-  const int e = blockIdx.y, lane8 = threadIdx.x & 7, deep = threadIdx.x >> 3;
+  const int e = blockIdx.z, lane8 = threadIdx.x & 7, deep = threadIdx.x >> 3;
   const int c0 = blockIdx.x * 64 + lane8 * 8;
   const int32_t first = offset_at(a.p, e), last = offset_at(a.p, e + 1);
-  const uint32_t rows = last > first ? last - first : 0, z = blockIdx.z;
+  const uint32_t rows = last > first ? last - first : 0, z = blockIdx.y;
   const uint32_t each = a.splits == 1 ? rows : (rows + a.splits - 1) / static_cast<uint32_t>(a.splits);
   const int64_t s = first + min(rows, each * z), t = first + min(rows, each * (z + 1));
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -1160,18 +1166,15 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(BiasGradArgs a) {
     const u32x4_t v = load_chunk(a.dout + r * a.n + c0, a.n - c0);
     u32x4_t x = {0, 0, 0, 0};
     if (ACT != RRB_ACT_NONE) x = load_chunk(a.pre + r * a.n + c0, a.n - c0);
+    float d[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float f, d0, d1;
-      activate_grad<ACT>(bf16_lo(x[q]), f, d0);
-      activate_grad<ACT>(bf16_hi(x[q]), f, d1);
-      d0 *= bf16_lo(v[q]);
-      d1 *= bf16_hi(v[q]);
-      sum[2 * q] += d0;
-      sum[2 * q + 1] += d1;
-      x[q] = cvt_pk_bf16(d0, d1);
+    for (int q = 0; q < 8; ++q) {
+      float f, df;
+      activate_grad<ACT>(q & 1 ? bf16_hi(x[q >> 1]) : bf16_lo(x[q >> 1]), f, df);
+      d[q] = df * (q & 1 ? bf16_hi(v[q >> 1]) : bf16_lo(v[q >> 1]));
+      sum[q] += d[q];
     }
-    if (a.dz && c0 < a.ldo) *reinterpret_cast<u32x4_t *>(a.dz + r * a.ldo + c0) = x;
+    if (COPY && c0 < a.ldo) store_cols<8>(a.dz + r * a.ldo + c0, 8, d);
   }
 #pragma unroll
   for (int q = 0; q < 8; ++q) part[deep][lane8 * 8 + q] = sum[q];
@@ -1183,7 +1186,7 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(BiasGradArgs a) {
     const int64_t at = static_cast<int64_t>(e) * a.n + col;
     if (col >= a.n) return;
     if (a.part)
-      a.part[static_cast<int64_t>(blockIdx.z) * a.p.groups * a.n + at] = total;
+      a.part[static_cast<int64_t>(z) * a.p.groups * a.n + at] = total;
     else
       a.db[at] = f32_to_bf16_rne(total);
   }
@@ -1359,22 +1362,29 @@ rrb_status launch_act_grad(const ActGradArgs &a, int act, hipStream_t s) {
   return launched("activation gradient");
 }
 
-// Splits of each group's rows for the bias gradient: towards four workgroups per
-// CU, of at least 128 rows on average (four turns of a thread), and at most 64,
-// which one thread then joins.
-int64_t bias_splits(const rrb_expert_spec &s) {
-  const int64_t whole = (s.out + 63) / 64 * s.groups;
-  const int64_t want = (1024 + whole - 1) / whole, most = (s.rows / s.groups + 127) / 128;
-  return std::max<int64_t>(1, std::min<int64_t>(64, std::min(want, most)));
+// Splits of each group's rows for the bias gradient, towards eight workgroups per
+// CU, and at most 64, which one thread then joins.  The join is a launch of 2 us.
+// Without an activation a turn of 32 rows takes 0.2 us, and groups of fewer than
+// 512 rows on average stay whole.  With one it takes up to 0.7, and the rows of
+// the whole arena count, as they may all be one group's (32768 x 64, silu, all in
+// one of 256 groups: the whole backward 428 us at four splits in the order
+// groups, splits; 247 at eight in this one).
+int64_t bias_splits(const rrb_expert_spec &s, bool act) {
+  const int64_t mean = s.rows / s.groups, most = act ? s.rows / 256 : mean < 512 ? 1 : mean / 128;
+  return std::max<int64_t>(1, std::min<int64_t>(64, std::min(2048 / ((s.out + 63) / 64 * s.groups), most)));
 }
 
 rrb_status launch_bias_grad(const BiasGradArgs &a, int act, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.n + 63) / 64), static_cast<unsigned>(a.p.groups),
-                  static_cast<unsigned>(a.splits));
+  // Splits before groups: a group's then run on different XCDs.
+  const dim3 grid(static_cast<unsigned>((a.n + 63) / 64), static_cast<unsigned>(a.splits),
+                  static_cast<unsigned>(a.p.groups));
   switch (act) {
 #define RRB_CASE(A)                                                              \
   case A:                                                                        \
-    hipLaunchKernelGGL((bias_grad_kernel<A>), grid, dim3(256), 0, s, a);         \
+    if (a.dz)                                                                    \
+      hipLaunchKernelGGL((bias_grad_kernel<A, true>), grid, dim3(256), 0, s, a); \
+    else                                                                         \
+      hipLaunchKernelGGL((bias_grad_kernel<A, false>), grid, dim3(256), 0, s, a); \
     break;
     RRB_CASE(RRB_ACT_NONE) RRB_CASE(RRB_ACT_SILU) RRB_CASE(RRB_ACT_GELU) RRB_CASE(RRB_ACT_GELU_TANH)
     RRB_CASE(RRB_ACT_RELU)
@@ -1476,8 +1486,9 @@ rrb_status rrb_expert_linear_backward_workspace(const rrb_expert_spec *spec, siz
   static const int32_t any = 0;
   rrb_status st = check_spec(spec, &any);
   if (st != RRB_OK) return st;
-  // dZ, and the bias gradient's partial sums where its rows are split.
-  const int64_t splits = bias_splits(*spec);
+  // dZ, and the bias gradient's partial sums where its rows are split (the more
+  // of them with an activation: one size serves all).
+  const int64_t splits = std::max(bias_splits(*spec, false), bias_splits(*spec, true));
   *bytes = static_cast<size_t>(spec->rows * padded(spec->out) * 2 +
                                (splits > 1 ? splits * spec->groups * spec->out * 4 : 0));
   return RRB_OK;
@@ -1594,7 +1605,7 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
     b.db = u16(d_dbias);
     b.dz = copy ? u16(d_workspace) : nullptr;
     b.ldo = padded(spec->out);
-    b.splits = static_cast<int32_t>(bias_splits(*spec));
+    b.splits = static_cast<int32_t>(bias_splits(*spec, act));
     if (b.splits > 1) b.part = reinterpret_cast<float *>(u16(d_workspace) + spec->rows * b.ldo);
     b.p = p;
     b.n = static_cast<int32_t>(spec->out);

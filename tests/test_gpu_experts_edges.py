@@ -323,3 +323,10 @@ def test_gate_gradient_of_experts_far_below_the_largest(dtype):
             want = T.OE.gate_grad(masked, idx[t:t + 1, used], d_w[t:t + 1, used].astype(np.float64), True)
             # weights below 1 known to (k + |l - m| + 8) 2^-23 <= 2^-19, times two terms of |dw|
             T._check("d_logits", out[t:t + 1], want, np.full_like(want, 2.0 ** -17 * np.abs(d_w[t]).max()))
+
+
+@pytest.mark.parametrize("name", ["none", "gelu"])
+def test_bias_gradient_of_one_group_among_many(name):
+    """All rows in one of 64 groups; the others' gradients are 0."""
+    require_gpu()
+    T._backward_linear(T.Problem(73, [0] * 40 + [9000] + [0] * 23, 16, 72), name)
