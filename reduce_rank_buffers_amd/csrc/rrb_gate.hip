@@ -132,9 +132,9 @@ __device__ __forceinline__ void load_scores(const T *row, int experts, int lane,
 }
 
 // Bound by its operations, the rounds' and the sum's (which renormalised weights
-// do not need): 32768 x 256 bf16, top-8, 13 us (45
-// with a whole wave per token and 64-bit keys through shuffles; the scores alone
-// move in 4); 16 x 256 fp32 4.2 us, of which the launch is 2.
+// do not need): 32768 x 256 bf16, top-8, 13 us (45 with a whole wave per token
+// and 64-bit keys through shuffles; the scores alone move in 4); 16 x 256 fp32
+// 4.2 us, of which the launch is 2.
 template <typename T, int L, int V, int W>
 __global__ void __launch_bounds__(256) gate_kernel(GateArgs a) {
   constexpr bool kShort = sizeof(T) == 2;
