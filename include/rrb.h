@@ -412,6 +412,76 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
                                       void *d_dx, void *d_dw, void *d_dbias, void *d_workspace,
                                       size_t workspace_bytes, rrb_stream_t stream);
 
+/*
+ * Serving with 8-bit integers.  A matrix is held as integers q (int8) and a
+ * scale (fp32) for each of its rows, q * scale standing for its values.
+ *
+ * rrb_quantize_rows makes them from rows of bf16 or fp32: scale = fl32(max |x| /
+ * 127), q = x / scale to the nearest integer, ties to even, exactly (kept within
+ * +-127 where a subnormal scale would pass it).  A row of zeros has the scale 0; a row with an infinity or a NaN
+ * has a NaN for its scale and zeros for its integers, so that what is computed
+ * from it is NaN.  d_offsets (nullable): int32, groups + 1 entries, of which the
+ * first and the last bound the rows that are read and written, clamped to
+ * 0..rows.  Weights [groups][out][in] are groups * out rows.  Limits
+ * (RRB_EUNSUPPORTED): rows < 2^31, width <= 2^20.
+ */
+rrb_status rrb_quantize_rows(int64_t rows, int64_t width, int32_t dtype, const void *d_x,
+                             const int32_t *d_offsets, int32_t groups, int8_t *d_q, float *d_scale,
+                             rrb_stream_t stream);
+
+/*
+ * The experts' products of such rows (d_x, d_x_scale[rows]) and weights (d_w,
+ * d_w_scale[groups][out]); rules, limits and rows outside the groups as for
+ * rrb_expert_linear and rrb_expert_gated, and in < 2^17.  Integers are summed
+ * exactly; p = fl(fl(fl32(sum) * x_scale) * w_scale), and
+ *   linear  out = act(p + bias) + residual
+ *   gated   out = act(p_gate) * p_up
+ * with bias, residual and out in bf16, each result rounded once.  The calls have no gradient.
+ */
+rrb_status rrb_expert_linear_int8(const rrb_expert_spec *spec, const int8_t *d_x, const float *d_x_scale,
+                                  const int32_t *d_offsets, const int8_t *d_w, const float *d_w_scale,
+                                  const void *d_bias, const void *d_residual, void *d_out,
+                                  rrb_stream_t stream);
+rrb_status rrb_expert_gated_int8(const rrb_expert_spec *spec, const int8_t *d_x, const float *d_x_scale,
+                                 const int32_t *d_offsets, const int8_t *d_w_gate,
+                                 const float *d_gate_scale, const int8_t *d_w_up, const float *d_up_scale,
+                                 void *d_out, rrb_stream_t stream);
+
+/*
+ * The whole expert layer for a few tokens (a decode step), without dispatch and
+ * combine:
+ *   y_t = sum over j of w[t][j] Wd[e] h,  h = act(Wg[e] x_t) * (Wu[e] x_t),  e = topk_idx[t][j]
+ * with x and y [tokens][hidden] bf16, Wg and Wu [experts][inner][hidden], Wd
+ * [experts][hidden][inner], and topk_idx, topk_w [tokens][topk] as rrb_moe_gate
+ * writes them.  Weights are bf16, or (all three scales given) int8 with scales
+ * [experts][inner], [experts][inner] and [experts][hidden].  Sums are fp32; h is
+ * rounded to bf16, and y once.  Choices outside 0..experts - 1 take no part (experts
+ * of another rank), nor does their weight; an expert that a token chose twice
+ * counts twice.  A token without choices has y = 0.  Weights of experts without
+ * tokens are not read.  Results do not depend on the launch: the same inputs give
+ * the same bits.  d_workspace holds h between the two kernels (caller-owned,
+ * 16-byte aligned, of the size the query gives; in use until the call's work
+ * completes).  Buffers need the alignment of their elements only; out and the
+ * workspace must not overlap inputs or each other (RRB_EINVAL).  Limits
+ * (RRB_EUNSUPPORTED): tokens <= 64, hidden and inner <= 2^20, experts <= 1024,
+ * topk <= 16.
+ */
+typedef struct {
+  int64_t tokens;     /* >= 0 */
+  int64_t hidden;
+  int64_t inner;
+  int32_t experts;
+  int32_t topk;
+  int32_t activation; /* rrb_activation */
+  int32_t reserved;
+} rrb_decode_spec;
+rrb_status rrb_moe_decode_workspace(const rrb_decode_spec *spec, size_t *bytes);
+rrb_status rrb_moe_decode(const rrb_decode_spec *spec, const void *d_x, const int32_t *d_topk_idx,
+                          const float *d_topk_w, const void *d_w_gate, const void *d_w_up,
+                          const void *d_w_down, const float *d_gate_scale, const float *d_up_scale,
+                          const float *d_down_scale, void *d_out, void *d_workspace,
+                          size_t workspace_bytes, rrb_stream_t stream);
+
 /* ---- SNAC: stage / notify / consume chain --------------------------------- */
 
 /*

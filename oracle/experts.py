@@ -9,7 +9,9 @@ arrays:
   descending score, ties to the lower expert; w = p of the chosen ones, or
   p / (their sum);
 * linear: Y = act(X W^T + b) + R, per group of rows;
-* gated: H = act(X Wg^T) * (X Wu^T), per group of rows.
+* gated: H = act(X Wg^T) * (X Wu^T), per group of rows;
+* quantize: a row as integers of at most 127 and a scale;
+* decode: the layer token by token, choice by choice.
 
 Pinned by central differences of every gradient and by hand-made cases
 (tests/test_oracle_experts.py).
@@ -129,3 +131,28 @@ def combine_grad(d_y, z, slot, w):
     d_z = np.zeros_like(z)
     d_z[slot.reshape(-1)] = (w[:, :, None] * d_y[:, None, :]).reshape(-1, z.shape[1])
     return d_z, (d_y[:, None, :] * z[slot]).sum(axis=2)
+
+
+def quantize(x):
+    """(q float64 [N, n] of whole numbers, s float32 [N]) of finite float64 rows
+    that hold float32 values: s the float32 nearest to max |x| / 127, q the
+    integer nearest to x / s (ties to even) within +-127, 0 where s is 0."""
+    s = (np.abs(x).max(axis=1) / 127.0).astype(np.float32)
+    d = s.astype(np.float64)[:, None]
+    return np.where(d == 0, 0.0, np.clip(np.rint(x / np.where(d == 0, 1.0, d)), -127, 127)), s
+
+
+def decode(x, idx, w, w_gate, w_up, w_down, name):
+    """(y [T, h], z) of the expert layer: y[t] the sum of w[t, j] z over the
+    choices j whose expert e = idx[t, j] is among the weights', z = Wd[e]
+    (act(Wg[e] x[t]) * (Wu[e] x[t])); z maps (t, j) to (z, hidden, gate, up)."""
+    y, parts = np.zeros_like(x), {}
+    for t in range(x.shape[0]):
+        for j, e in enumerate(idx[t]):
+            if 0 <= e < w_gate.shape[0]:
+                g, u = w_gate[e] @ x[t], w_up[e] @ x[t]
+                hidden = act(name, g) * u
+                z = w_down[e] @ hidden
+                y[t] += w[t, j] * z
+                parts[t, j] = z, hidden, g, u
+    return y, parts

@@ -18,5 +18,6 @@ from .api import (  # noqa: F401
 from .experts import (  # noqa: F401
     moe_gate, moe_gate_backward, expert_gated, expert_gated_backward, expert_gated_backward_workspace,
     expert_linear, expert_linear_backward, expert_linear_backward_workspace,
+    quantize_rows, expert_linear_int8, expert_gated_int8, moe_decode, moe_decode_workspace,
 )
 from ._lib import RrbError, lib  # noqa: F401

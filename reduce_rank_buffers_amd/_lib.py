@@ -57,6 +57,7 @@ EXPORTS = (
     "rrb_moe_gate", "rrb_moe_gate_backward", "rrb_moe_expert_offsets", "rrb_moe_combine_backward",
     "rrb_expert_gated", "rrb_expert_gated_backward_workspace", "rrb_expert_gated_backward",
     "rrb_expert_linear", "rrb_expert_linear_backward_workspace", "rrb_expert_linear_backward",
+    "rrb_quantize_rows", "rrb_expert_linear_int8", "rrb_expert_gated_int8", "rrb_moe_decode_workspace", "rrb_moe_decode",
     "rrb_moe_route_check", "rrb_plan_query", "rrb_plan_bind",
     "rrb_plan_segments", "rrb_plan_destroy",
     "rrb_copy", "rrb_reduce", "rrb_plan_launch_info", "rrb_empty_kernel",
@@ -84,6 +85,12 @@ class Segment(ctypes.Structure):
 class ExpertSpec(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("in_", ctypes.c_int64), ("out", ctypes.c_int64),
                 ("groups", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class DecodeSpec(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inner", ctypes.c_int64),
+                ("experts", ctypes.c_int32), ("topk", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class SnacStats(ctypes.Structure):
@@ -124,6 +131,11 @@ _SIGS = {
     "rrb_expert_linear": (_I32, [ctypes.POINTER(ExpertSpec)] + [_P] * 8),
     "rrb_expert_linear_backward_workspace": (_I32, [ctypes.POINTER(ExpertSpec), ctypes.POINTER(_SZ)]),
     "rrb_expert_linear_backward": (_I32, [ctypes.POINTER(ExpertSpec)] + [_P] * 9 + [_SZ, _P]),
+    "rrb_quantize_rows": (_I32, [_I64, _I64, _I32, _P, _P, _I32, _P, _P, _P]),
+    "rrb_expert_linear_int8": (_I32, [ctypes.POINTER(ExpertSpec)] + [_P] * 9),
+    "rrb_expert_gated_int8": (_I32, [ctypes.POINTER(ExpertSpec)] + [_P] * 9),
+    "rrb_moe_decode_workspace": (_I32, [ctypes.POINTER(DecodeSpec), ctypes.POINTER(_SZ)]),
+    "rrb_moe_decode": (_I32, [ctypes.POINTER(DecodeSpec)] + [_P] * 11 + [_SZ, _P]),
     "rrb_plan_query": (_I32, [_P, ctypes.POINTER(_SZ), _P, _P]),
     "rrb_plan_bind": (_I32, [_P, _P, _SZ, _P]),
     "rrb_plan_segments": (_I32, [_P, ctypes.POINTER(Segment), _I32, ctypes.POINTER(_I32)]),

@@ -22,7 +22,8 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "librrb.so")
 LIB_FENCED = os.path.join(PKG, "librrb_fenced.so")
 FENCED_SOURCE = "rrb_snac.hip"
-SOURCES = ["rrb_capi.cpp", "rrb_plan.cpp", "rrb_atom.hip", "rrb_moe.hip", "rrb_gate.hip", "rrb_experts.hip", "rrb_snac.hip"]
+SOURCES = ["rrb_capi.cpp", "rrb_plan.cpp", "rrb_atom.hip", "rrb_moe.hip", "rrb_gate.hip", "rrb_experts.hip",
+           "rrb_experts_int8.hip", "rrb_decode.hip", "rrb_snac.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -3,7 +3,9 @@
 The steps of an MoE layer around dispatch and combine: ``moe_gate`` makes the
 routing arrays from scores, the ``expert_*`` calls run on the dispatched rows,
 grouped by expert (``MoeDevicePlan.expert_offsets``), and each has its
-gradient.  Outputs are the caller's tensors, written in place; argument rules
+gradient.  For serving, ``quantize_rows`` and the ``expert_*_int8`` calls run
+the products in 8-bit integers, and ``moe_decode`` the whole expert layer of a
+few tokens without dispatch and combine; these have none.  Outputs are the caller's tensors, written in place; argument rules
 are api.py's (contiguous, on the current GPU, bf16 as torch.bfloat16 or its
 int16 / uint16 bit patterns), and shapes are checked too; the library refuses
 outputs that overlap what a call reads.  None of the calls takes part in
@@ -229,3 +231,110 @@ def expert_linear_backward(d_out, x, offsets, w, pre=None, activation="none", d_
     L.check(L.lib().rrb_expert_linear_backward(ctypes.byref(spec), *at, ws.data_ptr(), need, _raw_stream(stream, dev)),
             "rrb_expert_linear_backward")
     return d_x, d_w, d_bias
+
+
+# ---- serving -------------------------------------------------------------------
+
+_INT8 = (torch.int8,)
+
+
+def quantize_rows(x, q, scale, offsets=None, stream=None):
+    """Rows as 8-bit integers: x [..., n] bf16 or float32 -> q int8 of its
+    shape and scale float32 of x.shape[:-1], scale = max |x| / 127 of a row
+    (float32) and q = x / scale to the nearest integer, ties to even.  A row
+    of zeros has scale 0, a row with an infinity or a NaN scale NaN and zeros.
+    offsets (int32 [G + 1], x of two dimensions): only rows offsets[0] ..
+    offsets[-1] - 1 are read and written."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x: expected a tensor of at least two dimensions")
+    dt, n = _dtype_of(x), x.shape[-1]
+    named = [_shaped(x, "x", x.shape, (x.dtype,)), _shaped(q, "q", x.shape, _INT8),
+             _shaped(scale, "scale", x.shape[:-1], _F32_TYPES)]
+    groups = 0
+    if offsets is not None:
+        if x.dim() != 2 or not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets: expected a tensor of one dimension and at least two entries, x of two dimensions")
+        groups = offsets.numel() - 1
+    named.append(_shaped(offsets, "offsets", (groups + 1,), (torch.int32,)))
+    (xp, qp, sp, op), dev = _addresses(named, ("offsets",))
+    rows = scale.numel()
+    L.check(L.lib().rrb_quantize_rows(rows, n, dt, xp, op, groups, qp, sp, _raw_stream(stream, dev)),
+            "rrb_quantize_rows")
+    return q, scale
+
+
+def expert_linear_int8(x, x_scale, offsets, w, w_scale, out, bias=None, activation="none", residual=None, stream=None):
+    """expert_linear of rows and weights as quantize_rows makes them: x int8
+    [N, in], x_scale float32 [N], w int8 [G, out, in], w_scale float32
+    [G, out]; out, bias [G, out] and residual [N, out] (may be out itself)
+    bf16."""
+    spec, N, i, o, G = _spec(x, w, activation, "w")
+    ins = [_shaped(x, "x", (N, i), _INT8), _shaped(x_scale, "x_scale", (N,), _F32_TYPES), _offsets(offsets, G),
+           _shaped(w, "w", (G, o, i), _INT8), _shaped(w_scale, "w_scale", (G, o), _F32_TYPES),
+           _shaped(bias, "bias", (G, o)), _shaped(residual, "residual", (N, o))]
+    at, dev = _addresses(ins + [_shaped(out, "out", (N, o))], ("offsets", "bias", "residual"))
+    L.check(L.lib().rrb_expert_linear_int8(ctypes.byref(spec), *at, _raw_stream(stream, dev)),
+            "rrb_expert_linear_int8")
+    return out
+
+
+def expert_gated_int8(x, x_scale, offsets, w_gate, gate_scale, w_up, up_scale, out, activation="silu", stream=None):
+    """expert_gated of rows and weights as quantize_rows makes them: x int8
+    [N, in], x_scale float32 [N], w_gate and w_up int8 [G, inner, in] with
+    scales float32 [G, inner]; out [N, inner] bf16."""
+    spec, N, i, o, G = _spec(x, w_gate, activation, "w_gate")
+    ins = [_shaped(x, "x", (N, i), _INT8), _shaped(x_scale, "x_scale", (N,), _F32_TYPES), _offsets(offsets, G),
+           _shaped(w_gate, "w_gate", (G, o, i), _INT8), _shaped(gate_scale, "gate_scale", (G, o), _F32_TYPES),
+           _shaped(w_up, "w_up", (G, o, i), _INT8), _shaped(up_scale, "up_scale", (G, o), _F32_TYPES)]
+    at, dev = _addresses(ins + [_shaped(out, "out", (N, o))], ("offsets",))
+    L.check(L.lib().rrb_expert_gated_int8(ctypes.byref(spec), *at, _raw_stream(stream, dev)), "rrb_expert_gated_int8")
+    return out
+
+
+def _decode_workspace(spec):
+    n = ctypes.c_size_t()
+    L.check(L.lib().rrb_moe_decode_workspace(ctypes.byref(spec), ctypes.byref(n)), "rrb_moe_decode_workspace")
+    return n.value
+
+
+def moe_decode_workspace(tokens, topk, hidden, inner):
+    """Bytes of workspace that moe_decode needs."""
+    return _decode_workspace(L.DecodeSpec(tokens, hidden, inner, 1, topk, 0, 0))
+
+
+def moe_decode(x, topk_idx, topk_w, w_gate, w_up, w_down, out, activation="silu", scales=None, workspace=None,
+               stream=None):
+    """The expert layer of up to 64 tokens in two kernels, without dispatch and
+    combine: out[t] = sum over j of topk_w[t, j] Wd[e] (act(Wg[e] x[t]) *
+    (Wu[e] x[t])), e = topk_idx[t, j], for x and out [T, h], topk_idx int32
+    and topk_w float32 [T, k] (as moe_gate writes them), w_gate and w_up
+    [E, f, h], w_down [E, h, f].  Choices outside 0 .. E - 1 take no part.
+    scales: (gate, up, down) float32 [E, f], [E, f], [E, h] of weights held in
+    int8 (quantize_rows).  workspace: uint8 tensor of moe_decode_workspace
+    bytes (allocated per call if None)."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    for t, name, dims in ((x, "x", 2), (topk_idx, "topk_idx", 2), (w_gate, "w_gate", 3)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            raise ValueError(f"{name}: expected a tensor of {dims} dimensions")
+    (T, h), (E, f, wh), k = x.shape, w_gate.shape, topk_idx.shape[1]
+    if wh != h:
+        raise ValueError(f"w_gate: {wh} columns for rows of {h}")
+    types = _BF16_TYPES
+    sg = su = sd = None
+    if scales is not None:
+        if not isinstance(scales, (tuple, list)) or len(scales) != 3 or any(s is None for s in scales):
+            raise ValueError("scales: expected those of w_gate, w_up and w_down")
+        (sg, su, sd), types = scales, _INT8
+    named = [_shaped(x, "x", (T, h)), _shaped(topk_idx, "topk_idx", (T, k), (torch.int32,)),
+             _shaped(topk_w, "topk_w", (T, k), _F32_TYPES), _shaped(w_gate, "w_gate", (E, f, h), types),
+             _shaped(w_up, "w_up", (E, f, h), types), _shaped(w_down, "w_down", (E, h, f), types),
+             _shaped(sg, "scales[0]", (E, f), _F32_TYPES), _shaped(su, "scales[1]", (E, f), _F32_TYPES),
+             _shaped(sd, "scales[2]", (E, h), _F32_TYPES), _shaped(out, "out", (T, h))]
+    at, dev = _addresses(named, ("scales[0]", "scales[1]", "scales[2]"))
+    spec = L.DecodeSpec(T, h, f, E, k, ACTIVATIONS[activation], 0)
+    need = _decode_workspace(spec)
+    ws = _workspace(workspace, need, x, stream)
+    L.check(L.lib().rrb_moe_decode(ctypes.byref(spec), *at, ws.data_ptr(), need, _raw_stream(stream, dev)),
+            "rrb_moe_decode")
+    return out
