@@ -454,8 +454,8 @@ rrb_status rrb_expert_gated_int8(const rrb_expert_spec *spec, const int8_t *d_x,
  * with x and y [tokens][hidden] bf16, Wg and Wu [experts][inner][hidden], Wd
  * [experts][hidden][inner], and topk_idx, topk_w [tokens][topk] as rrb_moe_gate
  * writes them.  Weights are bf16, or (all three scales given) int8 with scales
- * [experts][inner], [experts][inner] and [experts][hidden].  Sums are fp32; h is
- * rounded to bf16, and y once.  Choices outside 0..experts - 1 take no part (experts
+ * [experts][inner], [experts][inner] and [experts][hidden].  Sums are fp32, h is
+ * kept in two bf16 parts (16 bits), and y is rounded once.  Choices outside 0..experts - 1 take no part (experts
  * of another rank), nor does their weight; an expert that a token chose twice
  * counts twice.  A token without choices has y = 0.  Weights of experts without
  * tokens are not read.  Results do not depend on the launch: the same inputs give

@@ -16,18 +16,18 @@
 #include "rrb_activations.h"
 #include "rrb_internal.h"
 #include "rrb_kernels.h"
+#include "rrb_lds.h"
 
 namespace rrb {
 namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxTokens = 64;
-constexpr int kMaxChoices = kMaxTokens * kRouteMaxTopk;
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kDirectExperts = 512;  // of layers whose weights go through LDS, which holds the tables too
 
 struct DecodeArgs {
   const uint16_t *x;
@@ -35,64 +35,146 @@ struct DecodeArgs {
   const float *w;
   const void *gate, *up, *down;
   const float *sgate, *sup, *sdown;  // integers' scales
-  uint16_t *h;                       // [tokens * topk][pitch]
+  uint16_t *h;                       // [rows][2][pitch]: bf16 parts whose sum is h
   uint16_t *y;
   int32_t tokens, topk, experts, hidden, inner, pitch, act, tiles;
 };
 
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 // ---- which experts have tokens -----------------------------------------------
+//
+// Every workgroup reads the choices and makes the same tables: each expert's tokens
+// as a mask, and the experts that have any, ascending, each with the row of h at
+// which its tokens' rows begin (one for each, in the tokens' order).
 
+template <int TOKENS, int EXPERTS>
 struct Choices {
-  int32_t idx[kMaxChoices];
-  uint32_t mask[kRouteMaxExperts / 32];
-  uint16_t list[kRouteMaxExperts];  // experts with tokens, ascending
+  static constexpr int BITS = TOKENS <= 8 ? 8 : 64;
+  static constexpr int ROWS = TOKENS * kRouteMaxTopk;
+  uint32_t mask[EXPERTS * BITS / 32];
+  uint32_t list[ROWS < EXPERTS ? ROWS : EXPERTS];  // expert | its first row << 16
+
+  __device__ __forceinline__ void add(int e, int t) {
+    if (BITS == 8)
+      atomicOr(&mask[e >> 2], 1u << (8 * (e & 3) + t));
+    else
+      atomicOr(&mask[2 * e + (t >> 5)], 1u << (t & 31));
+  }
+  __device__ __forceinline__ uint64_t tokens(int e) const {
+    if (BITS == 8) return mask[e >> 2] >> (8 * (e & 3)) & 0xff;
+    return mask[2 * e] | static_cast<uint64_t>(mask[2 * e + 1]) << 32;
+  }
 };
 
-// Fills `c` (NT threads) and returns the number of experts in its list.
-template <int NT>
-__device__ __forceinline__ int find_experts(const DecodeArgs &a, Choices &c) {
-  const int tid = threadIdx.x, n = a.tokens * a.topk;
-  if (tid < kRouteMaxExperts / 32) c.mask[tid] = 0;
-  __syncthreads();
-  for (int i = tid; i < n; i += NT) {
-    const int e = a.idx[i];
-    c.idx[i] = e;
-    if (e >= 0 && e < a.experts) atomicOr(&c.mask[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-  const int words = (a.experts + 31) >> 5;
-  int count = 0;
-  for (int i = 0; i < words; ++i) count += __popc(c.mask[i]);
-  for (int e = tid; e < a.experts; e += NT) {
-    if (!(c.mask[e >> 5] >> (e & 31) & 1)) continue;
-    int at = __popc(c.mask[e >> 5] & ((1u << (e & 31)) - 1));
-    for (int i = 0; i < e >> 5; ++i) at += __popc(c.mask[i]);
-    c.list[at] = e;
-  }
-  __syncthreads();
-  return uniform(count);
-}
+// What the second kernel needs besides: each row's weight.
+template <int TOKENS, int EXPERTS>
+struct Weights {
+  int16_t idx[TOKENS * kRouteMaxTopk];  // the choices: experts that are here, or -1
+  uint16_t row_of[EXPERTS];
+  float row[TOKENS * kRouteMaxTopk];
+};
 
-// The tokens of expert e, by lane: lane l < 64 is token l.  Of each its first
-// choice that is e, or -1.
-__device__ __forceinline__ int choice_of(const DecodeArgs &a, const Choices &c, int e, int t) {
-  int found = -1;
-  if (t < a.tokens) {
-    for (int j = a.topk - 1; j >= 0; --j)
-      if (c.idx[t * a.topk + j] == e) found = t * a.topk + j;
+struct Live {
+  int experts;  // in the list
+  int most;     // tokens of one expert, rounded up to a power of two
+};
+
+__device__ __forceinline__ uint64_t below(int lane) { return (uint64_t(1) << lane) - 1; }
+
+// Fills `c`, and `weights` if it is there (NT threads).
+template <int NT, int TOKENS, int EXPERTS>
+__device__ __forceinline__ Live find_experts(const DecodeArgs &a, Choices<TOKENS, EXPERTS> &c,
+                                             Weights<TOKENS, EXPERTS> *weights) {
+  constexpr int EACH = (TOKENS * kRouteMaxTopk + NT - 1) / NT;
+  const int tid = threadIdx.x, lane = tid & 63, n = a.tokens * a.topk;
+  int e[EACH], t[EACH];
+  float w[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int at = i * NT + tid;
+    e[i] = at < n ? a.idx[at] : -1;
+    w[i] = weights && at < n ? a.w[at] : 0.f;
+    t[i] = at / a.topk;
+    if (e[i] < 0 || e[i] >= a.experts) e[i] = -1;
   }
-  return found;
+  for (int i = tid; i < (a.experts * c.BITS + 31) / 32; i += NT) c.mask[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int at = i * NT + tid;
+    if (weights && at < n) weights->idx[at] = e[i];
+    if (e[i] >= 0) c.add(e[i], t[i]);
+  }
+  __syncthreads();
+  // Every wave makes the whole list, so that none waits for another's part.
+  Live live = {0, 1};
+  int rows = 0;
+  for (int first = 0; first < a.experts; first += 64) {
+    const int x = first + lane;
+    const int many = x < a.experts ? __popcll(c.tokens(x)) : 0;
+    const uint64_t set = __ballot(many > 0);
+    if (!set) continue;
+    int upto = many;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += v;
+    }
+    const int row = rows + upto - many;
+    if (many) {
+      c.list[live.experts + __popcll(set & below(lane))] = x | row << 16;
+      if (weights) weights->row_of[x] = row;
+    }
+    live.experts += __popcll(set);
+    rows += __shfl(upto, 63, 64);
+#pragma unroll
+    for (int m = 64; m >= 2; m >>= 1)
+      if (live.most < m && __ballot(many > m / 2)) live.most = m;
+  }
+  if (weights) {
+    // A token's first choice of an expert brings those of the same one with it.
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      if (e[i] < 0) continue;
+      const int j = i * NT + tid - t[i] * a.topk;
+      bool first = true;
+      for (int k = 0; k < a.topk; ++k) {
+        if (k == j || weights->idx[t[i] * a.topk + k] != e[i]) continue;
+        if (k < j) first = false;
+        w[i] += a.w[t[i] * a.topk + k];
+      }
+      if (first) weights->row[weights->row_of[e[i]] + __popcll(c.tokens(e[i]) & below(t[i]))] = w[i];
+    }
+    __syncthreads();
+  }
+  live.experts = uniform(live.experts);
+  live.most = uniform(live.most);
+  return live;
 }
 
 // Lane i receives the lane of the i-th set bit of `set` (the others' follow).
 __device__ __forceinline__ int in_order(uint64_t set) {
   const int lane = threadIdx.x & 63;
-  const uint64_t below = (uint64_t(1) << lane) - 1;
-  const int at = set >> lane & 1 ? __popcll(set & below) : __popcll(set) + __popcll(~set & below);
+  const int at = set >> lane & 1 ? __popcll(set & below(lane)) : __popcll(set) + __popcll(~set & below(lane));
   return __builtin_amdgcn_ds_permute(at * 4, lane);
 }
+
+// An expert of the list and its tokens.
+struct Expert {
+  int e, row;    // and its tokens' first row of h
+  uint64_t set;  // its tokens
+  int many;
+
+  template <int TOKENS, int EXPERTS>
+  __device__ __forceinline__ void find(const Choices<TOKENS, EXPERTS> &c, int slot) {
+    const int entry = uniform(static_cast<int>(c.list[slot]));
+    e = entry & 0xffff;
+    row = entry >> 16;
+    const uint64_t tokens = c.tokens(e);
+    set = static_cast<uint32_t>(uniform(static_cast<int>(tokens)));
+    if (c.BITS > 32) set |= static_cast<uint64_t>(static_cast<uint32_t>(uniform(static_cast<int>(tokens >> 32)))) << 32;
+    many = __popcll(set);
+  }
+};
 
 // ---- operands --------------------------------------------------------------------
 
@@ -104,13 +186,17 @@ constexpr int kFragment = INT ? 64 : 32;  // k
 
 __device__ __forceinline__ bf16x8_t as_bf16(u32x4_t v) { return __builtin_bit_cast(bf16x8_t, v); }
 
-// Eight integers (exact in bf16).
+// Eight integers (exact in bf16): a conversion that takes its byte, and half of
+// one that packs two, for each.
 __device__ __forceinline__ bf16x8_t as_bf16(uint32_t lo, uint32_t hi) {
-  bf16x8_t r;
+  u32x4_t r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    r[i] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)))));
-  return r;
+  for (int i = 0; i < 4; ++i) {
+    const int v = static_cast<int>(i < 2 ? lo : hi), at = 16 * (i & 1);
+    r[i] = cvt_pk_bf16(static_cast<float>(static_cast<int>(__builtin_amdgcn_sbfe(v, at, 8))),
+                       static_cast<float>(static_cast<int>(__builtin_amdgcn_sbfe(v, at + 8, 8))));
+  }
+  return as_bf16(r);
 }
 
 // 16 bytes from `src`, of which the first `have` elements exist, the others 0.
@@ -221,15 +307,31 @@ __device__ __forceinline__ void sum_blocks(f32x4_t (&acc)[M][NC],
     }
   }
   if (b < last) {
-    B part;
-    part.load_end(rows, xrows, b * B::K, end);
-    part.multiply(acc);
+    Block<INT, M, NC, 1> part;
+    for (int k = b * B::K; k < end; k += kFragment<INT>) {
+      part.load_end(rows, xrows, k, end);
+      part.multiply(acc);
+    }
   }
 }
 
-// Fragments per block, so that two blocks fit the registers.
+// Fragments per block, so that two blocks leave registers for enough waves.
 template <int NC>
-constexpr int kDepth = NC == 4 ? 2 : 4;
+constexpr int kDepth = NC == 4 ? 1 : NC == 2 ? 2 : 4;
+
+// Calls `run` with NC = 1, 2 or 4 tiles of 16, whichever holds `tiles` first; MOST
+// bounds what is compiled.
+template <int MOST, typename F>
+__device__ __forceinline__ void with_tiles(int tiles, F run) {
+  if (MOST == 1 || tiles <= 1) {
+    run(std::integral_constant<int, 1>{});
+  } else if constexpr (MOST >= 2) {
+    if (MOST == 2 || tiles <= 2)
+      run(std::integral_constant<int, 2>{});
+    else if constexpr (MOST >= 4)
+      run(std::integral_constant<int, 4>{});
+  }
+}
 
 // ---- h ------------------------------------------------------------------------------
 
@@ -247,33 +349,52 @@ __device__ __forceinline__ float gated(int act, float g, float u) {
   }
 }
 
+// Channels n .. n + 3 of a row of h from its two projections.
+__device__ __forceinline__ void store_h(const DecodeArgs &a, int n, int row, f32x4_t gate, f32x4_t up) {
+  uint16_t *to = a.h + static_cast<int64_t>(row) * 2 * a.pitch + n;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (n + q >= a.inner) continue;
+    const float h = gated(a.act, gate[q], up[q]);
+    const uint16_t first = f32_to_bf16_rne(h);
+    to[q] = first;
+    // (An infinity has no remainder.)
+    to[a.pitch + q] = f32_to_bf16_rne(fabsf(h) < INFINITY ? h - bf16_to_f32(first) : 0.f);
+  }
+}
+
+// Scales of four of an expert's channels, n of them all.
+__device__ __forceinline__ f32x4_t load_scales(const float *scales, int e, int n, int at) {
+  f32x4_t v;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = scales[static_cast<int64_t>(e) * n + min(at + q, n - 1)];
+  return v;
+}
+
 // Sixteen channels of one expert per workgroup: its waves take blocks of k by
 // turns, and wave 0 joins their sums in order.
-template <bool INT>
+template <bool INT, int MOST>
 __global__ void __launch_bounds__(kUpWaves * 64) decode_up_kernel(DecodeArgs a) {
   typedef typename Element<INT>::T T;
-  __shared__ Choices choices;
-  __shared__ f32x4_t part[kUpWaves - 1][2][4][64];
+  __shared__ Choices<kMaxTokens, kRouteMaxExperts> choices;
+  __shared__ f32x4_t part[kUpWaves - 1][2][MOST][64];
   const int slot = blockIdx.x / a.tiles, n0 = (blockIdx.x - slot * a.tiles) * 16;
-  const int count = find_experts<kUpWaves * 64>(a, choices);
-  if (slot >= count) return;
-  const int e = uniform(choices.list[slot]);
+  if (slot >= find_experts<kUpWaves * 64, kMaxTokens, kRouteMaxExperts>(a, choices, nullptr).experts) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int mine = choice_of(a, choices, e, lane);
-  const uint64_t set = __ballot(mine >= 0);
-  const int tokens = __popcll(set), order = in_order(set);
+  Expert who;
+  who.find(choices, slot);
+  const int e = who.e, order = in_order(who.set);
   const int64_t row = min(n0 + (lane & 15), a.inner - 1) + static_cast<int64_t>(e) * a.inner;
   const T *const rows[2] = {static_cast<const T *>(a.gate) + row * a.hidden, static_cast<const T *>(a.up) + row * a.hidden};
-  auto run = [&](auto tiles) {
+  with_tiles<MOST>((who.many + 15) / 16, [&](auto tiles) {
     constexpr int NC = decltype(tiles)::value, U = kDepth<NC>, K = U * kFragment<INT>;
     const uint16_t *xrows[NC];
-    int choice[NC];
+    int to[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int i = c * 16 + (lane & 15), t = __shfl(order, i < tokens ? i : 0, 64);
-      xrows[c] = a.x + static_cast<int64_t>(t) * a.hidden;
-      const int from = __shfl(mine, t, 64);  // by every lane, before any is left out
-      choice[c] = i < tokens ? from : -1;
+      const int i = c * 16 + (lane & 15);
+      xrows[c] = a.x + static_cast<int64_t>(__shfl(order, i < who.many ? i : 0, 64)) * a.hidden;
+      to[c] = i < who.many ? who.row + i : -1;
     }
     f32x4_t acc[2][NC];
 #pragma unroll
@@ -295,107 +416,483 @@ __global__ void __launch_bounds__(kUpWaves * 64) decode_up_kernel(DecodeArgs a) 
 #pragma unroll
       for (int m = 0; m < 2; ++m)
         for (int i = 0; i < kUpWaves - 1; ++i) acc[m][c] += part[i][m][c][lane];
-      if (choice[c] < 0) continue;
-      uint16_t *to = a.h + static_cast<int64_t>(choice[c]) * a.pitch + n;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (n + q >= a.inner) continue;
-        float g = acc[0][c][q], u = acc[1][c][q];
-        if (INT) {
-          const int64_t at = static_cast<int64_t>(e) * a.inner + n + q;
-          g *= a.sgate[at];
-          u *= a.sup[at];
-        }
-        to[q] = f32_to_bf16_rne(gated(a.act, g, u));
+      if (INT) {
+        acc[0][c] *= load_scales(a.sgate, e, a.inner, n);
+        acc[1][c] *= load_scales(a.sup, e, a.inner, n);
       }
+      if (to[c] >= 0) store_h(a, n, to[c], acc[0][c], acc[1][c]);
     }
-  };
-  if (tokens <= 16)
-    run(std::integral_constant<int, 1>{});
-  else if (tokens <= 32)
-    run(std::integral_constant<int, 2>{});
-  else
-    run(std::integral_constant<int, 4>{});
+  });
 }
 
 // ---- y ------------------------------------------------------------------------------
 
+// Adds an expert's sixteen channels of a token to its sums: those of both parts of
+// h, which are two columns, HALF apart.
+template <int HALF>
+__device__ __forceinline__ void add_expert(f32x4_t acc, bool scaled, f32x4_t scale, int token, float share,
+                                           f32x4_t *sums) {
+  f32x4_t z;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    // row_ror by 16 - HALF: lane i of a row receives lane (i + HALF) % 16.
+    z[q] = acc[q] + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[q]), 0x120 + 16 - HALF, 0xf, 0xf, false));
+    if (scaled) z[q] *= scale[q];
+  }
+  if (token < 0) return;
+  f32x4_t &s = sums[token * 4 + ((threadIdx.x & 63) >> 4)];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s[q] += share * z[q];
+}
+
+// y of the workgroup's sixteen channels from its waves' sums, [wave][token][16].
+template <int WAVES>
+__device__ __forceinline__ void store_y(const DecodeArgs &a, int n0, const float *all) {
+  for (int i = threadIdx.x; i < a.tokens * 16; i += WAVES * 64) {
+    float v = 0.f;
+    for (int s = 0; s < WAVES; ++s) v += all[s * a.tokens * 16 + i];
+    const int n = n0 + (i & 15);
+    if (n < a.hidden) a.y[static_cast<int64_t>(i >> 4) * a.hidden + n] = f32_to_bf16_rne(v);
+  }
+}
+
 // Sixteen channels of y per workgroup, of every token: its waves share the blocks
 // of all experts' k evenly, each a run of them, and add what an expert gives to
-// sums of their own, which are joined in order at the end.
-template <bool INT>
-__global__ void __launch_bounds__(kDownWaves * 64) decode_down_kernel(DecodeArgs a) {
+// sums of their own, which are joined in order at the end.  The two parts of a
+// token's h are two columns of the matrix instruction, which has sixteen whether
+// they are used or not: eight tokens at a time.
+template <bool INT, int WAVES, int MOST>
+__global__ void __launch_bounds__(WAVES * 64) decode_down_kernel(DecodeArgs a) {
   typedef typename Element<INT>::T T;
-  constexpr int NT = kDownWaves * 64;
-  __shared__ Choices choices;
-  __shared__ f32x4_t sums[kDownWaves][kMaxTokens][4];  // [wave][token][channel / 4]
+  constexpr int NT = WAVES * 64;
+  __shared__ Choices<kMaxTokens, kRouteMaxExperts> choices;
+  __shared__ Weights<kMaxTokens, kRouteMaxExperts> weights;
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  f32x4_t *const all = reinterpret_cast<f32x4_t *>(dynamic);  // [wave][token][channel / 4]
   const int n0 = blockIdx.x * 16;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  for (int t = lane; t < a.tokens * 4; t += 64) sums[wave][t >> 2][t & 3] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int count = find_experts<NT>(a, choices);
-  constexpr int K = 2 * kFragment<INT>;  // the smallest block
-  const int per = (a.inner + K - 1) / K;  // blocks per expert
-  int b = static_cast<int>(static_cast<int64_t>(count) * per * wave / kDownWaves);
-  const int end = static_cast<int>(static_cast<int64_t>(count) * per * (wave + 1) / kDownWaves);
+  f32x4_t *const sums = all + wave * a.tokens * 4;
+  for (int t = lane; t < a.tokens * 4; t += 64) sums[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int count = find_experts<NT, kMaxTokens, kRouteMaxExperts>(a, choices, &weights).experts;
+  constexpr int K = kFragment<INT> * kDepth<1>;  // a unit of the waves' shares: whole blocks of every depth
+  const int per = (a.inner + K - 1) / K;         // units per expert
+  int b = static_cast<int>(static_cast<int64_t>(count) * per * wave / WAVES);
+  const int end = static_cast<int>(static_cast<int64_t>(count) * per * (wave + 1) / WAVES);
   while (b < end) {
     const int slot = b / per, from = b - slot * per, to = min(per, from + end - b);
-    const int e = uniform(choices.list[slot]);
-    const int mine = choice_of(a, choices, e, lane);
-    float weight = 0.f;
-    if (mine >= 0) {
-      for (int j = 0; j < a.topk; ++j)
-        if (choices.idx[lane * a.topk + j] == e) weight += a.w[lane * a.topk + j];
-    }
-    const uint64_t set = __ballot(mine >= 0);
-    const int tokens = __popcll(set), order = in_order(set);
+    Expert who;
+    who.find(choices, slot);
+    const int e = who.e, order = in_order(who.set);
     const int64_t row = min(n0 + (lane & 15), a.hidden - 1) + static_cast<int64_t>(e) * a.hidden;
     const T *const rows[1] = {static_cast<const T *>(a.down) + row * a.inner};
-    auto run = [&](auto tiles) {
-      constexpr int NC = decltype(tiles)::value;
-      const uint16_t *xrows[NC];
-      int token[NC];
-      float share[NC];
+    for (int base = 0; base < who.many; base += 8 * MOST) {
+      with_tiles<MOST>((who.many - base + 7) / 8, [&](auto tiles) {
+        constexpr int NC = decltype(tiles)::value, U = kDepth<NC>, PER = kDepth<1> / U;
+        const uint16_t *xrows[NC];
+        int token[NC];
+        float share[NC];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int i = c * 16 + (lane & 15), t = __shfl(order, i < tokens ? i : 0, 64);
-        xrows[c] = a.h + static_cast<int64_t>(__shfl(mine, t, 64)) * a.pitch;
-        share[c] = __shfl(weight, t, 64);
-        token[c] = i < tokens ? t : -1;
-      }
-      f32x4_t acc[1][NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) acc[0][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      sum_blocks<INT, 1, NC, 2>(acc, rows, xrows, from, 1, to, a.inner);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (token[c] < 0) continue;
-        f32x4_t z = acc[0][c];
-        if (INT) {
-          const int n = n0 + (lane >> 4) * 4;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            z[q] *= a.sdown[static_cast<int64_t>(e) * a.hidden + min(n + q, a.hidden - 1)];
+        for (int c = 0; c < NC; ++c) {
+          const int i = min(base + c * 8 + (lane & 7), who.many - 1), t = __shfl(order, i, 64);
+          xrows[c] = a.h + (static_cast<int64_t>(who.row + i) * 2 + (lane >> 3 & 1)) * a.pitch;
+          share[c] = weights.row[who.row + i];
+          token[c] = base + c * 8 + (lane & 7) < who.many && !(lane & 8) ? t : -1;
         }
-        f32x4_t &s = sums[wave][token[c]][lane >> 4];
+        f32x4_t acc[1][NC];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] += share[c] * z[q];
-      }
-    };
-    if (tokens <= 16)
-      run(std::integral_constant<int, 1>{});
-    else if (tokens <= 32)
-      run(std::integral_constant<int, 2>{});
-    else
-      run(std::integral_constant<int, 4>{});
+        for (int c = 0; c < NC; ++c) acc[0][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        constexpr int B = U * kFragment<INT>;
+        sum_blocks<INT, 1, NC, U>(acc, rows, xrows, from * PER, 1, min(to * PER, (a.inner + B - 1) / B), a.inner);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          f32x4_t scale = {1.f, 1.f, 1.f, 1.f};
+          if (INT) scale = load_scales(a.sdown, e, a.hidden, n0 + (lane >> 4) * 4);
+          add_expert<8>(acc[0][c], INT, scale, token[c], share[c], sums);
+        }
+      });
+    }
     b += to - from;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.tokens * 16; i += NT) {
-    const int t = i >> 4, c = i & 15;
-    float v = 0.f;
-    for (int s = 0; s < kDownWaves; ++s) v += sums[s][t][c >> 2][c & 3];
-    if (n0 + c < a.hidden) a.y[static_cast<int64_t>(t) * a.hidden + n0 + c] = f32_to_bf16_rne(v);
+  store_y<WAVES>(a, n0, reinterpret_cast<const float *>(all));
+}
+
+// ---- weights through LDS -------------------------------------------------------------
+//
+// Rows on 16-byte boundaries go from memory to LDS without a register
+// (buffer_load_dwordx4 ... lds), eight lanes to 128 bytes of a row: memory is read
+// in whole lines, and once, so past the caches.  A wave has a ring of stages of its
+// own and waits for nobody but its loads: a stage is 128 bytes of each of 16 rows of
+// the M matrices and, as rows of the same kind, what they are multiplied by, of NX
+// groups of eight columns.  Row r keeps its 16-byte chunk c at c ^ (r / 2 % 8), so
+// that a fragment's reads meet all banks.
+
+constexpr int kStageBytes = 128;  // of a weight row
+__device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
+
+// What a stage's loads start from: a segment's matrices and columns.
+template <int M, int NX>
+struct Source {
+  u32x4_t wd[M], xd;
+  int wv[2], xv[NX];  // this lane's bytes in the buffers: of its weight rows, of its columns
+
+  // Of every matrix `rows` rows exist, `pitch` bytes apart.  This lane's column of
+  // group g begins `at[g]` bytes into the buffer xd, or is not there (-1).
+  __device__ __forceinline__ void begin(int pitch, int rows, const int (&at)[NX]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = h * 8 + (lane >> 3);
+      wv[h] = r < rows ? r * pitch + ((lane & 7) ^ row_swizzle(r)) * 16 : kOutside;
+    }
+#pragma unroll
+    for (int g = 0; g < NX; ++g)
+      xv[g] = at[g] < 0 ? kOutside : at[g] + ((lane & 7) ^ row_swizzle(g * 8 + (lane >> 3))) * 16;
   }
+};
+
+template <bool INT, int M, int NX, int RING>
+struct Stream {
+  static constexpr int XB = INT ? 2 : 1;                    // 128-byte blocks of a column per stage
+  static constexpr int NC = NX <= 2 ? 1 : NX / 2;           // tiles of 16 columns
+  static constexpr int LOADS = 2 * M + NX * XB;             // of 1 KiB
+  static constexpr int STAGE = LOADS * 1024;
+  static constexpr int STAGES = RING / STAGE < 8 ? RING / STAGE : 8;
+  static_assert(STAGES >= 2 && (STAGES - 2) * LOADS < 64, "stages in the ring, loads that can be counted");
+
+  // Starts stage `s` (128 bytes at s * 128 of rows of `end` bytes) into the ring at
+  // LDS address `to`; where it is not live nothing is read.
+  static __device__ __forceinline__ void start(const Source<M, NX> &from, int s, bool live, int end, int to) {
+    const int lane = threadIdx.x & 63;
+    const int along = live ? s * kStageBytes : 0;
+    const bool part = live && (s + 1) * kStageBytes > end;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int chunk = (lane & 7) ^ row_swizzle(h * 8 + (lane >> 3));
+        const bool out = !live || (part && along + chunk * 16 >= end);
+        load_to_lds<true>(from.wd[m], to + (m * 2 + h) * 1024, out ? kOutside : from.wv[h], along);
+      }
+#pragma unroll
+    for (int g = 0; g < NX; ++g)
+#pragma unroll
+      for (int b = 0; b < XB; ++b) {
+        // (Integers: a stage's 128 elements are 256 bytes of a column.)
+        const int chunk = b * 8 + ((lane & 7) ^ row_swizzle(g * 8 + (lane >> 3)));
+        const bool out = !live || (part && along + chunk * (16 / XB) >= end);
+        load_to_lds(from.xd, to + (2 * M + g * XB + b) * 1024, out ? kOutside : from.xv[g],
+                    live ? along * XB + b * kStageBytes : 0);
+      }
+  }
+
+  static __device__ __forceinline__ void multiply(const unsigned char *stage, f32x4_t (&acc)[M][NC]) {
+    const int lane = threadIdx.x & 63, q = lane >> 4;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      u32x4_t w[M], x[NC][XB];
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int r = lane & 15;
+        w[m] = *reinterpret_cast<const u32x4_t *>(stage + m * 2048 + r * 128 + ((kk * 4 + q) ^ row_swizzle(r)) * 16);
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        // One group of eight columns stands in both halves of the sixteen.
+        const int col = NX == 1 ? lane & 7 : c * 16 + (lane & 15);
+        const unsigned char *row = stage + (2 * M + (col >> 3) * XB) * 1024 + (col & 7) * 128;
+#pragma unroll
+        for (int h = 0; h < XB; ++h) {
+          const int chunk = (INT ? 2 * q + h : kk * 4 + q) ^ row_swizzle(col);
+          x[c][h] = *reinterpret_cast<const u32x4_t *>(row + (INT ? kk * 1024 : 0) + chunk * 16);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int h = 0; h < XB; ++h) {
+          const bf16x8_t wf = INT ? as_bf16(w[m][2 * h], w[m][2 * h + 1]) : as_bf16(w[m]);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, as_bf16(x[c][h]), acc[m][c], 0, 0, 0);
+        }
+    }
+  }
+
+  // Goes through the segments from `segment` on, the loads of the next ones ahead
+  // of the sums of this one: for each, `finish` gets the sums of its stages from,
+  // from + step, .. below to (rows of `end` bytes).
+  template <typename S, typename F>
+  static __device__ __forceinline__ void run(unsigned char *ring, S segment, int step, int end, F finish) {
+    // (A wave without any segment has no buffers to load through.)
+    if (!segment.valid()) return;
+    const int at = lds_address(ring);
+    S ahead = segment;
+    Source<M, NX> source;
+    int s = 0, to = 0;
+    auto begin = [&] {
+      if (ahead.valid()) {
+        ahead.template begin<M, NX>(source);
+        s = ahead.from();
+        to = ahead.to();
+      }
+    };
+    auto next = [&](int buf) {
+      while (ahead.valid() && s >= to) {
+        ahead.next();
+        begin();
+      }
+      start(source, s, ahead.valid(), end, at + buf * STAGE);
+      s += step;
+    };
+    begin();
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) next(i);
+    int buf = 0, free = STAGES - 1;
+    for (; segment.valid(); segment.next()) {
+      f32x4_t acc[M][NC];
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int i = segment.from(); i < segment.to(); i += step) {
+        // This stage's loads have landed, and what was read of the one that is
+        // loaded next has arrived.
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((STAGES - 2) * LOADS) : "memory");
+        next(free);
+        free = buf;
+        multiply(ring + buf * STAGE, acc);
+        buf = buf + 1 == STAGES ? 0 : buf + 1;
+      }
+      finish(segment, acc);
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  }
+};
+
+// Calls `run` with NX = 1, 2, 4 or 8 groups of eight columns, whichever holds
+// `groups` first; MOST bounds what is compiled (more groups go by turns).
+template <int MOST, typename F>
+__device__ __forceinline__ void with_groups(int groups, F run) {
+  if (MOST == 1 || groups <= 1) {
+    run(std::integral_constant<int, 1>{});
+  } else if constexpr (MOST >= 2) {
+    if (MOST == 2 || groups <= 2) {
+      run(std::integral_constant<int, 2>{});
+    } else if constexpr (MOST >= 4) {
+      if (MOST == 4 || groups <= 4)
+        run(std::integral_constant<int, 4>{});
+      else if constexpr (MOST >= 8)
+        run(std::integral_constant<int, 8>{});
+    }
+  }
+}
+
+// Sixteen scales of an integer matrix's rows, of which this lane gets its four;
+// through scalar registers, whose loads are not counted with the stages'.
+__device__ __forceinline__ f32x4_t four_scales(const float *scales, int64_t at) {
+  typedef __attribute__((address_space(4))) const float *constant;
+  const constant s = (constant)(reinterpret_cast<uintptr_t>(uniform(scales + at)));
+  // (Pinned to scalars: a lane's own four would be a vector load.)
+  auto scalar = [](float v) {
+    asm volatile("" : "+s"(v));
+    return v;
+  };
+  const int q = (threadIdx.x & 63) >> 4;
+  f32x4_t v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float v0 = scalar(s[i]), v1 = scalar(s[4 + i]), v2 = scalar(s[8 + i]), v3 = scalar(s[12 + i]);
+    const float lo = q & 1 ? v1 : v0, hi = q & 1 ? v3 : v2;
+    v[i] = q & 2 ? hi : lo;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void barrier_without_loads() {
+  // What was written to LDS is there; the stages under way stay so.
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// A segment of the first kernel: sixteen channels of one expert for up to 8 NX of
+// its tokens; every wave of the workgroup has stages of it.
+template <typename C, int NX>
+struct UpSegment {
+  const DecodeArgs &a;
+  const C &choices;
+  int item, items, size, wave;  // 16 channels of an expert each, `gridDim.x` apart
+  int n0, base;
+  Expert who;
+
+  __device__ __forceinline__ void enter() {
+    if (!valid()) return;
+    const int slot = item / a.tiles;
+    n0 = (item - slot * a.tiles) * 16;
+    base = 0;
+    who.find(choices, slot);
+  }
+  __device__ __forceinline__ bool valid() const { return item < items; }
+  __device__ __forceinline__ void next() {
+    base += 8 * NX;
+    if (base < who.many) return;
+    item += gridDim.x;
+    enter();
+  }
+  __device__ __forceinline__ int from() const { return wave; }
+  __device__ __forceinline__ int to() const { return (a.hidden * size + kStageBytes - 1) / kStageBytes; }
+  template <int M, int G>
+  __device__ __forceinline__ void begin(Source<M, G> &s) const {
+    const int rows = min(16, a.inner - n0), pitch = a.hidden * size;
+    const int64_t row = (static_cast<int64_t>(who.e) * a.inner + n0) * pitch;
+    s.wd[0] = descriptor(static_cast<const uint8_t *>(a.gate) + row, rows * pitch);
+    s.wd[1] = descriptor(static_cast<const uint8_t *>(a.up) + row, rows * pitch);
+    s.xd = descriptor(a.x, a.tokens * a.hidden * 2);
+    const int order = in_order(who.set);
+    int at[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int i = base + g * 8 + ((threadIdx.x & 63) >> 3), t = __shfl(order, i & 63, 64);
+      at[g] = i < who.many ? t * a.hidden * 2 : -1;
+    }
+    s.begin(pitch, rows, at);
+  }
+};
+
+// decode_up_kernel's work.  TOKENS: what the launch is for; MOST: groups of eight
+// tokens at a time.
+template <bool INT, int TOKENS, int MOST, int RING>
+__global__ void __launch_bounds__(kUpWaves * 64) decode_up_direct_kernel(DecodeArgs a) {
+  constexpr int TILES = (MOST + 1) / 2;
+  typedef Choices<TOKENS, kDirectExperts> C;
+  __shared__ C choices;
+  __shared__ __align__(16) unsigned char rings[kUpWaves][RING];
+  // One group of columns stands twice in the sixteen, and is kept once.
+  constexpr int LANES = MOST == 1 ? 32 : 64;
+  __shared__ f32x4_t parts[kUpWaves][2 * TILES][LANES];
+  const Live live = find_experts<kUpWaves * 64, TOKENS, kDirectExperts>(a, choices, nullptr);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int at = MOST == 1 ? (lane >> 4) * 8 + (lane & 7) : lane;
+  with_groups<MOST>((live.most + 7) / 8, [&](auto groups) {
+    constexpr int NX = decltype(groups)::value;
+    typedef Stream<INT, 2, NX, RING> S;
+    typedef UpSegment<C, NX> Segment;
+    Segment first{a, choices, static_cast<int>(blockIdx.x), live.experts * a.tiles, INT ? 1 : 2, wave, 0, 0, {}};
+    first.enter();
+    int turn = 0;
+    S::run(rings[wave], first, kUpWaves, a.hidden * (INT ? 1 : 2), [&](const Segment &s, f32x4_t (&acc)[2][S::NC]) {
+      // The waves' sums meet in LDS, and waves take turns at joining them, in order.
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int c = 0; c < S::NC; ++c) parts[wave][m * S::NC + c][at] = acc[m][c];
+      barrier_without_loads();
+      f32x4_t sum[2][S::NC];
+      const bool joins = (turn++ & (kUpWaves - 1)) == wave;
+      if (joins) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int c = 0; c < S::NC; ++c) {
+            sum[m][c] = parts[0][m * S::NC + c][at];
+            for (int i = 1; i < kUpWaves; ++i) sum[m][c] += parts[i][m * S::NC + c][at];
+          }
+      }
+      barrier_without_loads();
+      if (!joins) return;
+      if (INT) {
+        const int64_t row = static_cast<int64_t>(s.who.e) * a.inner + s.n0;
+        const f32x4_t gate = four_scales(a.sgate, row), up = four_scales(a.sup, row);
+#pragma unroll
+        for (int c = 0; c < S::NC; ++c) sum[0][c] *= gate, sum[1][c] *= up;
+      }
+#pragma unroll
+      for (int c = 0; c < S::NC; ++c) {
+        const int i = s.base + c * 16 + (lane & 15);
+        if (i < s.who.many && (NX > 1 || !(lane & 8)))
+          store_h(a, s.n0 + (lane >> 4) * 4, s.who.row + i, sum[0][c], sum[1][c]);
+      }
+    });
+  });
+}
+
+// A segment of the second kernel: this wave's stages of one expert for up to
+// 4 NX of its tokens.
+template <typename C, int NX>
+struct DownSegment {
+  static constexpr int HALF = NX == 1 ? 4 : 8;  // columns between a token's two
+  const DecodeArgs &a;
+  const C &choices;
+  int slot, first, end, size, per;  // this wave's stages, counted over all experts
+  int base;
+  Expert who;
+
+  __device__ __forceinline__ void enter() {
+    if (!valid()) return;
+    base = 0;
+    who.find(choices, slot);
+  }
+  __device__ __forceinline__ bool valid() const { return slot * per < end; }
+  __device__ __forceinline__ void next() {
+    base += 4 * NX;
+    if (base < who.many) return;
+    ++slot;
+    enter();
+  }
+  __device__ __forceinline__ int from() const { return max(0, first - slot * per); }
+  __device__ __forceinline__ int to() const { return min(per, end - slot * per); }
+  template <int M, int G>
+  __device__ __forceinline__ void begin(Source<M, G> &s) const {
+    const int n0 = blockIdx.x * 16, rows = min(16, a.hidden - n0), pitch = a.inner * size;
+    s.wd[0] = descriptor(static_cast<const uint8_t *>(a.down) + (static_cast<int64_t>(who.e) * a.hidden + n0) * pitch,
+                         rows * pitch);
+    s.xd = descriptor(a.h, a.tokens * a.topk * 2 * a.pitch * 2);
+    int at[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int col = g * 8 + ((threadIdx.x & 63) >> 3), i = base + col / (2 * HALF) * HALF + col % HALF;
+      at[g] = i < who.many ? ((who.row + i) * 2 + col / HALF % 2) * a.pitch * 2 : -1;
+    }
+    s.begin(pitch, rows, at);
+  }
+};
+
+// decode_down_kernel's work.  MOST: groups of eight columns at a time.
+template <bool INT, int TOKENS, int WAVES, int MOST, int RING>
+__global__ void __launch_bounds__(WAVES * 64) decode_down_direct_kernel(DecodeArgs a) {
+  typedef Choices<TOKENS, kDirectExperts> C;
+  __shared__ C choices;
+  __shared__ Weights<TOKENS, kDirectExperts> weights;
+  __shared__ __align__(16) unsigned char rings[WAVES][RING];
+  __shared__ f32x4_t all[WAVES * TOKENS * 4];  // [wave][token][channel / 4]
+  const int n0 = blockIdx.x * 16;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  f32x4_t *const sums = all + wave * a.tokens * 4;
+  for (int t = lane; t < a.tokens * 4; t += 64) sums[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const Live live = find_experts<WAVES * 64, TOKENS, kDirectExperts>(a, choices, &weights);
+  with_groups<MOST>((live.most + 3) / 4, [&](auto groups) {
+    constexpr int NX = decltype(groups)::value;
+    typedef Stream<INT, 1, NX, RING> S;
+    typedef DownSegment<C, NX> Segment;
+    const int pitch = a.inner * (INT ? 1 : 2), per = (pitch + kStageBytes - 1) / kStageBytes;
+    const int64_t total = static_cast<int64_t>(live.experts) * per;
+    const int from = static_cast<int>(total * wave / WAVES), to = static_cast<int>(total * (wave + 1) / WAVES);
+    Segment first{a, choices, from / per, from, to, INT ? 1 : 2, per, 0, {}};
+    if (from == to) first.slot = live.experts, first.end = 0;
+    first.enter();
+    S::run(rings[wave], first, 1, pitch, [&](const Segment &s, f32x4_t (&acc)[1][S::NC]) {
+      f32x4_t scale = {1.f, 1.f, 1.f, 1.f};
+      if (INT) scale = four_scales(a.sdown, static_cast<int64_t>(s.who.e) * a.hidden + n0);
+      const int order = in_order(s.who.set);
+#pragma unroll
+      for (int c = 0; c < S::NC; ++c) {
+        const int i = s.base + c * 8 + (lane & (Segment::HALF - 1)), t = __shfl(order, i & 63, 64);
+        const bool there = i < s.who.many && (lane & 15) < Segment::HALF;
+        add_expert<Segment::HALF>(acc[0][c], INT, scale, there ? t : -1, weights.row[there ? s.who.row + i : 0], sums);
+      }
+    });
+  });
+  __syncthreads();
+  store_y<WAVES>(a, n0, reinterpret_cast<const float *>(all));
 }
 
 // ---- launchers -------------------------------------------------------------------
@@ -420,14 +917,54 @@ rrb_status check_spec(const rrb_decode_spec *s) {
   return RRB_OK;
 }
 
+// Tiles that the kernels are compiled for: 1, 2 or 4, of which one token's expert
+// can fill `tiles`.
+template <bool INT>
+auto up_kernel(int tiles) {
+  return tiles <= 1 ? decode_up_kernel<INT, 1> : tiles <= 2 ? decode_up_kernel<INT, 2> : decode_up_kernel<INT, 4>;
+}
+template <bool INT>
+auto down_kernel(int tiles) {
+  return tiles <= 1   ? decode_down_kernel<INT, kDownWaves, 1>
+         : tiles <= 2 ? decode_down_kernel<INT, kDownWaves, 2>
+                      : decode_down_kernel<INT, kDownWaves, 4>;
+}
+
 template <bool INT>
 rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
   const int most = a.experts < a.tokens * a.topk ? a.experts : a.tokens * a.topk;
-  hipLaunchKernelGGL(decode_up_kernel<INT>, dim3(static_cast<unsigned>(most * a.tiles)), dim3(kUpWaves * 64), 0, s, a);
+  dim3 up_grid(static_cast<unsigned>(most * a.tiles)), down_grid(static_cast<unsigned>((a.hidden + 15) / 16));
+  const int per = INT ? 16 : 8;  // elements of 16 bytes
+  const uintptr_t weights = reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.up) |
+                            reinterpret_cast<uintptr_t>(a.down) | reinterpret_cast<uintptr_t>(a.x);
+  // Where offsets into h fit the buffers' 31 bits (all but widths near 2^20).
+  const bool direct = a.experts <= kDirectExperts && a.hidden % per == 0 && a.inner % per == 0 && weights % 16 == 0 &&
+                      static_cast<int64_t>(a.tokens) * a.topk * 4 * a.pitch < (1LL << 31);
+  void (*up)(DecodeArgs), (*down)(DecodeArgs);
+  int down_waves = kDownWaves;
+  unsigned lds = 0;
+  if (direct) {
+    // Two workgroups a CU.
+    if (up_grid.x > 512) up_grid.x = 512;
+    const int t = a.tokens;
+    const bool dense = t > 8 && t * a.topk > 16 * a.experts, wide = down_grid.x > 256;
+    up = t <= 8  ? decode_up_direct_kernel<INT, 8, 1, 18432>
+         : dense ? decode_up_direct_kernel<INT, 64, 4, 24576>
+                 : decode_up_direct_kernel<INT, 64, 2, INT ? 16384 : 15360>;
+    if (t <= 8) down = wide ? decode_down_direct_kernel<INT, 8, 4, 2, 18432> : decode_down_direct_kernel<INT, 8, 8, 2, 18432>;
+    else if (dense) down = decode_down_direct_kernel<INT, 64, 4, INT ? 4 : 8, 30720>;
+    else down = wide ? decode_down_direct_kernel<INT, 64, 4, INT ? 2 : 4, 12288>
+                     : decode_down_direct_kernel<INT, 64, 8, INT ? 2 : 4, 12288>;
+    down_waves = dense || wide ? 4 : 8;
+  } else {
+    up = up_kernel<INT>((a.tokens + 15) / 16);
+    down = down_kernel<INT>((a.tokens + 7) / 8);
+    lds = kDownWaves * a.tokens * 64;
+  }
+  hipLaunchKernelGGL(up, up_grid, dim3(kUpWaves * 64), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(RRB_EHIP, "decode launch: %s", hipGetErrorString(e));
-  hipLaunchKernelGGL(decode_down_kernel<INT>, dim3(static_cast<unsigned>((a.hidden + 15) / 16)), dim3(kDownWaves * 64),
-                     0, s, a);
+  hipLaunchKernelGGL(down, down_grid, dim3(down_waves * 64), lds, s, a);
   e = hipGetLastError();
   return e == hipSuccess ? RRB_OK : fail(RRB_EHIP, "decode launch: %s", hipGetErrorString(e));
 }
@@ -445,7 +982,7 @@ rrb_status rrb_moe_decode_workspace(const rrb_decode_spec *spec, size_t *bytes) 
   *bytes = 0;
   const rrb_status st = check_spec(spec);
   if (st != RRB_OK) return st;
-  *bytes = static_cast<size_t>(spec->tokens * spec->topk * pitch_of(*spec) * 2);
+  *bytes = static_cast<size_t>(spec->tokens * spec->topk * 2 * pitch_of(*spec) * 2);
   return RRB_OK;
 }
 

@@ -18,6 +18,7 @@
 #include "rrb_activations.h"
 #include "rrb_internal.h"
 #include "rrb_kernels.h"
+#include "rrb_lds.h"
 
 namespace rrb {
 namespace {
@@ -26,7 +27,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 // Groups that a wave counts, 64 at a time, before it starts on its tile.
 constexpr int kMaxGroups = 4096;
@@ -99,17 +99,6 @@ __device__ __forceinline__ int32_t offset_at(const ProductArgs<EL> &p, int e) {
   if (!p.offsets) return e == 0 ? 0 : p.rows;
   const int32_t v = p.offsets[e];
   return v < 0 ? 0 : v > p.rows ? p.rows : v;
-}
-
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-template <typename EL>
-__device__ __forceinline__ const EL *uniform(const EL *q) {
-  const uint64_t v = reinterpret_cast<uint64_t>(q);
-  const uint32_t lo = uniform(static_cast<int>(v)), hi = uniform(static_cast<int>(v >> 32));
-  // As a global address: through a plain one the loads would be flat, which
-  // wait with the LDS's.
-  typedef __attribute__((address_space(1))) const EL *global;
-  return (const EL *)(global)(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 // ---- operand tiles in LDS -----------------------------------------------------
@@ -694,34 +683,6 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs<EL> p)
 // 16 groups, 4096 -> 2048, in 58 us (64 x 64 79, 256 x 256 74).  Four stages of
 // 32 x 128, eight to twelve of 32 x 64 and 128 x 256 in three were within 10% of
 // these or behind.
-
-template <typename EL>
-__device__ __forceinline__ u32x4_t descriptor(const EL *base, int bytes) {
-  const uint64_t v = reinterpret_cast<uint64_t>(uniform(base));
-  return u32x4_t{static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32), static_cast<uint32_t>(uniform(bytes)),
-                 0x00020000u};
-}
-constexpr int kOutside = 0x7fffffff;
-
-// Address of a workgroup's LDS as the loads below take it.
-__device__ __forceinline__ int lds_address(const unsigned char *lds) {
-  return static_cast<int>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const unsigned char *)lds));
-}
-
-// 16 bytes per lane from `d` at voffset + soffset to LDS address `at` (the
-// wave's first byte, uniform) + 16 * lane.  As assembly, because the compiler
-// would wait for every such load in flight before it reads any LDS
-// transposed; the kernels wait themselves, by count.  (m0 is reserved: the
-// compiler keeps nothing in it from one use to the next.  The five wait states
-// stand between a vector instruction that may just have written the scalar
-// operands and the load that reads them; the compiler sees to that only for
-// instructions of its own.)
-__device__ __forceinline__ void load_to_lds(u32x4_t d, int at, int voffset, int soffset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :
-               : "s"(uniform(at)), "v"(voffset), "s"(d), "s"(uniform(soffset))
-               : "memory");
-}
 
 // Two such loads, 8 KiB apart in LDS, behind one set of wait states.
 __device__ __forceinline__ void load_two_to_lds(u32x4_t d, int at, int voffset0, int voffset1, int soffset) {

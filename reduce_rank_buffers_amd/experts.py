@@ -115,9 +115,13 @@ def _spec(x, w, activation, what):
     return L.ExpertSpec(N, i, o, G, ACTIVATIONS[activation]), N, i, o, G
 
 
-def _offsets(offsets, G):
+def _offsets_for(offsets, G):
     if offsets is None and G != 1:
         raise ValueError(f"offsets is required with {G} groups")
+
+
+def _offsets(offsets, G):
+    _offsets_for(offsets, G)
     return _shaped(offsets, "offsets", (G + 1,), (torch.int32,))
 
 
@@ -236,6 +240,39 @@ def expert_linear_backward(d_out, x, offsets, w, pre=None, activation="none", d_
 # ---- serving -------------------------------------------------------------------
 
 _INT8 = (torch.int8,)
+_INT32 = (torch.int32,)
+
+
+def _required(**tensors):
+    for what, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{what} is required")
+
+
+def _checked(named):
+    """Addresses of (what, tensor, shape, dtypes), None where there is none,
+    and the GPU they are on; as _shaped and _addresses check them, in one pass
+    over tensors that are as they should be (a decode step's calls are bound by
+    the host)."""
+    out, dev = [], -1
+    for what, t, shape, types in named:
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype not in types or t.shape != shape or not t.is_contiguous():
+            _shaped(t, what, shape, types)
+        at = t.get_device()
+        if at != dev:
+            if dev != -1 or at < 0:
+                dev = -2
+            elif dev == -1:
+                dev = at
+        out.append(t.data_ptr())
+    if dev < 0 or dev != torch.cuda.current_device():
+        for what, t, _, _ in named:
+            if t is not None:
+                _on_gpu(t, what)
+    return out, dev
 
 
 def quantize_rows(x, q, scale, offsets=None, stream=None):
@@ -248,17 +285,16 @@ def quantize_rows(x, q, scale, offsets=None, stream=None):
     if not isinstance(x, torch.Tensor) or x.dim() < 2:
         raise ValueError("x: expected a tensor of at least two dimensions")
     dt, n = _dtype_of(x), x.shape[-1]
-    named = [_shaped(x, "x", x.shape, (x.dtype,)), _shaped(q, "q", x.shape, _INT8),
-             _shaped(scale, "scale", x.shape[:-1], _F32_TYPES)]
     groups = 0
     if offsets is not None:
         if x.dim() != 2 or not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
             raise ValueError("offsets: expected a tensor of one dimension and at least two entries, x of two dimensions")
         groups = offsets.numel() - 1
-    named.append(_shaped(offsets, "offsets", (groups + 1,), (torch.int32,)))
-    (xp, qp, sp, op), dev = _addresses(named, ("offsets",))
-    rows = scale.numel()
-    L.check(L.lib().rrb_quantize_rows(rows, n, dt, xp, op, groups, qp, sp, _raw_stream(stream, dev)),
+    _required(q=q, scale=scale)
+    (xp, qp, sp, op), dev = _checked((("x", x, x.shape, (x.dtype,)), ("q", q, x.shape, _INT8),
+                                      ("scale", scale, x.shape[:-1], _F32_TYPES),
+                                      ("offsets", offsets, (groups + 1,), _INT32)))
+    L.check(L.lib().rrb_quantize_rows(scale.numel(), n, dt, xp, op, groups, qp, sp, _raw_stream(stream, dev)),
             "rrb_quantize_rows")
     return q, scale
 
@@ -269,10 +305,12 @@ def expert_linear_int8(x, x_scale, offsets, w, w_scale, out, bias=None, activati
     [G, out]; out, bias [G, out] and residual [N, out] (may be out itself)
     bf16."""
     spec, N, i, o, G = _spec(x, w, activation, "w")
-    ins = [_shaped(x, "x", (N, i), _INT8), _shaped(x_scale, "x_scale", (N,), _F32_TYPES), _offsets(offsets, G),
-           _shaped(w, "w", (G, o, i), _INT8), _shaped(w_scale, "w_scale", (G, o), _F32_TYPES),
-           _shaped(bias, "bias", (G, o)), _shaped(residual, "residual", (N, o))]
-    at, dev = _addresses(ins + [_shaped(out, "out", (N, o))], ("offsets", "bias", "residual"))
+    _offsets_for(offsets, G)
+    _required(x_scale=x_scale, w_scale=w_scale, out=out)
+    at, dev = _checked((("x", x, (N, i), _INT8), ("x_scale", x_scale, (N,), _F32_TYPES),
+                        ("offsets", offsets, (G + 1,), _INT32), ("w", w, (G, o, i), _INT8),
+                        ("w_scale", w_scale, (G, o), _F32_TYPES), ("bias", bias, (G, o), _BF16_TYPES),
+                        ("residual", residual, (N, o), _BF16_TYPES), ("out", out, (N, o), _BF16_TYPES)))
     L.check(L.lib().rrb_expert_linear_int8(ctypes.byref(spec), *at, _raw_stream(stream, dev)),
             "rrb_expert_linear_int8")
     return out
@@ -283,10 +321,12 @@ def expert_gated_int8(x, x_scale, offsets, w_gate, gate_scale, w_up, up_scale, o
     [N, in], x_scale float32 [N], w_gate and w_up int8 [G, inner, in] with
     scales float32 [G, inner]; out [N, inner] bf16."""
     spec, N, i, o, G = _spec(x, w_gate, activation, "w_gate")
-    ins = [_shaped(x, "x", (N, i), _INT8), _shaped(x_scale, "x_scale", (N,), _F32_TYPES), _offsets(offsets, G),
-           _shaped(w_gate, "w_gate", (G, o, i), _INT8), _shaped(gate_scale, "gate_scale", (G, o), _F32_TYPES),
-           _shaped(w_up, "w_up", (G, o, i), _INT8), _shaped(up_scale, "up_scale", (G, o), _F32_TYPES)]
-    at, dev = _addresses(ins + [_shaped(out, "out", (N, o))], ("offsets",))
+    _offsets_for(offsets, G)
+    _required(x_scale=x_scale, gate_scale=gate_scale, w_up=w_up, up_scale=up_scale, out=out)
+    at, dev = _checked((("x", x, (N, i), _INT8), ("x_scale", x_scale, (N,), _F32_TYPES),
+                        ("offsets", offsets, (G + 1,), _INT32), ("w_gate", w_gate, (G, o, i), _INT8),
+                        ("gate_scale", gate_scale, (G, o), _F32_TYPES), ("w_up", w_up, (G, o, i), _INT8),
+                        ("up_scale", up_scale, (G, o), _F32_TYPES), ("out", out, (N, o), _BF16_TYPES)))
     L.check(L.lib().rrb_expert_gated_int8(ctypes.byref(spec), *at, _raw_stream(stream, dev)), "rrb_expert_gated_int8")
     return out
 
@@ -326,15 +366,19 @@ def moe_decode(x, topk_idx, topk_w, w_gate, w_up, w_down, out, activation="silu"
         if not isinstance(scales, (tuple, list)) or len(scales) != 3 or any(s is None for s in scales):
             raise ValueError("scales: expected those of w_gate, w_up and w_down")
         (sg, su, sd), types = scales, _INT8
-    named = [_shaped(x, "x", (T, h)), _shaped(topk_idx, "topk_idx", (T, k), (torch.int32,)),
-             _shaped(topk_w, "topk_w", (T, k), _F32_TYPES), _shaped(w_gate, "w_gate", (E, f, h), types),
-             _shaped(w_up, "w_up", (E, f, h), types), _shaped(w_down, "w_down", (E, h, f), types),
-             _shaped(sg, "scales[0]", (E, f), _F32_TYPES), _shaped(su, "scales[1]", (E, f), _F32_TYPES),
-             _shaped(sd, "scales[2]", (E, h), _F32_TYPES), _shaped(out, "out", (T, h))]
-    at, dev = _addresses(named, ("scales[0]", "scales[1]", "scales[2]"))
+    _required(topk_w=topk_w, w_up=w_up, w_down=w_down, out=out)
+    at, dev = _checked((("x", x, (T, h), _BF16_TYPES), ("topk_idx", topk_idx, (T, k), _INT32),
+                        ("topk_w", topk_w, (T, k), _F32_TYPES), ("w_gate", w_gate, (E, f, h), types),
+                        ("w_up", w_up, (E, f, h), types), ("w_down", w_down, (E, h, f), types),
+                        ("scales[0]", sg, (E, f), _F32_TYPES), ("scales[1]", su, (E, f), _F32_TYPES),
+                        ("scales[2]", sd, (E, h), _F32_TYPES), ("out", out, (T, h), _BF16_TYPES)))
     spec = L.DecodeSpec(T, h, f, E, k, ACTIVATIONS[activation], 0)
-    need = _decode_workspace(spec)
-    ws = _workspace(workspace, need, x, stream)
-    L.check(L.lib().rrb_moe_decode(ctypes.byref(spec), *at, ws.data_ptr(), need, _raw_stream(stream, dev)),
-            "rrb_moe_decode")
+    if workspace is None:
+        workspace = _workspace(None, _decode_workspace(spec), x, stream)
+    elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor of torch.uint8")
+    elif workspace.get_device() != dev:
+        _on_gpu(workspace, "workspace")
+    ws, size = workspace.data_ptr(), workspace.numel()  # (too small or misaligned: refused by the library)
+    L.check(L.lib().rrb_moe_decode(ctypes.byref(spec), *at, ws, size, _raw_stream(stream, dev)), "rrb_moe_decode")
     return out

@@ -68,7 +68,7 @@ REFUSED = [
     (_linear, {"x": _bf(5, 8)}, "x: dtype"),
     (_linear, {"w": _bf(2, 6, 8)}, "w: dtype"),
     (_linear, {"x_scale": _f32(6)}, "x_scale: shape"),
-    (_linear, {"x_scale": None}, "not on the current GPU"),
+    (_linear, {"x_scale": None}, "x_scale is required"),
     (_linear, {"w_scale": _f32(6)}, "w_scale: shape"),
     (_linear, {"w_scale": _f32(2, 6).double()}, "w_scale: dtype"),
     (_linear, {"offsets": None}, "offsets is required with 2 groups"),
@@ -81,7 +81,7 @@ REFUSED = [
     (_gated, {}, "not on the current GPU"),
     (_gated, {"w_up": _i8(2, 7, 8)}, "w_up: shape"),
     (_gated, {"gate_scale": _f32(2, 7)}, "gate_scale: shape"),
-    (_gated, {"up_scale": None}, "not on the current GPU"),
+    (_gated, {"up_scale": None}, "up_scale is required"),
     (_gated, {"out": _bf(4, 6)}, "out: shape"),
     (_decode, {}, "not on the current GPU"),
     (_decode, {"x": _f32(3, 8)}, "x: dtype"),
@@ -212,7 +212,7 @@ def test_abi_decode_refuses_pointers(librrb):
     n = ctypes.c_size_t()
     assert librrb.rrb_moe_decode_workspace(_layer(), None) == E
     assert librrb.rrb_moe_decode_workspace(_layer(), ctypes.byref(n)) == L.RRB_OK
-    assert n.value == rrb.moe_decode_workspace(3, 2, 8, 6) == 3 * 2 * 8 * 2
+    assert n.value == rrb.moe_decode_workspace(3, 2, 8, 6) == 3 * 2 * 2 * 8 * 2
     for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10):  # (6, 7, 8: one scale without the others)
         a = at(11)
         a[i] = None
