@@ -52,7 +52,26 @@ template <>
 struct Eight<uint16_t> {
   u32x4_t w;
   __device__ __forceinline__ void load(const uint16_t *src, int have) { w = load_chunk(src, have); }
+  // A whole one that is read once: past the caches, in lines that the wave reads whole.
+  __device__ __forceinline__ void stream(const uint16_t *src, bool there) {
+    typedef u32x4_t unaligned __attribute__((aligned(2)));
+    w = u32x4_t{0, 0, 0, 0};
+    if (there) w = __builtin_nontemporal_load(reinterpret_cast<const unaligned *>(src));
+  }
   __device__ __forceinline__ float at(int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+  // The largest |x| as fp32 bits, two by two: bf16 patterns order as the values do.
+  __device__ __forceinline__ uint32_t most(uint32_t than) const {
+    typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t bits = w[i] & 0x7fff7fffu;
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, bits));
+    }
+    return max(than, static_cast<uint32_t>(max(m[0], m[1])) << 16);
+  }
+  // Keeps the row as it lies in memory until it is used again.
+  __device__ __forceinline__ void keep() { asm volatile("" : "+v"(w)); }
 };
 template <>
 struct Eight<float> {
@@ -65,12 +84,19 @@ struct Eight<float> {
       for (int i = 0; i < 8; ++i) w[i] = i < have ? src[i] : 0.f;
     }
   }
+  __device__ __forceinline__ void stream(const float *src, bool there) { load(src, there ? 8 : 0); }
   __device__ __forceinline__ float at(int i) const { return w[i]; }
+  __device__ __forceinline__ uint32_t most(uint32_t than) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) than = max(than, __float_as_uint(w[i]) & 0x7fffffffu);
+    return than;
+  }
+  __device__ __forceinline__ void keep() {}
 };
 
-// L lanes (a wave's 64, or a workgroup's 1024) share a row, eight elements each
-// by turns.  HELD: widths of whole eights, in at most so many turns, which stay
-// in registers; 0: any width, the row read twice.
+// L lanes (a wave's 64, or a workgroup's 256 or 1024) share a row, eight elements
+// each by turns.  HELD: widths of whole eights, in at most so many turns, which
+// stay in registers; 0: any width, the row read twice.
 template <typename T, int L, int HELD>
 __global__ void __launch_bounds__(L == 64 ? 256 : L) quantize_kernel(QuantizeArgs a) {
   constexpr int ROWS = L == 64 ? 4 : 1;  // per workgroup at a time
@@ -90,19 +116,18 @@ __global__ void __launch_bounds__(L == 64 ? 256 : L) quantize_kernel(QuantizeArg
     // The largest |x| as its bits, which order as the values do and put
     // infinities and NaN above them.
     uint32_t most = 0;
-    auto take = [&](const Eight<T> &e) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(e.at(i)) & 0x7fffffffu);
-    };
     if (HELD) {
 #pragma unroll
-      for (int h = 0; h < HELD; ++h) v[h].load(x + (h * L + lane) * 8, (h * L + lane) * 8 < a.width ? 8 : 0);
+      for (int h = 0; h < HELD; ++h) v[h].stream(x + (h * L + lane) * 8, (h * L + lane) * 8 < a.width);
 #pragma unroll
-      for (int h = 0; h < HELD; ++h) take(v[h]);
+      for (int h = 0; h < HELD; ++h) {
+        most = v[h].most(most);
+        v[h].keep();
+      }
     } else {
       for (int c = lane * 8; c < a.width; c += L * 8) {
         v[0].load(x + c, a.width - c);
-        take(v[0]);
+        most = v[0].most(most);
       }
     }
 #pragma unroll
@@ -165,21 +190,27 @@ __global__ void __launch_bounds__(L == 64 ? 256 : L) quantize_kernel(QuantizeArg
   }
 }
 
+// A wave per row where rows are many and at most 4096 wide, else a workgroup of 256,
+// or of 1024 beyond 8192 (us: 8000 x 4096 bf16 28 by waves, 31 by 256 lanes; 4096 x
+// 7168 30 and 26; 16 x 7168 10.6 and 5.6; 32768 x 7168 127 and 125, 5.5 TB/s, where
+// loads that stay in the caches took 140 and rows held as fp32 163).
 template <typename T>
 void launch_quantize(const QuantizeArgs &a, hipStream_t s) {
   void (*kernel)(QuantizeArgs);
-  const int turns = a.width % 8 ? 0 : (a.width + 511) / 512;  // whole ones
-  const bool wide = a.width > 16 * 512;
-  if (wide) kernel = quantize_kernel<T, 1024, 0>;
-  else if (turns == 0) kernel = quantize_kernel<T, 64, 0>;
-  else if (turns <= 2) kernel = quantize_kernel<T, 64, 2>;
-  else if (turns <= 4) kernel = quantize_kernel<T, 64, 4>;
-  else if (turns <= 8) kernel = quantize_kernel<T, 64, 8>;
-  else kernel = quantize_kernel<T, 64, 16>;
-  const int rows = wide ? 1 : 4;
+  const int lanes = a.width > 8192 ? 1024 : a.width > 512 && (a.rows < 4096 || a.width > 4096) ? 256 : 64;
+  const int turns = a.width % 8 ? 0 : (a.width + lanes * 8 - 1) / (lanes * 8);  // whole ones
+#define RRB_PICK(LANES)                                     \
+  turns == 0 || turns > 8 ? quantize_kernel<T, LANES, 0>    \
+  : turns <= 1            ? quantize_kernel<T, LANES, 1>    \
+  : turns <= 2            ? quantize_kernel<T, LANES, 2>    \
+  : turns <= 4            ? quantize_kernel<T, LANES, 4>    \
+                          : quantize_kernel<T, LANES, LANES == 256 ? 4 : 8>
+  kernel = lanes == 1024 ? RRB_PICK(1024) : lanes == 256 ? RRB_PICK(256) : RRB_PICK(64);
+#undef RRB_PICK
+  const int rows = lanes == 64 ? 4 : 1;
   const int64_t blocks = (a.rows + rows - 1) / rows;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : 1 << 20)),
-                     dim3(wide ? 1024 : 256), 0, s, a);
+                     dim3(lanes == 64 ? 256 : lanes), 0, s, a);
 }
 
 // ---- the products -----------------------------------------------------------------

@@ -312,6 +312,18 @@ __device__ __forceinline__ void store_tile(const ProductArgs<EL> &p, const typen
     if (!GATED && bias) load_cols<W>(bias + n0 + n, have, b);
     if constexpr (INT) load_scales<W>(scales.col[0] + n0 + n, have, cs);
     if constexpr (INT && GATED) load_scales<W>(scales.col[1] + n0 + n, have, us);
+    // Integers: the residual of all rows is asked for before any is needed (8000 x
+    // 4096 -> 8192, us, gelu with the whole epilogue: 298 -> 286, silu 287 -> 267; row
+    // by row each load was waited for).
+    constexpr bool EARLY = INT && !GATED;
+    [[maybe_unused]] uint32_t early[EARLY ? FM : 1][W / 2];
+    if constexpr (EARLY) {
+      if (residual && have >= W) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          if (row_at(i) < mvalid) __builtin_memcpy(early[i], residual + row_at(i) * p.ldc + n0 + n, W * 2);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int m = row_at(i);
@@ -346,7 +358,13 @@ __device__ __forceinline__ void store_tile(const ProductArgs<EL> &p, const typen
         for (int q = 0; q < W; ++q) v[q] = activate<ACT>(v[q]);
         if (residual) {
           float r[W];
-          load_cols<W>(residual + m * p.ldc + n0 + n, have, r);
+          if (EARLY && have >= W) {
+#pragma unroll
+            for (int q = 0; q < W; ++q)
+              r[q] = q & 1 ? bf16_hi(early[EARLY ? i : 0][q >> 1]) : bf16_lo(early[EARLY ? i : 0][q >> 1]);
+          } else {
+            load_cols<W>(residual + m * p.ldc + n0 + n, have, r);
+          }
 #pragma unroll
           for (int q = 0; q < W; ++q) v[q] += r[q];
         }
@@ -694,7 +712,7 @@ __device__ __forceinline__ void load_two_to_lds(u32x4_t d, int at, int voffset0,
       : "memory");
 }
 
-template <int BM, int BN, int WR, int WC, int STAGES, int FORM, bool GATED, typename EL>
+template <int BM, int BN, int WR, int WC, int STAGES, int FORM, bool GATED, typename EL, bool ONCE = false>
 __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs<EL> p) {
   constexpr int PER = kPer<EL>, STEP = kSteps<EL>;
   constexpr int NT = WR * WC * 64;
@@ -785,7 +803,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
         }
         // The wave's eight rows are all gate rows or all up rows.
         const bool up = GATED && gated_up((i * NT + wave * 64) >> 3);
-        load_to_lds(up ? d1 : d0, tb + i * NT * 16, v, along);
+        load_to_lds<ONCE>(up ? d1 : d0, tb + i * NT * 16, v, along);
       }
     }
   };
@@ -1155,6 +1173,52 @@ double estimate(const ProductArgs<EL> &p, int bm, int bn, int resident, double s
   return std::max(matrix, std::max(moved * kStep * 2 / 10e6, weights / 5.5e6 * whole));
 }
 
+// Estimated time (us) of an integer product over BM x BN tiles: rounds of tiles as
+// above, or the weights from HBM.  In whole tiles where one group has all rows; where
+// there are more how many tiles are partial is not known, and rounds come out a
+// third longer.
+template <bool GATED>
+double estimate_integers(const ProductArgs<int8_t> &p, int bm, int bn, int resident, double step, double rest) {
+  const double live = p.groups < p.rows ? p.groups : p.rows;
+  const int cols = GATED ? bn / 2 : bn;
+  const double across = (p.n + cols - 1) / cols, steps = (p.k + kSteps<int8_t> - 1) / kSteps<int8_t>;
+  double down = static_cast<double>(p.rows) / bm + live / 2;
+  if (down < live) down = live;
+  if (p.groups == 1) down = (p.rows + bm - 1) / bm;
+  double rounds = down * across / (256.0 * resident);
+  rounds = rounds <= 1 ? 1 : p.groups == 1 ? std::ceil(rounds) : rounds + 0.35;
+  return std::max(3 + rounds * (steps * step + rest), live * p.n * (GATED ? 2.0 : 1.0) * p.k / 5.2e6);
+}
+
+// Integer products have half the steps of bf16 ones, so what a tile takes besides
+// its steps weighs more, and shapes between 64 x 64 and 256 x 256 are worth their
+// place.  Measured (us; 256 x 256, 128 x 256, 64 x 128, 64 x 64), products of `rows`
+// in each of G groups:
+//   G 1, 8000 rows, 4096 x 8192: 239, 313, 428, 548   G 1, 2048, 4096 x 2048: 52, 40, 30, 38
+//   G 2, 1024, 4096 x 4096: 57, 45, 57, 71            G 1, 512, 8192 x 1024: 96, 64, 40, 27
+//   G 9, 334, 2000 x 1112: 35, 28, 26, 31             G 32, 160, 2048 x 1024: 34, 30, 36, 39
+//   G 16, 64, 4096 x 2048: 49, 45, 41, 36             gated, G 32, 74 to 410, 7168 x 2048: 244, 223, 296, 350
+// Weights of groups that have few rows are read by one row of tiles, and go past
+// the caches (G 24, 1 row, 7168 x 2048 gated: 119 -> 110, 6.4 TB/s; G 32, 16 rows: 88
+// -> 81; where three rows of tiles share them, G 32, 160 rows: 39 -> 46).
+template <bool GATED>
+rrb_status launch_integers(const ProductArgs<int8_t> &p, hipStream_t s) {
+  const int64_t rows = p.rows, groups = p.groups;
+  if (rows <= 32 * groups)
+    return launch_tiles<64, 64, kForward, GATED>(product_direct_kernel<64, 64, 2, 2, 5, kForward, GATED, int8_t, true>, 256,
+                                                 p, s);
+  const double big = estimate_integers<GATED>(p, 256, 256, 1, 1.4, 12), wide = estimate_integers<GATED>(p, 128, 256, 1, 0.95, 8.6);
+  const double mid = estimate_integers<GATED>(p, 64, 128, 2, 0.58, 9), low = estimate_integers<GATED>(p, 64, 64, 2, 0.35, 6.3);
+  const double best = std::min(std::min(big, wide), std::min(mid, low));
+  if (low == best || rows <= 64 * groups)
+    return launch_tiles<64, 64, kForward, GATED>(product_direct_kernel<64, 64, 2, 2, 5, kForward, GATED, int8_t>, 256, p, s);
+  if (mid == best)
+    return launch_tiles<64, 128, kForward, GATED>(product_direct_kernel<64, 128, 2, 2, 3, kForward, GATED, int8_t>, 256, p, s);
+  if (wide == best)
+    return launch_tiles<128, 256, kForward, GATED>(product_direct_kernel<128, 256, 2, 4, 3, kForward, GATED, int8_t>, 512, p, s);
+  return launch_tiles<256, 256, kForward, GATED>(product_turns_kernel<kForward, GATED, int8_t>, 512, p, s);
+}
+
 // Three tile shapes.  256 x 256 is the fastest by far where there are enough
 // tiles to fill the CUs (1.3 PFLOP/s; 64 x 256 reaches 0.7, 64 x 64 0.5), but
 // few tiles leave CUs idle, and few rows leave a tile empty.  Measured (us;
@@ -1172,6 +1236,7 @@ rrb_status launch_product(const ProductArgs<EL> &p, hipStream_t s) {
       return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED, EL>, 256, p, s);
     return launch_tiles<64, 64, FORM, GATED>(product_kernel<64, 64, 2, 2, FORM, GATED, EL>, 256, p, s);
   }
+  if constexpr (sizeof(EL) == 1) return launch_integers<GATED>(p, s);
   // A tile of at most 128 valid rows takes about half a 256-row step.
   const bool half = FORM != kGradW && static_cast<int64_t>(p.groups) * 128 >= p.rows;
   const double big = estimate<FORM, GATED>(p, 256, 256, 1, half ? 0.9 : 1.55, 8);

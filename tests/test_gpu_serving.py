@@ -256,6 +256,27 @@ def test_large_int8(i, o, lead, tail):
     _gated_int8(Integers(14, X.RAGGED, i, o // 2, lead, tail), ACTS[(i + 2) % 5])
 
 
+@pytest.mark.parametrize("sizes,i,o", [([1500, 0, 300, 1], 2064, 2056), ([700, 129, 64, 1, 0, 300], 1040, 2056),
+                                       ([2500, 1, 0, 4000, 77], 528, 4104), ([900, 0, 65, 257], 272, 1032),
+                                       ([8000], 272, 4104), ([300, 130, 0, 1, 500], 4112, 520),
+                                       ([64, 1, 30, 0] * 8, 1040, 264)], ids=lambda v: str(v)[:24])
+def test_int8_tile_shapes(sizes, i, o):
+    """Each tile shape that the sizes choose, with partial tiles in both
+    directions and a residual in the output's place."""
+    require_gpu()
+    _say(f"int8 tiles {sizes} {i} {o}")
+    _gated_int8(Integers(31, sizes, i, o, 1, 2), "silu")
+    _gated_int8(Integers(32, sizes, i, o // 2), "gelu")
+    _linear_int8(Integers(33, sizes, i, o, 1, 2), "gelu_tanh", True, True)
+    p = Integers(34, sizes, i, o)
+    w, s = p.weight()
+    r = X._bf16(p.rng, (p.N, p.o))
+    y = p.put(r)
+    rrb.expert_linear_int8(p.put(p.x), p.put(p.sx), p.d_off, p.put(w), p.put(s), y, residual=y)
+    prod, nr = p.product(w, s), r.double().numpy()
+    _check("out", y, prod + nr, SCALED * np.abs(prod) + ADD * (np.abs(prod) + np.abs(nr)))
+
+
 def test_int8_sums_are_exact():
     """The largest sums: all -128 against all -128 at the largest depth."""
     require_gpu()
