@@ -258,8 +258,9 @@ __device__ __forceinline__ void store_tile(const ProductArgs<EL> &p, const typen
   constexpr bool INT = sizeof(EL) == 1;
   constexpr int W = WIDE ? 8 : 4;                           // consecutive columns per lane
   constexpr int BLOCKS = (GATED ? 2 : 1) * (WIDE ? 2 : 1);  // blocks that make them
+  static_assert(FN % BLOCKS == 0, "a wave has whole outputs");
   const int lane = threadIdx.x & 63;
-  auto row_at = [&](int i) { return spot.m + (i >= FM / 2 ? spot.down + (i - FM / 2) * 16 : i * 16) + (lane & 15); };
+  auto row_at = [&](int i) { return spot.m + (FM > 1 && i >= FM / 2 ? spot.down + (i - FM / 2) * 16 : i * 16) + (lane & 15); };
   auto col_at = [&](int j) {
     const int g = j / BLOCKS, halves = FN / BLOCKS / 2;
     return spot.n + (halves && g >= halves ? spot.right + (g - halves) * W * 4 : g * W * 4) + (lane >> 4) * W;
@@ -1198,14 +1199,17 @@ double estimate_integers(const ProductArgs<int8_t> &p, int bm, int bn, int resid
 //   G 2, 1024, 4096 x 4096: 57, 45, 57, 71            G 1, 512, 8192 x 1024: 96, 64, 40, 27
 //   G 9, 334, 2000 x 1112: 35, 28, 26, 31             G 32, 160, 2048 x 1024: 34, 30, 36, 39
 //   G 16, 64, 4096 x 2048: 49, 45, 41, 36             gated, G 32, 74 to 410, 7168 x 2048: 244, 223, 296, 350
-// Weights of groups that have few rows are read by one row of tiles, and go past
-// the caches (G 24, 1 row, 7168 x 2048 gated: 119 -> 110, 6.4 TB/s; G 32, 16 rows: 88
-// -> 81; where three rows of tiles share them, G 32, 160 rows: 39 -> 46).
+// Groups of few rows take 32 x 64 tiles, three workgroups a CU, and their weights,
+// which one row of tiles reads, go past the caches (G 24, 1 row, 2048 x 7168: 75 at
+// 64 x 64, 71 past the caches, 61 at 32 x 64, 5.8 TB/s; 7168 x 2048 gated: 119, 110,
+// 105; G 32, 16 rows, 7168 x 2048: 88, 81, 75; G 1, 1 row, 4096 x 4096: 17, 17, 14.
+// Where three rows of tiles share the weights, G 32, 160 rows: 39 and 46 past the
+// caches).
 template <bool GATED>
 rrb_status launch_integers(const ProductArgs<int8_t> &p, hipStream_t s) {
   const int64_t rows = p.rows, groups = p.groups;
   if (rows <= 32 * groups)
-    return launch_tiles<64, 64, kForward, GATED>(product_direct_kernel<64, 64, 2, 2, 5, kForward, GATED, int8_t, true>, 256,
+    return launch_tiles<32, 64, kForward, GATED>(product_direct_kernel<32, 64, 2, 2, 4, kForward, GATED, int8_t, true>, 256,
                                                  p, s);
   const double big = estimate_integers<GATED>(p, 256, 256, 1, 1.4, 12), wide = estimate_integers<GATED>(p, 128, 256, 1, 0.95, 8.6);
   const double mid = estimate_integers<GATED>(p, 64, 128, 2, 0.58, 9), low = estimate_integers<GATED>(p, 64, 64, 2, 0.35, 6.3);
