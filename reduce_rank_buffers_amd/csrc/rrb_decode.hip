@@ -199,18 +199,23 @@ __device__ __forceinline__ bf16x8_t as_bf16(uint32_t lo, uint32_t hi) {
   return as_bf16(r);
 }
 
-// 16 bytes from `src`, of which the first `have` elements exist, the others 0.
+// 16 bytes from `src` in a row of `length` elements, of which `have` are left there;
+// the others are 0.
 template <typename T>
-__device__ __forceinline__ u32x4_t load_part(const T *src, int have) {
+__device__ __forceinline__ u32x4_t load_part(const T *src, int have, int length) {
   constexpr int N = 16 / sizeof(T), PER = 4 / sizeof(T);
   u32x4_t v = {0, 0, 0, 0};
   if (have >= N) {
     __builtin_memcpy(&v, src, 16);
+  } else if (have > 0 && length >= N) {
+    uint64_t w[2];
+    load_last(src, have * static_cast<int>(sizeof(T)), w);
+    __builtin_memcpy(&v, w, 16);
   } else if (have > 0) {
+    for (int i = 0; i < have; ++i) {
+      const uint32_t e = static_cast<uint32_t>(src[i]) << (8 * static_cast<int>(sizeof(T)) * (i % PER));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint32_t e = src[i < have ? i : have - 1];
-      v[i / PER] |= i < have ? e << (8 * static_cast<int>(sizeof(T)) * (i % PER)) : 0u;
+      for (int q = 0; q < 4; ++q) v[q] |= i / PER == q ? e : 0u;
     }
   }
   return v;
@@ -255,11 +260,11 @@ struct Block {
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * kFragment<INT> + q * (kFragment<INT> / 4);
 #pragma unroll
-      for (int m = 0; m < M; ++m) w[m][u] = load_part(rows[m] + k, end - k);
+      for (int m = 0; m < M; ++m) w[m][u] = load_part(rows[m] + k, end - k, end);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int h = 0; h < XS; ++h) x[c][u][h] = load_part(xrows[c] + k + h * 8, end - k - h * 8);
+        for (int h = 0; h < XS; ++h) x[c][u][h] = load_part(xrows[c] + k + h * 8, end - k - h * 8, end);
     }
   }
   __device__ __forceinline__ void multiply(f32x4_t (&acc)[M][NC]) const {
@@ -307,8 +312,10 @@ __device__ __forceinline__ void sum_blocks(f32x4_t (&acc)[M][NC],
     }
   }
   if (b < last) {
-    Block<INT, M, NC, 1> part;
-    for (int k = b * B::K; k < end; k += kFragment<INT>) {
+    // (At once where the registers have room.)
+    typedef Block<INT, M, NC, NC == 1 ? U : 1> P;
+    P part;
+    for (int k = b * B::K; k < end; k += P::K) {
       part.load_end(rows, xrows, k, end);
       part.multiply(acc);
     }

@@ -60,6 +60,16 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&a)[8]) {
   return o;
 }
 
+// The last `have` (1 .. 15) bytes of a run of at least 16, which ends `have` bytes
+// behind `src`: the 16 bytes to the run's end, moved down, and zeros behind them.  One
+// load where the bytes one by one would be as many.
+__device__ __forceinline__ void load_last(const void *src, int have, uint64_t (&v)[2]) {
+  __builtin_memcpy(v, static_cast<const char *>(src) + have - 16, 16);
+  const int by = 8 * (16 - have);  // 8 .. 120 bits
+  v[0] = by >= 64 ? v[1] >> (by - 64) : v[0] >> by | v[1] << (64 - by);
+  v[1] = by >= 64 ? 0 : v[1] >> by;
+}
+
 // Fixed rank-order fold of 8 bf16 lanes from R sources: fp32 accumulation,
 // one rounding at the end.  The adds are written one per step so the
 // compiler cannot reassociate them (no fast-math anywhere in this library).

@@ -174,20 +174,23 @@ __device__ __forceinline__ u32x4_t load_chunk(const uint16_t *src, int64_t have)
   return v;
 }
 
-// The same of 16 8-bit integers.
-__device__ __forceinline__ u32x4_t load_chunk(const int8_t *src, int64_t have) {
+// The same of 16 8-bit integers, of a row of `length`, whose end the chunk may pass.
+__device__ __forceinline__ u32x4_t load_chunk(const int8_t *src, int64_t have, int length) {
   u32x4_t v = {0, 0, 0, 0};
   if (have >= 16) {
     __builtin_memcpy(&v, src, 16);
+  } else if (have > 0 && length >= 16) {
+    uint64_t w[2];
+    load_last(src, static_cast<int>(have), w);
+    __builtin_memcpy(&v, w, 16);
   } else if (have > 0) {
-    uint32_t e[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) e[i] = static_cast<uint8_t>(src[i < have ? i : have - 1]);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i >> 2] |= i < have ? e[i] << (8 * (i & 3)) : 0;
+    for (int i = 0; i < 15; ++i)
+      if (i < have) v[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[i])) << (8 * (i & 3));
   }
   return v;
 }
+__device__ __forceinline__ u32x4_t load_chunk(const uint16_t *src, int64_t have, int) { return load_chunk(src, have); }
 
 // W consecutive columns of one row, W = 4 or 8, as fp32; `have` of them exist.
 template <int W>
@@ -617,20 +620,20 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs<EL> p)
 #pragma unroll
     for (int i = 0; i < CA; ++i) {
       const int id = i * NT + tid;
-      if (A_COL) {
+      if constexpr (A_COL) {
         const int kr = id / (BM / 8), pos = id % (BM / 8);
         const int ch = pos ^ (col_swizzle<BM>(kr) << 1);
         ra[i] = load_chunk(t.a[0] + (k0 + kr) * p.lda + ch * 8, there(k0 + kr, p.m - t.m0 - ch * 8, p.m, p.lda));
       } else {
         const int r = id >> 3, ch = (id & 7) ^ row_swizzle(r);
         const int64_t have = klen - k0 - ch * PER;
-        ra[i] = load_chunk(t.a[h] + r * p.lda + k0 + ch * PER, r < t.mvalid ? have : 0);
+        ra[i] = load_chunk(t.a[h] + r * p.lda + k0 + ch * PER, r < t.mvalid ? have : 0, klen);
       }
     }
 #pragma unroll
     for (int i = 0; i < CB; ++i) {
       const int id = i * NT + tid;
-      if (B_COL) {
+      if constexpr (B_COL) {
         const int kr = id / (BN / 8), pos = id % (BN / 8);
         const int ch = pos ^ (col_swizzle<BN>(kr) << 1);
         rb[i] = load_chunk(t.b[h] + (k0 + kr) * p.ldb + ch * 8, there(k0 + kr, p.n - t.n0 - ch * 8, p.n, p.ldb));
@@ -639,7 +642,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_kernel(ProductArgs<EL> p)
         const int64_t have = klen - k0 - ch * PER;
         const int n = GATED ? gated_row(r) : r;
         const EL *src = GATED && gated_up(r) ? t.b[1] : t.b[0];
-        rb[i] = load_chunk(src + n * p.ldb + k0 + ch * PER, t.n0 + n < p.n ? have : 0);
+        rb[i] = load_chunk(src + n * p.ldb + k0 + ch * PER, t.n0 + n < p.n ? have : 0, klen);
       }
     }
   };
@@ -1205,9 +1208,18 @@ double estimate_integers(const ProductArgs<int8_t> &p, int bm, int bn, int resid
 // 105; G 32, 16 rows, 7168 x 2048: 88, 81, 75; G 1, 1 row, 4096 x 4096: 17, 17, 14.
 // Where three rows of tiles share the weights, G 32, 160 rows: 39 and 46 past the
 // caches).
+// Rows off 16-byte boundaries: 128 x 128 by eight waves where there are enough (G 9,
+// 334 rows, 2001 x 1111: 43 -> 31, gated 72 -> 42; G 1, 4000, 4001 x 4001: 241 ->
+// 136), else 64 x 64 (G 16, 1 row, 2001 x 1111: 24 and 21).
 template <bool GATED>
-rrb_status launch_integers(const ProductArgs<int8_t> &p, hipStream_t s) {
+rrb_status launch_integers(const ProductArgs<int8_t> &p, bool direct, hipStream_t s) {
   const int64_t rows = p.rows, groups = p.groups;
+  if (!direct) {
+    const int64_t tiles = (rows / 128 + std::min(groups, rows) / 2) * ((p.n + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
+    if (rows > 64 * groups && tiles >= 128)
+      return launch_tiles<128, 128, kForward, GATED>(product_kernel<128, 128, 2, 4, kForward, GATED, int8_t>, 512, p, s);
+    return launch_tiles<64, 64, kForward, GATED>(product_kernel<64, 64, 2, 2, kForward, GATED, int8_t>, 256, p, s);
+  }
   if (rows <= 32 * groups)
     return launch_tiles<32, 64, kForward, GATED>(product_direct_kernel<32, 64, 2, 2, 4, kForward, GATED, int8_t, true>, 256,
                                                  p, s);
@@ -1235,12 +1247,12 @@ template <int FORM, bool GATED, typename EL>
 rrb_status launch_product(const ProductArgs<EL> &p, hipStream_t s) {
   bool direct = p.lda % kPer<EL> == 0 && p.ldb % kPer<EL> == 0;
   for (int h = 0; h < 2; ++h) direct = direct && aligned(p.a[h], 16) && aligned(p.b[h], 16);
+  if constexpr (sizeof(EL) == 1) return launch_integers<GATED>(p, direct, s);
   if (!direct) {
     if (estimate<FORM, GATED>(p, 128, 128, 2, 1.7, 2) <= estimate<FORM, GATED>(p, 64, 64, 4, 1.1, 1))
       return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED, EL>, 256, p, s);
     return launch_tiles<64, 64, FORM, GATED>(product_kernel<64, 64, 2, 2, FORM, GATED, EL>, 256, p, s);
   }
-  if constexpr (sizeof(EL) == 1) return launch_integers<GATED>(p, s);
   // A tile of at most 128 valid rows takes about half a 256-row step.
   const bool half = FORM != kGradW && static_cast<int64_t>(p.groups) * 128 >= p.rows;
   const double big = estimate<FORM, GATED>(p, 256, 256, 1, half ? 0.9 : 1.55, 8);
