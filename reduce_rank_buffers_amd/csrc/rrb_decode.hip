@@ -48,7 +48,7 @@ struct DecodeArgs {
 
 template <int TOKENS, int EXPERTS>
 struct Choices {
-  static constexpr int BITS = TOKENS <= 8 ? 8 : 64;
+  static constexpr int BITS = TOKENS <= 8 ? 8 : TOKENS <= 16 ? 16 : 64;
   static constexpr int ROWS = TOKENS * kRouteMaxTopk;
   uint32_t mask[EXPERTS * BITS / 32];
   uint32_t list[ROWS < EXPERTS ? ROWS : EXPERTS];  // expert | its first row << 16
@@ -56,11 +56,14 @@ struct Choices {
   __device__ __forceinline__ void add(int e, int t) {
     if (BITS == 8)
       atomicOr(&mask[e >> 2], 1u << (8 * (e & 3) + t));
+    else if (BITS == 16)
+      atomicOr(&mask[e >> 1], 1u << (16 * (e & 1) + t));
     else
       atomicOr(&mask[2 * e + (t >> 5)], 1u << (t & 31));
   }
   __device__ __forceinline__ uint64_t tokens(int e) const {
     if (BITS == 8) return mask[e >> 2] >> (8 * (e & 3)) & 0xff;
+    if (BITS == 16) return mask[e >> 1] >> (16 * (e & 1)) & 0xffff;
     return mask[2 * e] | static_cast<uint64_t>(mask[2 * e + 1]) << 32;
   }
 };
@@ -74,8 +77,8 @@ struct Weights {
 };
 
 struct Live {
-  int experts;  // in the list
-  int most;     // tokens of one expert, rounded up to a power of two
+  int experts;   // in the list
+  int turns[4];  // sum over them of tokens / 4, / 8, / 16 and / 32, rounded up
 };
 
 __device__ __forceinline__ uint64_t below(int lane) { return (uint64_t(1) << lane) - 1; }
@@ -106,8 +109,8 @@ __device__ __forceinline__ Live find_experts(const DecodeArgs &a, Choices<TOKENS
   }
   __syncthreads();
   // Every wave makes the whole list, so that none waits for another's part.
-  Live live = {0, 1};
-  int rows = 0;
+  Live live = {0, {0, 0, 0, 0}};
+  int rows = 0, fours = 0, sixteens = 0;  // turns of four and (upper half) eight, ..
   for (int first = 0; first < a.experts; first += 64) {
     const int x = first + lane;
     const int many = x < a.experts ? __popcll(c.tokens(x)) : 0;
@@ -126,10 +129,18 @@ __device__ __forceinline__ Live find_experts(const DecodeArgs &a, Choices<TOKENS
     }
     live.experts += __popcll(set);
     rows += __shfl(upto, 63, 64);
-#pragma unroll
-    for (int m = 64; m >= 2; m >>= 1)
-      if (live.most < m && __ballot(many > m / 2)) live.most = m;
+    fours += (many + 3) / 4 | (many + 7) / 8 << 16;
+    sixteens += (many + 15) / 16 | (many + 31) / 32 << 16;
   }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    fours += __shfl_xor(fours, d, 64);
+    sixteens += __shfl_xor(sixteens, d, 64);
+  }
+  live.turns[0] = uniform(fours) & 0xffff;
+  live.turns[1] = uniform(fours) >> 16;
+  live.turns[2] = uniform(sixteens) & 0xffff;
+  live.turns[3] = uniform(sixteens) >> 16;
   if (weights) {
     // A token's first choice of an expert brings those of the same one with it.
 #pragma unroll
@@ -147,7 +158,6 @@ __device__ __forceinline__ Live find_experts(const DecodeArgs &a, Choices<TOKENS
     __syncthreads();
   }
   live.experts = uniform(live.experts);
-  live.most = uniform(live.most);
   return live;
 }
 
@@ -571,15 +581,28 @@ struct Stream {
   // LDS address `to`; where it is not live nothing is read.
   static __device__ __forceinline__ void start(const Source<M, NX> &from, int s, bool live, int end, int to) {
     const int lane = threadIdx.x & 63;
-    const int along = live ? s * kStageBytes : 0;
-    const bool part = live && (s + 1) * kStageBytes > end;
+    const int along = s * kStageBytes;
+    if (live && along + kStageBytes <= end) {
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_to_lds<true>(from.wd[m], to + (m * 2 + h) * 1024, from.wv[h], along);
+#pragma unroll
+      for (int g = 0; g < NX; ++g)
+#pragma unroll
+        for (int b = 0; b < XB; ++b)
+          load_to_lds(from.xd, to + (2 * M + g * XB + b) * 1024, from.xv[g], along * XB + b * kStageBytes);
+      return;
+    }
+    // The row's last bytes, or nothing: chunks past the end lie outside the buffers.
+    const int first = live ? along : end;
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int chunk = (lane & 7) ^ row_swizzle(h * 8 + (lane >> 3));
-        const bool out = !live || (part && along + chunk * 16 >= end);
-        load_to_lds<true>(from.wd[m], to + (m * 2 + h) * 1024, out ? kOutside : from.wv[h], along);
+        load_to_lds<true>(from.wd[m], to + (m * 2 + h) * 1024, first + chunk * 16 >= end ? kOutside : from.wv[h],
+                          live ? along : 0);
       }
 #pragma unroll
     for (int g = 0; g < NX; ++g)
@@ -587,8 +610,7 @@ struct Stream {
       for (int b = 0; b < XB; ++b) {
         // (Integers: a stage's 128 elements are 256 bytes of a column.)
         const int chunk = b * 8 + ((lane & 7) ^ row_swizzle(g * 8 + (lane >> 3)));
-        const bool out = !live || (part && along + chunk * (16 / XB) >= end);
-        load_to_lds(from.xd, to + (2 * M + g * XB + b) * 1024, out ? kOutside : from.xv[g],
+        load_to_lds(from.xd, to + (2 * M + g * XB + b) * 1024, first + chunk * (16 / XB) >= end ? kOutside : from.xv[g],
                     live ? along * XB + b * kStageBytes : 0);
       }
   }
@@ -677,8 +699,22 @@ struct Stream {
   }
 };
 
-// Calls `run` with NX = 1, 2, 4 or 8 groups of eight columns, whichever holds
-// `groups` first; MOST bounds what is compiled (more groups go by turns).
+// Groups of eight columns, 1 .. MOST, that make the least work: an expert with more
+// tokens than they hold goes by turns, each of which reads its weights again (W KiB a
+// stage), and every group is read and multiplied for every expert (X KiB, from the
+// L2, at about half the cost).  live.turns[FIRST] is that of one group.
+template <int W, int X, int MOST, int FIRST>
+__device__ __forceinline__ int best_groups(const Live &live) {
+  int best = 1, cost = live.turns[FIRST] * (2 * W + X);
+#pragma unroll
+  for (int i = 1; 1 << i <= MOST; ++i) {
+    const int c = live.turns[FIRST + i < 4 ? FIRST + i : 3] * (2 * W + (X << i));
+    if (c < cost) best = 1 << i, cost = c;
+  }
+  return best;
+}
+
+// Calls `run` with NX = 1, 2, 4 or 8; MOST bounds what is compiled.
 template <int MOST, typename F>
 __device__ __forceinline__ void with_groups(int groups, F run) {
   if (MOST == 1 || groups <= 1) {
@@ -775,11 +811,11 @@ __global__ void __launch_bounds__(kUpWaves * 64) decode_up_direct_kernel(DecodeA
   __shared__ __align__(16) unsigned char rings[kUpWaves][RING];
   // One group of columns stands twice in the sixteen, and is kept once.
   constexpr int LANES = MOST == 1 ? 32 : 64;
-  __shared__ f32x4_t parts[kUpWaves][2 * TILES][LANES];
+  __shared__ f32x4_t parts[kUpWaves - 1][2 * TILES][LANES];
   const Live live = find_experts<kUpWaves * 64, TOKENS, kDirectExperts>(a, choices, nullptr);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int at = MOST == 1 ? (lane >> 4) * 8 + (lane & 7) : lane;
-  with_groups<MOST>((live.most + 7) / 8, [&](auto groups) {
+  with_groups<MOST>(best_groups<4, INT ? 2 : 1, MOST, 1>(live), [&](auto groups) {
     constexpr int NX = decltype(groups)::value;
     typedef Stream<INT, 2, NX, RING> S;
     typedef UpSegment<C, NX> Segment;
@@ -787,25 +823,31 @@ __global__ void __launch_bounds__(kUpWaves * 64) decode_up_direct_kernel(DecodeA
     first.enter();
     int turn = 0;
     S::run(rings[wave], first, kUpWaves, a.hidden * (INT ? 1 : 2), [&](const Segment &s, f32x4_t (&acc)[2][S::NC]) {
-      // The waves' sums meet in LDS, and waves take turns at joining them, in order.
+      // The waves' sums meet in LDS, but for those of the wave whose turn it is to
+      // join them, in the waves' order.
+      const int joins = turn++ & (kUpWaves - 1);
+      if (wave != joins) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int c = 0; c < S::NC; ++c) parts[wave][m * S::NC + c][at] = acc[m][c];
+          for (int c = 0; c < S::NC; ++c) parts[wave - (wave > joins)][m * S::NC + c][at] = acc[m][c];
+      }
       barrier_without_loads();
       f32x4_t sum[2][S::NC];
-      const bool joins = (turn++ & (kUpWaves - 1)) == wave;
-      if (joins) {
+      if (wave == joins) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int c = 0; c < S::NC; ++c) {
-            sum[m][c] = parts[0][m * S::NC + c][at];
-            for (int i = 1; i < kUpWaves; ++i) sum[m][c] += parts[i][m * S::NC + c][at];
+            f32x4_t all = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kUpWaves; ++i)
+              all += i == wave ? acc[m][c] : parts[min(i - (i > wave), kUpWaves - 2)][m * S::NC + c][at];
+            sum[m][c] = all;
           }
       }
       barrier_without_loads();
-      if (!joins) return;
+      if (wave != joins) return;
       if (INT) {
         const int64_t row = static_cast<int64_t>(s.who.e) * a.inner + s.n0;
         const f32x4_t gate = four_scales(a.sgate, row), up = four_scales(a.sup, row);
@@ -876,7 +918,7 @@ __global__ void __launch_bounds__(WAVES * 64) decode_down_direct_kernel(DecodeAr
   f32x4_t *const sums = all + wave * a.tokens * 4;
   for (int t = lane; t < a.tokens * 4; t += 64) sums[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const Live live = find_experts<WAVES * 64, TOKENS, kDirectExperts>(a, choices, &weights);
-  with_groups<MOST>((live.most + 3) / 4, [&](auto groups) {
+  with_groups<MOST>(best_groups<2, INT ? 2 : 1, MOST, 0>(live), [&](auto groups) {
     constexpr int NX = decltype(groups)::value;
     typedef Stream<INT, 1, NX, RING> S;
     typedef DownSegment<C, NX> Segment;
@@ -951,18 +993,26 @@ rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
   int down_waves = kDownWaves;
   unsigned lds = 0;
   if (direct) {
-    // Two workgroups a CU.
-    if (up_grid.x > 512) up_grid.x = 512;
+    // The first kernel's workgroups stay, two a CU, or one with deeper rings and tables
+    // for up to 64 tokens (us, both kernels, 64 tokens on 8 experts, top-2, 4096 x 4096:
+    // 249 at two a CU, where an expert's tokens go sixteen at a time, and 220; 64
+    // tokens, an eighth of them here, on 32 experts, 7168 x 2048: 371 either way).
     const int t = a.tokens;
-    const bool dense = t > 8 && t * a.topk > 16 * a.experts, wide = down_grid.x > 256;
-    up = t <= 8  ? decode_up_direct_kernel<INT, 8, 1, 18432>
-         : dense ? decode_up_direct_kernel<INT, 64, 4, 24576>
-                 : decode_up_direct_kernel<INT, 64, 2, INT ? 16384 : 15360>;
+    int there = 512;
+    if (t <= 8) up = decode_up_direct_kernel<INT, 8, 1, 18432>;
+    else if (t <= 16) up = decode_up_direct_kernel<INT, 16, 2, 18432>;
+    else up = decode_up_direct_kernel<INT, 64, 4, 34816>, there = 256;
+    if (up_grid.x > static_cast<unsigned>(there)) up_grid.x = there;
+    // The second kernel's are as many as there are tiles of 16 channels: two of four
+    // waves a CU, or one of eight where they are at most the CUs.  Tokens that all
+    // meet on few experts want all columns at once, and the LDS for it.
+    const bool wide = down_grid.x > 256, dense = t > 16 && t * a.topk > 16 * a.experts;
+    constexpr int MOST = INT ? 2 : 4;
     if (t <= 8) down = wide ? decode_down_direct_kernel<INT, 8, 4, 2, 18432> : decode_down_direct_kernel<INT, 8, 8, 2, 18432>;
-    else if (dense) down = decode_down_direct_kernel<INT, 64, 4, INT ? 4 : 8, 30720>;
-    else down = wide ? decode_down_direct_kernel<INT, 64, 4, INT ? 2 : 4, 12288>
-                     : decode_down_direct_kernel<INT, 64, 8, INT ? 2 : 4, 12288>;
-    down_waves = dense || wide ? 4 : 8;
+    else if (t <= 16) down = wide ? decode_down_direct_kernel<INT, 16, 4, MOST, 17408> : decode_down_direct_kernel<INT, 16, 8, MOST, 17408>;
+    else if (dense) down = decode_down_direct_kernel<INT, 64, 4, 2 * MOST, 32768>;
+    else down = wide ? decode_down_direct_kernel<INT, 64, 4, MOST, 12288> : decode_down_direct_kernel<INT, 64, 8, MOST, 12288>;
+    down_waves = wide || dense ? 4 : 8;
   } else {
     up = up_kernel<INT>((a.tokens + 15) / 16);
     down = down_kernel<INT>((a.tokens + 7) / 8);
