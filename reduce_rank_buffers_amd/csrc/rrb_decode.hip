@@ -6,11 +6,12 @@
 // output channel; x, h and y are bf16, and sums fp32.
 //
 // With few tokens the time is the weights' bytes: every weight of an expert that
-// some token chose is read once, by one wave, for all of its tokens.  A wave
-// computes sixteen output channels (rows of a weight matrix, straight from memory
-// into the matrix instruction's registers) for up to sixteen tokens at a time;
-// which tokens chose which experts each workgroup finds for itself from the
-// choices.
+// some token chose is read once, for all of its tokens (so long as they are not
+// many).  A wave computes sixteen output channels, rows of a weight matrix, for up to
+// sixteen columns at a time, the tokens; which tokens chose which experts each
+// workgroup finds for itself from the choices.  h is kept in two bf16 parts: rounded
+// to one it would cost more than the result's own rounding (0.0024 of the result's
+// norm off instead of 0.0017), and the matrix instruction has columns to spare.
 #include <hip/hip_runtime.h>
 
 #include "rrb_activations.h"
@@ -27,7 +28,8 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kMaxTokens = 64;
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 constexpr int kUpWaves = 4, kDownWaves = 8;
-constexpr int kDirectExperts = 512;  // of layers whose weights go through LDS, which holds the tables too
+// Experts of layers whose weights go through LDS, which holds the tables too.
+constexpr int direct_experts(int tokens) { return tokens <= 8 ? kRouteMaxExperts : 512; }
 
 struct DecodeArgs {
   const uint16_t *x;
@@ -374,9 +376,10 @@ __device__ __forceinline__ void store_h(const DecodeArgs &a, int n, int row, f32
     if (n + q >= a.inner) continue;
     const float h = gated(a.act, gate[q], up[q]);
     const uint16_t first = f32_to_bf16_rne(h);
+    const float value = bf16_to_f32(first);
     to[q] = first;
-    // (An infinity has no remainder.)
-    to[a.pitch + q] = f32_to_bf16_rne(fabsf(h) < INFINITY ? h - bf16_to_f32(first) : 0.f);
+    // (An infinity, h's or by its rounding, has no remainder, nor has a NaN.)
+    to[a.pitch + q] = f32_to_bf16_rne(fabsf(value) < INFINITY ? h - value : 0.f);
   }
 }
 
@@ -388,58 +391,65 @@ __device__ __forceinline__ f32x4_t load_scales(const float *scales, int e, int n
   return v;
 }
 
-// Sixteen channels of one expert per workgroup: its waves take blocks of k by
-// turns, and wave 0 joins their sums in order.
+// Sixteen channels of one expert per workgroup at a time: its waves take blocks of
+// k by turns, and wave 0 joins their sums in order.  For rows off 16-byte boundaries,
+// whose weights go straight into the matrix instruction's registers: bound by the
+// loads in flight and their alignment (5 tokens, 1001 x 333: 9.4 us and the second
+// kernel 8.0, mostly latency; 64 tokens on 16 experts, 2001 x 1001: 70 and 72, 1.8 TB/s).
 template <bool INT, int MOST>
 __global__ void __launch_bounds__(kUpWaves * 64) decode_up_kernel(DecodeArgs a) {
   typedef typename Element<INT>::T T;
   __shared__ Choices<kMaxTokens, kRouteMaxExperts> choices;
   __shared__ f32x4_t part[kUpWaves - 1][2][MOST][64];
-  const int slot = blockIdx.x / a.tiles, n0 = (blockIdx.x - slot * a.tiles) * 16;
-  if (slot >= find_experts<kUpWaves * 64, kMaxTokens, kRouteMaxExperts>(a, choices, nullptr).experts) return;
+  const int items = a.tiles * find_experts<kUpWaves * 64, kMaxTokens, kRouteMaxExperts>(a, choices, nullptr).experts;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  Expert who;
-  who.find(choices, slot);
-  const int e = who.e, order = in_order(who.set);
-  const int64_t row = min(n0 + (lane & 15), a.inner - 1) + static_cast<int64_t>(e) * a.inner;
-  const T *const rows[2] = {static_cast<const T *>(a.gate) + row * a.hidden, static_cast<const T *>(a.up) + row * a.hidden};
-  with_tiles<MOST>((who.many + 15) / 16, [&](auto tiles) {
-    constexpr int NC = decltype(tiles)::value, U = kDepth<NC>, K = U * kFragment<INT>;
-    const uint16_t *xrows[NC];
-    int to[NC];
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int slot = item / a.tiles, n0 = (item - slot * a.tiles) * 16;
+    Expert who;
+    who.find(choices, slot);
+    const int e = who.e, order = in_order(who.set);
+    const int64_t row = min(n0 + (lane & 15), a.inner - 1) + static_cast<int64_t>(e) * a.inner;
+    const T *const rows[2] = {static_cast<const T *>(a.gate) + row * a.hidden,
+                              static_cast<const T *>(a.up) + row * a.hidden};
+    with_tiles<MOST>((who.many + 15) / 16, [&](auto tiles) {
+      constexpr int NC = decltype(tiles)::value, U = kDepth<NC>, K = U * kFragment<INT>;
+      const uint16_t *xrows[NC];
+      int to[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int i = c * 16 + (lane & 15);
-      xrows[c] = a.x + static_cast<int64_t>(__shfl(order, i < who.many ? i : 0, 64)) * a.hidden;
-      to[c] = i < who.many ? who.row + i : -1;
-    }
-    f32x4_t acc[2][NC];
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    sum_blocks<INT, 2, NC, U>(acc, rows, xrows, wave, kUpWaves, (a.hidden + K - 1) / K, a.hidden);
-    if (wave) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) part[wave - 1][m][c][lane] = acc[m][c];
-    }
-    __syncthreads();
-    if (wave) return;
-    const int n = n0 + (lane >> 4) * 4;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-        for (int i = 0; i < kUpWaves - 1; ++i) acc[m][c] += part[i][m][c][lane];
-      if (INT) {
-        acc[0][c] *= load_scales(a.sgate, e, a.inner, n);
-        acc[1][c] *= load_scales(a.sup, e, a.inner, n);
+      for (int c = 0; c < NC; ++c) {
+        const int i = c * 16 + (lane & 15);
+        xrows[c] = a.x + static_cast<int64_t>(__shfl(order, i < who.many ? i : 0, 64)) * a.hidden;
+        to[c] = i < who.many ? who.row + i : -1;
       }
-      if (to[c] >= 0) store_h(a, n, to[c], acc[0][c], acc[1][c]);
-    }
-  });
+      f32x4_t acc[2][NC];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      sum_blocks<INT, 2, NC, U>(acc, rows, xrows, wave, kUpWaves, (a.hidden + K - 1) / K, a.hidden);
+      if (wave) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) part[wave - 1][m][c][lane] = acc[m][c];
+      }
+      __syncthreads();
+      if (wave) return;
+      const int n = n0 + (lane >> 4) * 4;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          for (int i = 0; i < kUpWaves - 1; ++i) acc[m][c] += part[i][m][c][lane];
+        if (INT) {
+          acc[0][c] *= load_scales(a.sgate, e, a.inner, n);
+          acc[1][c] *= load_scales(a.sup, e, a.inner, n);
+        }
+        if (to[c] >= 0) store_h(a, n, to[c], acc[0][c], acc[1][c]);
+      }
+    });
+    __syncthreads();
+  }
 }
 
 // ---- y ------------------------------------------------------------------------------
@@ -542,7 +552,17 @@ __global__ void __launch_bounds__(WAVES * 64) decode_down_kernel(DecodeArgs a) {
 // own and waits for nobody but its loads: a stage is 128 bytes of each of 16 rows of
 // the M matrices and, as rows of the same kind, what they are multiplied by, of NX
 // groups of eight columns.  Row r keeps its 16-byte chunk c at c ^ (r / 2 % 8), so
-// that a fragment's reads meet all banks.
+// that a fragment's reads meet all banks.  Rings do not empty between experts or
+// tiles: the loads run ahead into the next segment.
+//
+// Bound by HBM where rows are long: a pure read of such rows reaches 6.0 TB/s
+// through the caches and 6.65 past them (whole lines; 5.6 in halves, as the matrix
+// instruction's own layout reads them).  Measured, us (first kernel and second):
+// one token, 8 of 32 experts, 7168 x 2048 bf16: 70 (6.7 TB/s) and 44 (5.3), where loads
+// into registers took 79 and 48; int8 39 and 24 (integers are converted at 1.5
+// operations each, and the columns' bytes are twice as many beside the weights'); 64
+// tokens on 28 of 32 experts, bf16: 277 (5.9) and 151 (5.4); one token, 2048 x 1024
+// (100 MB): 14 and 11, of which launch, tables and the first loads are 4 to 5 each.
 
 constexpr int kStageBytes = 128;  // of a weight row
 __device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
@@ -806,13 +826,13 @@ struct UpSegment {
 template <bool INT, int TOKENS, int MOST, int RING>
 __global__ void __launch_bounds__(kUpWaves * 64) decode_up_direct_kernel(DecodeArgs a) {
   constexpr int TILES = (MOST + 1) / 2;
-  typedef Choices<TOKENS, kDirectExperts> C;
+  typedef Choices<TOKENS, direct_experts(TOKENS)> C;
   __shared__ C choices;
   __shared__ __align__(16) unsigned char rings[kUpWaves][RING];
   // One group of columns stands twice in the sixteen, and is kept once.
   constexpr int LANES = MOST == 1 ? 32 : 64;
   __shared__ f32x4_t parts[kUpWaves - 1][2 * TILES][LANES];
-  const Live live = find_experts<kUpWaves * 64, TOKENS, kDirectExperts>(a, choices, nullptr);
+  const Live live = find_experts<kUpWaves * 64, TOKENS, direct_experts(TOKENS)>(a, choices, nullptr);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int at = MOST == 1 ? (lane >> 4) * 8 + (lane & 7) : lane;
   with_groups<MOST>(best_groups<4, INT ? 2 : 1, MOST, 1>(live), [&](auto groups) {
@@ -908,16 +928,16 @@ struct DownSegment {
 // decode_down_kernel's work.  MOST: groups of eight columns at a time.
 template <bool INT, int TOKENS, int WAVES, int MOST, int RING>
 __global__ void __launch_bounds__(WAVES * 64) decode_down_direct_kernel(DecodeArgs a) {
-  typedef Choices<TOKENS, kDirectExperts> C;
+  typedef Choices<TOKENS, direct_experts(TOKENS)> C;
   __shared__ C choices;
-  __shared__ Weights<TOKENS, kDirectExperts> weights;
+  __shared__ Weights<TOKENS, direct_experts(TOKENS)> weights;
   __shared__ __align__(16) unsigned char rings[WAVES][RING];
   __shared__ f32x4_t all[WAVES * TOKENS * 4];  // [wave][token][channel / 4]
   const int n0 = blockIdx.x * 16;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   f32x4_t *const sums = all + wave * a.tokens * 4;
   for (int t = lane; t < a.tokens * 4; t += 64) sums[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const Live live = find_experts<WAVES * 64, TOKENS, kDirectExperts>(a, choices, &weights);
+  const Live live = find_experts<WAVES * 64, TOKENS, direct_experts(TOKENS)>(a, choices, &weights);
   with_groups<MOST>(best_groups<2, INT ? 2 : 1, MOST, 0>(live), [&](auto groups) {
     constexpr int NX = decltype(groups)::value;
     typedef Stream<INT, 1, NX, RING> S;
@@ -987,7 +1007,7 @@ rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
   const uintptr_t weights = reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.up) |
                             reinterpret_cast<uintptr_t>(a.down) | reinterpret_cast<uintptr_t>(a.x);
   // Where offsets into h fit the buffers' 31 bits (all but widths near 2^20).
-  const bool direct = a.experts <= kDirectExperts && a.hidden % per == 0 && a.inner % per == 0 && weights % 16 == 0 &&
+  const bool direct = a.experts <= direct_experts(a.tokens) && a.hidden % per == 0 && a.inner % per == 0 && weights % 16 == 0 &&
                       static_cast<int64_t>(a.tokens) * a.topk * 4 * a.pitch < (1LL << 31);
   void (*up)(DecodeArgs), (*down)(DecodeArgs);
   int down_waves = kDownWaves;
@@ -1014,6 +1034,7 @@ rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
     else down = wide ? decode_down_direct_kernel<INT, 64, 4, MOST, 12288> : decode_down_direct_kernel<INT, 64, 8, MOST, 12288>;
     down_waves = wide || dense ? 4 : 8;
   } else {
+    if (up_grid.x > 1 << 20) up_grid.x = 1 << 20;
     up = up_kernel<INT>((a.tokens + 15) / 16);
     down = down_kernel<INT>((a.tokens + 7) / 8);
     lds = kDownWaves * a.tokens * 64;

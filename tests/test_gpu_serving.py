@@ -405,7 +405,7 @@ class Layer:
 
 
 LAYERS = [
-    (64, 4, 8, 256, 144, 0), (20, 6, 6, 4160, 64, 0), (12, 2, 600, 64, 32, 0), (33, 2, 400, 96, 32, 10), (64, 16, 513, 64, 16, 0),
+    (64, 4, 8, 256, 144, 0), (20, 6, 6, 4160, 64, 0), (12, 2, 600, 64, 32, 0), (8, 3, 1024, 64, 32, 1), (3, 16, 1023, 96, 48, 0), (33, 2, 400, 96, 32, 10), (64, 16, 513, 64, 16, 0),
     # T, k, E, h, f, experts beyond either end
     (1, 1, 1, 8, 8, 0), (1, 1, 1, 1, 1, 0), (1, 8, 64, 512, 256, 0), (2, 2, 3, 7, 5, 0), (3, 1, 4, 64, 48, 1),
     (5, 3, 12, 1001, 333, 6), (16, 4, 8, 256, 128, 0), (17, 2, 3, 136, 72, 0), (16, 16, 40, 72, 200, 0),
@@ -474,6 +474,23 @@ def test_decode_values_do_not_leak(int8):
         hit_t = torch.from_numpy(hit).to(DEV)
         assert torch.equal(p.y[~hit_t], clean[~hit_t])
         assert not p.y[3].isfinite().any() and not p.y[torch.from_numpy((idx == 4).any(axis=1)).to(DEV)].isfinite().any()
+
+
+@pytest.mark.parametrize("width", [8, 7])
+def test_decode_hidden_values_that_round_to_infinity(width):
+    """h half a step above bf16's largest: finite in fp32, an infinity once
+    rounded, and no NaN."""
+    require_gpu()
+    bf = lambda *s: torch.zeros(s, dtype=BF)
+    x, wg, wu, wd = bf(1, width), bf(1, width, width), bf(1, width, width), bf(1, width, width)
+    x[0, :2] = 1
+    wg[0, 0, 0], wg[0, 0, 1], wu[0, 0, 0] = 1.9921875 * 2.0 ** 63, 2.0 ** 55, 2.0 ** 64
+    wd[0, :, 0] = 1
+    assert (wg[0, 0, 0].double() + wg[0, 0, 1].double()) * 2.0 ** 64 < torch.finfo(torch.float32).max
+    y = torch.empty(1, width, dtype=BF, device=DEV)
+    rrb.moe_decode(x.to(DEV), torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.ones(1, 1, device=DEV), wg.to(DEV),
+                   wu.to(DEV), wd.to(DEV), y, activation="none")
+    assert torch.isposinf(y).all()
 
 
 def test_decode_zero_weight_of_a_finite_expert():
