@@ -418,9 +418,9 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
  *
  * rrb_quantize_rows makes them from rows of bf16 or fp32: scale = fl32(max |x| /
  * 127), q = x / scale to the nearest integer, ties to even, exactly (kept within
- * +-127 where a subnormal scale would pass it).  A row of zeros has the scale 0; a row with an infinity or a NaN
- * has a NaN for its scale and zeros for its integers, so that what is computed
- * from it is NaN.  d_offsets (nullable): int32, groups + 1 entries, of which the
+ * +-127 where a subnormal scale would pass it).  A row of zeros has the scale 0;
+ * a row with an infinity or a NaN has a NaN for its scale and zeros for its
+ * integers, so that what is computed from it is NaN.  d_offsets (nullable): int32, groups + 1 entries, of which the
  * first and the last bound the rows that are read and written, clamped to
  * 0..rows.  Weights [groups][out][in] are groups * out rows.  Limits
  * (RRB_EUNSUPPORTED): rows < 2^31, width <= 2^20.
@@ -436,7 +436,8 @@ rrb_status rrb_quantize_rows(int64_t rows, int64_t width, int32_t dtype, const v
  * exactly; p = fl(fl(fl32(sum) * x_scale) * w_scale), and
  *   linear  out = act(p + bias) + residual
  *   gated   out = act(p_gate) * p_up
- * with bias, residual and out in bf16, each result rounded once.  The calls have no gradient.
+ * with bias, residual and out in bf16, each result rounded once.  The calls have
+ * no gradient.
  */
 rrb_status rrb_expert_linear_int8(const rrb_expert_spec *spec, const int8_t *d_x, const float *d_x_scale,
                                   const int32_t *d_offsets, const int8_t *d_w, const float *d_w_scale,

@@ -463,7 +463,8 @@ __device__ __forceinline__ void add_expert(f32x4_t acc, bool scaled, f32x4_t sca
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     // row_ror by 16 - HALF: lane i of a row receives lane (i + HALF) % 16.
-    z[q] = acc[q] + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[q]), 0x120 + 16 - HALF, 0xf, 0xf, false));
+    const int other = __builtin_amdgcn_mov_dpp(__float_as_int(acc[q]), 0x120 + 16 - HALF, 0xf, 0xf, false);
+    z[q] = acc[q] + __int_as_float(other);
     if (scaled) z[q] *= scale[q];
   }
   if (token < 0) return;
@@ -1007,7 +1008,8 @@ rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
   const uintptr_t weights = reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.up) |
                             reinterpret_cast<uintptr_t>(a.down) | reinterpret_cast<uintptr_t>(a.x);
   // Where offsets into h fit the buffers' 31 bits (all but widths near 2^20).
-  const bool direct = a.experts <= direct_experts(a.tokens) && a.hidden % per == 0 && a.inner % per == 0 && weights % 16 == 0 &&
+  const bool direct = a.experts <= direct_experts(a.tokens) && a.hidden % per == 0 && a.inner % per == 0 &&
+                      weights % 16 == 0 &&
                       static_cast<int64_t>(a.tokens) * a.topk * 4 * a.pitch < (1LL << 31);
   void (*up)(DecodeArgs), (*down)(DecodeArgs);
   int down_waves = kDownWaves;
@@ -1019,19 +1021,28 @@ rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
     // tokens, an eighth of them here, on 32 experts, 7168 x 2048: 371 either way).
     const int t = a.tokens;
     int there = 512;
-    if (t <= 8) up = decode_up_direct_kernel<INT, 8, 1, 18432>;
-    else if (t <= 16) up = decode_up_direct_kernel<INT, 16, 2, 18432>;
-    else up = decode_up_direct_kernel<INT, 64, 4, 34816>, there = 256;
+    if (t <= 8)
+      up = decode_up_direct_kernel<INT, 8, 1, 18432>;
+    else if (t <= 16)
+      up = decode_up_direct_kernel<INT, 16, 2, 18432>;
+    else
+      up = decode_up_direct_kernel<INT, 64, 4, 34816>, there = 256;
     if (up_grid.x > static_cast<unsigned>(there)) up_grid.x = there;
     // The second kernel's are as many as there are tiles of 16 channels: two of four
     // waves a CU, or one of eight where they are at most the CUs.  Tokens that all
     // meet on few experts want all columns at once, and the LDS for it.
     const bool wide = down_grid.x > 256, dense = t > 16 && t * a.topk > 16 * a.experts;
     constexpr int MOST = INT ? 2 : 4;
-    if (t <= 8) down = wide ? decode_down_direct_kernel<INT, 8, 4, 2, 18432> : decode_down_direct_kernel<INT, 8, 8, 2, 18432>;
-    else if (t <= 16) down = wide ? decode_down_direct_kernel<INT, 16, 4, MOST, 17408> : decode_down_direct_kernel<INT, 16, 8, MOST, 17408>;
-    else if (dense) down = decode_down_direct_kernel<INT, 64, 4, 2 * MOST, 32768>;
-    else down = wide ? decode_down_direct_kernel<INT, 64, 4, MOST, 12288> : decode_down_direct_kernel<INT, 64, 8, MOST, 12288>;
+    if (t <= 8)
+      down = wide ? decode_down_direct_kernel<INT, 8, 4, 2, 18432> : decode_down_direct_kernel<INT, 8, 8, 2, 18432>;
+    else if (t <= 16)
+      down = wide ? decode_down_direct_kernel<INT, 16, 4, MOST, 17408>
+                  : decode_down_direct_kernel<INT, 16, 8, MOST, 17408>;
+    else if (dense)
+      down = decode_down_direct_kernel<INT, 64, 4, 2 * MOST, 32768>;
+    else
+      down = wide ? decode_down_direct_kernel<INT, 64, 4, MOST, 12288>
+                  : decode_down_direct_kernel<INT, 64, 8, MOST, 12288>;
     down_waves = wide || dense ? 4 : 8;
   } else {
     if (up_grid.x > 1 << 20) up_grid.x = 1 << 20;

@@ -263,7 +263,9 @@ __device__ __forceinline__ void store_tile(const ProductArgs<EL> &p, const typen
   constexpr int BLOCKS = (GATED ? 2 : 1) * (WIDE ? 2 : 1);  // blocks that make them
   static_assert(FN % BLOCKS == 0, "a wave has whole outputs");
   const int lane = threadIdx.x & 63;
-  auto row_at = [&](int i) { return spot.m + (FM > 1 && i >= FM / 2 ? spot.down + (i - FM / 2) * 16 : i * 16) + (lane & 15); };
+  auto row_at = [&](int i) {
+    return spot.m + (FM > 1 && i >= FM / 2 ? spot.down + (i - FM / 2) * 16 : i * 16) + (lane & 15);
+  };
   auto col_at = [&](int j) {
     const int g = j / BLOCKS, halves = FN / BLOCKS / 2;
     return spot.n + (halves && g >= halves ? spot.right + (g - halves) * W * 4 : g * W * 4) + (lane >> 4) * W;
@@ -1217,21 +1219,23 @@ rrb_status launch_integers(const ProductArgs<int8_t> &p, bool direct, hipStream_
   if (!direct) {
     const int64_t tiles = (rows / 128 + std::min(groups, rows) / 2) * ((p.n + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
     if (rows > 64 * groups && tiles >= 128)
-      return launch_tiles<128, 128, kForward, GATED>(product_kernel<128, 128, 2, 4, kForward, GATED, int8_t>, 512, p, s);
+      return launch_tiles<128, 128, kForward, GATED>(product_kernel<128, 128, 2, 4, kForward, GATED, int8_t>, 512, p,
+                                                     s);
     return launch_tiles<64, 64, kForward, GATED>(product_kernel<64, 64, 2, 2, kForward, GATED, int8_t>, 256, p, s);
   }
-  if (rows <= 32 * groups)
-    return launch_tiles<32, 64, kForward, GATED>(product_direct_kernel<32, 64, 2, 2, 4, kForward, GATED, int8_t, true>, 256,
-                                                 p, s);
-  const double big = estimate_integers<GATED>(p, 256, 256, 1, 1.4, 12), wide = estimate_integers<GATED>(p, 128, 256, 1, 0.95, 8.6);
-  const double mid = estimate_integers<GATED>(p, 64, 128, 2, 0.58, 9), low = estimate_integers<GATED>(p, 64, 64, 2, 0.35, 6.3);
+#define RRB_DIRECT(BM, BN, WR, WC, STAGES, ONCE)                                                                   \
+  launch_tiles<BM, BN, kForward, GATED>(                                                                           \
+      product_direct_kernel<BM, BN, WR, WC, STAGES, kForward, GATED, int8_t, ONCE>, WR * WC * 64, p, s)
+  if (rows <= 32 * groups) return RRB_DIRECT(32, 64, 2, 2, 4, true);
+  const double big = estimate_integers<GATED>(p, 256, 256, 1, 1.4, 12);
+  const double wide = estimate_integers<GATED>(p, 128, 256, 1, 0.95, 8.6);
+  const double mid = estimate_integers<GATED>(p, 64, 128, 2, 0.58, 9);
+  const double low = estimate_integers<GATED>(p, 64, 64, 2, 0.35, 6.3);
   const double best = std::min(std::min(big, wide), std::min(mid, low));
-  if (low == best || rows <= 64 * groups)
-    return launch_tiles<64, 64, kForward, GATED>(product_direct_kernel<64, 64, 2, 2, 5, kForward, GATED, int8_t>, 256, p, s);
-  if (mid == best)
-    return launch_tiles<64, 128, kForward, GATED>(product_direct_kernel<64, 128, 2, 2, 3, kForward, GATED, int8_t>, 256, p, s);
-  if (wide == best)
-    return launch_tiles<128, 256, kForward, GATED>(product_direct_kernel<128, 256, 2, 4, 3, kForward, GATED, int8_t>, 512, p, s);
+  if (low == best || rows <= 64 * groups) return RRB_DIRECT(64, 64, 2, 2, 5, false);
+  if (mid == best) return RRB_DIRECT(64, 128, 2, 2, 3, false);
+  if (wide == best) return RRB_DIRECT(128, 256, 2, 4, 3, false);
+#undef RRB_DIRECT
   return launch_tiles<256, 256, kForward, GATED>(product_turns_kernel<kForward, GATED, int8_t>, 512, p, s);
 }
 

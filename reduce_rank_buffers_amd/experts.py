@@ -5,11 +5,11 @@ routing arrays from scores, the ``expert_*`` calls run on the dispatched rows,
 grouped by expert (``MoeDevicePlan.expert_offsets``), and each has its
 gradient.  For serving, ``quantize_rows`` and the ``expert_*_int8`` calls run
 the products in 8-bit integers, and ``moe_decode`` the whole expert layer of a
-few tokens without dispatch and combine; these have none.  Outputs are the caller's tensors, written in place; argument rules
-are api.py's (contiguous, on the current GPU, bf16 as torch.bfloat16 or its
-int16 / uint16 bit patterns), and shapes are checked too; the library refuses
-outputs that overlap what a call reads.  None of the calls takes part in
-autograd.
+few tokens without dispatch and combine; these have none.  Outputs are the
+caller's tensors, written in place; argument rules are api.py's (contiguous, on
+the current GPU, bf16 as torch.bfloat16 or its int16 / uint16 bit patterns),
+and shapes are checked too; the library refuses outputs that overlap what a
+call reads.  None of the calls takes part in autograd.
 """
 
 import ctypes
@@ -288,7 +288,8 @@ def quantize_rows(x, q, scale, offsets=None, stream=None):
     groups = 0
     if offsets is not None:
         if x.dim() != 2 or not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
-            raise ValueError("offsets: expected a tensor of one dimension and at least two entries, x of two dimensions")
+            raise ValueError("offsets: expected a tensor of one dimension and at least two entries, "
+                             "x of two dimensions")
         groups = offsets.numel() - 1
     _required(q=q, scale=scale)
     (xp, qp, sp, op), dev = _checked((("x", x, x.shape, (x.dtype,)), ("q", q, x.shape, _INT8),

@@ -405,7 +405,8 @@ class Layer:
 
 
 LAYERS = [
-    (64, 4, 8, 256, 144, 0), (20, 6, 6, 4160, 64, 0), (12, 2, 600, 64, 32, 0), (8, 3, 1024, 64, 32, 1), (3, 16, 1023, 96, 48, 0), (33, 2, 400, 96, 32, 10), (64, 16, 513, 64, 16, 0),
+    (64, 4, 8, 256, 144, 0), (20, 6, 6, 4160, 64, 0), (12, 2, 600, 64, 32, 0), (8, 3, 1024, 64, 32, 1),
+    (3, 16, 1023, 96, 48, 0), (33, 2, 400, 96, 32, 10), (64, 16, 513, 64, 16, 0),
     # T, k, E, h, f, experts beyond either end
     (1, 1, 1, 8, 8, 0), (1, 1, 1, 1, 1, 0), (1, 8, 64, 512, 256, 0), (2, 2, 3, 7, 5, 0), (3, 1, 4, 64, 48, 1),
     (5, 3, 12, 1001, 333, 6), (16, 4, 8, 256, 128, 0), (17, 2, 3, 136, 72, 0), (16, 16, 40, 72, 200, 0),
