@@ -1179,6 +1179,14 @@ double estimate(const ProductArgs<EL> &p, int bm, int bn, int resident, double s
   return std::max(matrix, std::max(moved * kStep * 2 / 10e6, weights / 5.5e6 * whole));
 }
 
+// Whether one launch (2^32 threads, at most 512 a tile, and the run of tiles that a
+// grid is rounded up to) holds the integer product's tiles of that shape.
+template <bool GATED>
+bool fits(const ProductArgs<int8_t> &p, int bm, int bn) {
+  const int cols = GATED ? bn / 2 : bn;
+  return most_row_tiles(p, bm) * ((p.n + cols - 1) / cols) <= (1 << 23) - 512;
+}
+
 // Estimated time (us) of an integer product over BM x BN tiles: rounds of tiles as
 // above, or the weights from HBM.  In whole tiles where one group has all rows; where
 // there are more how many tiles are partial is not known, and rounds come out a
@@ -1187,6 +1195,7 @@ template <bool GATED>
 double estimate_integers(const ProductArgs<int8_t> &p, int bm, int bn, int resident, double step, double rest) {
   const double live = p.groups < p.rows ? p.groups : p.rows;
   const int cols = GATED ? bn / 2 : bn;
+  if (!fits<GATED>(p, bm, bn)) return INFINITY;
   const double across = (p.n + cols - 1) / cols, steps = (p.k + kSteps<int8_t> - 1) / kSteps<int8_t>;
   double down = static_cast<double>(p.rows) / bm + live / 2;
   if (down < live) down = live;
@@ -1218,7 +1227,7 @@ rrb_status launch_integers(const ProductArgs<int8_t> &p, bool direct, hipStream_
   const int64_t rows = p.rows, groups = p.groups;
   if (!direct) {
     const int64_t tiles = (rows / 128 + std::min(groups, rows) / 2) * ((p.n + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
-    if (rows > 64 * groups && tiles >= 128)
+    if ((rows > 64 * groups && tiles >= 128) || !fits<GATED>(p, 64, 64))
       return launch_tiles<128, 128, kForward, GATED>(product_kernel<128, 128, 2, 4, kForward, GATED, int8_t>, 512, p,
                                                      s);
     return launch_tiles<64, 64, kForward, GATED>(product_kernel<64, 64, 2, 2, kForward, GATED, int8_t>, 256, p, s);
@@ -1226,15 +1235,15 @@ rrb_status launch_integers(const ProductArgs<int8_t> &p, bool direct, hipStream_
 #define RRB_DIRECT(BM, BN, WR, WC, STAGES, ONCE)                                                                   \
   launch_tiles<BM, BN, kForward, GATED>(                                                                           \
       product_direct_kernel<BM, BN, WR, WC, STAGES, kForward, GATED, int8_t, ONCE>, WR * WC * 64, p, s)
-  if (rows <= 32 * groups) return RRB_DIRECT(32, 64, 2, 2, 4, true);
+  if (rows <= 32 * groups && fits<GATED>(p, 32, 64)) return RRB_DIRECT(32, 64, 2, 2, 4, true);
   const double big = estimate_integers<GATED>(p, 256, 256, 1, 1.4, 12);
   const double wide = estimate_integers<GATED>(p, 128, 256, 1, 0.95, 8.6);
   const double mid = estimate_integers<GATED>(p, 64, 128, 2, 0.58, 9);
   const double low = estimate_integers<GATED>(p, 64, 64, 2, 0.35, 6.3);
   const double best = std::min(std::min(big, wide), std::min(mid, low));
-  if (low == best || rows <= 64 * groups) return RRB_DIRECT(64, 64, 2, 2, 5, false);
-  if (mid == best) return RRB_DIRECT(64, 128, 2, 2, 3, false);
-  if (wide == best) return RRB_DIRECT(128, 256, 2, 4, 3, false);
+  if (std::isfinite(low) && (low == best || rows <= 64 * groups)) return RRB_DIRECT(64, 64, 2, 2, 5, false);
+  if (std::isfinite(mid) && mid == best) return RRB_DIRECT(64, 128, 2, 2, 3, false);
+  if (std::isfinite(wide) && wide == best) return RRB_DIRECT(128, 256, 2, 4, 3, false);
 #undef RRB_DIRECT
   return launch_tiles<256, 256, kForward, GATED>(product_turns_kernel<kForward, GATED, int8_t>, 512, p, s);
 }

@@ -254,7 +254,7 @@ def _checked(named):
     and the GPU they are on; as _shaped and _addresses check them, in one pass
     over tensors that are as they should be (a decode step's calls are bound by
     the host)."""
-    out, dev = [], -1
+    out, dev, mixed = [], None, False
     for what, t, shape, types in named:
         if t is None:
             out.append(None)
@@ -263,12 +263,10 @@ def _checked(named):
             _shaped(t, what, shape, types)
         at = t.get_device()
         if at != dev:
-            if dev != -1 or at < 0:
-                dev = -2
-            elif dev == -1:
-                dev = at
+            mixed = mixed or dev is not None
+            dev = at
         out.append(t.data_ptr())
-    if dev < 0 or dev != torch.cuda.current_device():
+    if mixed or dev < 0 or dev != torch.cuda.current_device():
         for what, t, _, _ in named:
             if t is not None:
                 _on_gpu(t, what)

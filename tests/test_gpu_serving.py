@@ -591,6 +591,60 @@ def test_decode_repeats_streams_and_graphs(int8):
             _check("y", got, *p.expect(name))
 
 
+def test_decode_scales_off_16_bytes():
+    """Weights on 16-byte boundaries, scales and results 4 and 2 bytes off."""
+    require_gpu()
+    p = Layer(35, 5, 3, 6, 256, 96, int8=True)
+    put = Put(1)
+    p.scales = [put(s.cpu()) for s in p.scales]
+    p.d_w, p.d_idx, p.y = put(p.d_w.cpu()), put(p.d_idx.cpu()), put(p.y.cpu())
+    p.check("silu")
+
+
+def test_calls_refuse_tensors_off_the_gpu():
+    """One tensor on the host among those on the GPU, whichever it is."""
+    require_gpu()
+    p = Layer(36, 3, 2, 4, 32, 16, int8=True)
+    args = [p.d_x, p.d_idx, p.d_w, *p.mats, p.y]
+    for i in range(len(args)):
+        a = list(args)
+        a[i] = a[i].cpu()
+        with pytest.raises(ValueError, match="not on the current GPU"):
+            rrb.moe_decode(*a, scales=tuple(p.scales), workspace=p.work)
+    with pytest.raises(ValueError, match="not on the current GPU"):
+        rrb.moe_decode(*args, scales=(p.scales[0], p.scales[1].cpu(), p.scales[2]), workspace=p.work)
+    with pytest.raises(ValueError, match="not on the current GPU"):
+        rrb.moe_decode(*args, scales=tuple(p.scales), workspace=p.work.cpu())
+    q = Integers(37, [5, 3], 32, 16)
+    (w, s), put = q.weight(), q.put
+    args = [put(q.x), put(q.sx), q.d_off, put(w), put(s), q.out()]
+    for i in range(len(args)):
+        a = list(args)
+        a[i] = a[i].cpu()
+        with pytest.raises(ValueError, match="not on the current GPU"):
+            rrb.expert_linear_int8(*a)
+        with pytest.raises(ValueError, match="not on the current GPU"):
+            rrb.expert_gated_int8(a[0], a[1], a[2], a[3], a[4], args[3], args[4], a[5])
+    x = torch.zeros(4, 8, dtype=BF, device=DEV)
+    for a in ((x.cpu(), torch.zeros(4, 8, dtype=torch.int8, device=DEV), torch.zeros(4, device=DEV)),
+              (x, torch.zeros(4, 8, dtype=torch.int8), torch.zeros(4, device=DEV)),
+              (x, torch.zeros(4, 8, dtype=torch.int8, device=DEV), torch.zeros(4))):
+        with pytest.raises(ValueError, match="not on the current GPU"):
+            rrb.quantize_rows(*a)
+
+
+def test_decode_refuses_workspaces():
+    require_gpu()
+    p = Layer(38, 3, 2, 4, 32, 16)
+    for bad in (p.work[:-1], torch.empty(p.work.numel() + 16, dtype=torch.uint8, device=DEV)[8:]):
+        with pytest.raises(rrb.RrbError):
+            p.run("silu", workspace=bad)
+    with pytest.raises(ValueError):
+        p.run("silu", workspace=p.work.view(torch.int8))
+    with pytest.raises(ValueError):
+        p.run("silu", workspace=torch.empty(2 * p.work.numel(), dtype=torch.uint8, device=DEV)[::2])
+
+
 def test_decode_without_tokens():
     require_gpu()
     bf = lambda *s: torch.zeros(s, dtype=BF, device=DEV)
