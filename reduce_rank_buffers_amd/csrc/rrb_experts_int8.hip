@@ -95,13 +95,15 @@ struct Eight<float> {
 };
 
 // L lanes (a wave's 64, or a workgroup's 256 or 1024) share a row, eight elements
-// each by turns.  HELD: widths of whole eights, in at most so many turns, which
-// stay in registers; 0: any width, the row read twice.
-template <typename T, int L, int HELD>
+// each by turns, the row's last eight where fewer are left (what two lanes have, both
+// write alike).  HELD: at most so many turns, which stay in registers; 0: any width,
+// the row read twice.  WHOLE: rows of at least eight.
+template <typename T, int L, int HELD, bool WHOLE>
 __global__ void __launch_bounds__(L == 64 ? 256 : L) quantize_kernel(QuantizeArgs a) {
   constexpr int ROWS = L == 64 ? 4 : 1;  // per workgroup at a time
   __shared__ uint32_t part[L / 64];
   const int lane = threadIdx.x & (L - 1);
+  auto at = [&](int c) { return WHOLE ? min(c, a.width - 8) : c; };
   int64_t first = 0, last = a.rows;
   if (a.offsets) {
     first = a.offsets[0], last = a.offsets[a.groups];
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(L == 64 ? 256 : L) quantize_kernel(QuantizeArg
     uint32_t most = 0;
     if (HELD) {
 #pragma unroll
-      for (int h = 0; h < HELD; ++h) v[h].stream(x + (h * L + lane) * 8, (h * L + lane) * 8 < a.width);
+      for (int h = 0; h < HELD; ++h) v[h].stream(x + at((h * L + lane) * 8), (h * L + lane) * 8 < a.width);
 #pragma unroll
       for (int h = 0; h < HELD; ++h) {
         most = v[h].most(most);
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(L == 64 ? 256 : L) quantize_kernel(QuantizeArg
       }
     } else {
       for (int c = lane * 8; c < a.width; c += L * 8) {
-        v[0].load(x + c, a.width - c);
+        v[0].load(x + at(c), WHOLE ? 8 : a.width - c);
         most = v[0].most(most);
       }
     }
@@ -180,11 +182,11 @@ __global__ void __launch_bounds__(L == 64 ? 256 : L) quantize_kernel(QuantizeArg
     if (HELD) {
 #pragma unroll
       for (int h = 0; h < HELD; ++h)
-        if ((h * L + lane) * 8 < a.width) put((h * L + lane) * 8, v[h], 8);
+        if ((h * L + lane) * 8 < a.width) put(at((h * L + lane) * 8), v[h], 8);
     } else {
       for (int c = lane * 8; c < a.width; c += L * 8) {
-        v[0].load(x + c, a.width - c);
-        put(c, v[0], a.width - c);
+        v[0].load(x + at(c), WHOLE ? 8 : a.width - c);
+        put(at(c), v[0], WHOLE ? 8 : a.width - c);
       }
     }
   }
@@ -198,14 +200,17 @@ template <typename T>
 void launch_quantize(const QuantizeArgs &a, hipStream_t s) {
   void (*kernel)(QuantizeArgs);
   const int lanes = a.width > 8192 ? 1024 : a.width > 512 && (a.rows < 4096 || a.width > 4096) ? 256 : 64;
-  const int turns = a.width % 8 ? 0 : (a.width + lanes * 8 - 1) / (lanes * 8);  // whole ones
-#define RRB_PICK(LANES)                                     \
-  turns == 0 || turns > 8 ? quantize_kernel<T, LANES, 0>    \
-  : turns <= 1            ? quantize_kernel<T, LANES, 1>    \
-  : turns <= 2            ? quantize_kernel<T, LANES, 2>    \
-  : turns <= 4            ? quantize_kernel<T, LANES, 4>    \
-                          : quantize_kernel<T, LANES, LANES == 256 ? 4 : 8>
-  kernel = lanes == 1024 ? RRB_PICK(1024) : lanes == 256 ? RRB_PICK(256) : RRB_PICK(64);
+  const int turns = (a.width + lanes * 8 - 1) / (lanes * 8);
+#define RRB_PICK(LANES)                                          \
+  turns > 8    ? quantize_kernel<T, LANES, 0, true>              \
+  : turns <= 1 ? quantize_kernel<T, LANES, 1, true>              \
+  : turns <= 2 ? quantize_kernel<T, LANES, 2, true>              \
+  : turns <= 4 ? quantize_kernel<T, LANES, 4, true>              \
+               : quantize_kernel<T, LANES, LANES == 256 ? 4 : 8, true>
+  kernel = a.width < 8 ? quantize_kernel<T, 64, 0, false>
+           : lanes == 1024 ? RRB_PICK(1024)
+           : lanes == 256  ? RRB_PICK(256)
+                           : RRB_PICK(64);
 #undef RRB_PICK
   const int rows = lanes == 64 ? 4 : 1;
   const int64_t blocks = (a.rows + rows - 1) / rows;
