@@ -1004,22 +1004,24 @@ template <bool INT>
 rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
   const int most = a.experts < a.tokens * a.topk ? a.experts : a.tokens * a.topk;
   dim3 up_grid(static_cast<unsigned>(most * a.tiles)), down_grid(static_cast<unsigned>((a.hidden + 15) / 16));
-  const int per = INT ? 16 : 8;  // elements of 16 bytes
-  const uintptr_t weights = reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.up) |
-                            reinterpret_cast<uintptr_t>(a.down) | reinterpret_cast<uintptr_t>(a.x);
-  // Where offsets into h fit the buffers' 31 bits (all but widths near 2^20).
-  const bool direct = a.experts <= direct_experts(a.tokens) && a.hidden % per == 0 && a.inner % per == 0 &&
-                      weights % 16 == 0 &&
-                      static_cast<int64_t>(a.tokens) * a.topk * 4 * a.pitch < (1LL << 31);
+  // Weights go through LDS where the rows that a kernel reads start on 16-byte
+  // boundaries (integers: and both widths are of whole sixteens, as their scales are
+  // read), the tables have room, and (all but widths near 2^20) offsets into h fit the
+  // buffers' 31 bits.
+  auto whole = [](const void *p, int width) { return width % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  const bool room = a.experts <= direct_experts(a.tokens) && (!INT || (a.hidden % 16 == 0 && a.inner % 16 == 0));
+  const bool up_direct = room && whole(a.gate, a.hidden) && whole(a.up, a.hidden) && whole(a.x, a.hidden);
+  const bool down_direct = room && whole(a.down, a.inner) &&
+                           static_cast<int64_t>(a.tokens) * a.topk * 4 * a.pitch < (1LL << 31);
   void (*up)(DecodeArgs), (*down)(DecodeArgs);
   int down_waves = kDownWaves;
   unsigned lds = 0;
-  if (direct) {
+  const int t = a.tokens;
+  if (up_direct) {
     // The first kernel's workgroups stay, two a CU, or one with deeper rings and tables
     // for up to 64 tokens (us, both kernels, 64 tokens on 8 experts, top-2, 4096 x 4096:
     // 249 at two a CU, where an expert's tokens go sixteen at a time, and 220; 64
     // tokens, an eighth of them here, on 32 experts, 7168 x 2048: 371 either way).
-    const int t = a.tokens;
     int there = 512;
     if (t <= 8)
       up = decode_up_direct_kernel<INT, 8, 1, 18432>;
@@ -1028,6 +1030,11 @@ rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
     else
       up = decode_up_direct_kernel<INT, 64, 4, 34816>, there = 256;
     if (up_grid.x > static_cast<unsigned>(there)) up_grid.x = there;
+  } else {
+    if (up_grid.x > 1 << 20) up_grid.x = 1 << 20;
+    up = up_kernel<INT>((t + 15) / 16);
+  }
+  if (down_direct) {
     // The second kernel's are as many as there are tiles of 16 channels: two of four
     // waves a CU, or one of eight where they are at most the CUs.  Tokens that all
     // meet on few experts want all columns at once, and the LDS for it.
@@ -1045,10 +1052,8 @@ rrb_status launch_decode(const DecodeArgs &a, hipStream_t s) {
                   : decode_down_direct_kernel<INT, 64, 8, MOST, 12288>;
     down_waves = wide || dense ? 4 : 8;
   } else {
-    if (up_grid.x > 1 << 20) up_grid.x = 1 << 20;
-    up = up_kernel<INT>((a.tokens + 15) / 16);
-    down = down_kernel<INT>((a.tokens + 7) / 8);
-    lds = kDownWaves * a.tokens * 64;
+    down = down_kernel<INT>((t + 7) / 8);
+    lds = kDownWaves * t * 64;
   }
   hipLaunchKernelGGL(up, up_grid, dim3(kUpWaves * 64), 0, s, a);
   hipError_t e = hipGetLastError();

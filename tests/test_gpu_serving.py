@@ -405,6 +405,7 @@ class Layer:
 
 
 LAYERS = [
+    (6, 2, 5, 264, 301, 0), (6, 2, 5, 301, 264, 0), (30, 2, 5, 72, 203, 1), (30, 2, 5, 203, 72, 1),
     (64, 4, 8, 256, 144, 0), (20, 6, 6, 4160, 64, 0), (12, 2, 600, 64, 32, 0), (8, 3, 1024, 64, 32, 1),
     (3, 16, 1023, 96, 48, 0), (33, 2, 400, 96, 32, 10), (64, 16, 513, 64, 16, 0),
     # T, k, E, h, f, experts beyond either end
