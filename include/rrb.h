@@ -420,10 +420,10 @@ rrb_status rrb_expert_linear_backward(const rrb_expert_spec *spec, const void *d
  * 127), q = x / scale to the nearest integer, ties to even, exactly (kept within
  * +-127 where a subnormal scale would pass it).  A row of zeros has the scale 0;
  * a row with an infinity or a NaN has a NaN for its scale and zeros for its
- * integers, so that what is computed from it is NaN.  d_offsets (nullable): int32, groups + 1 entries, of which the
- * first and the last bound the rows that are read and written, clamped to
- * 0..rows.  Weights [groups][out][in] are groups * out rows.  Limits
- * (RRB_EUNSUPPORTED): rows < 2^31, width <= 2^20.
+ * integers, so that what is computed from it is NaN.  d_offsets (nullable):
+ * int32, groups + 1 entries, of which the first and the last bound the rows that
+ * are read and written, clamped to 0..rows.  Weights [groups][out][in] are
+ * groups * out rows.  Limits (RRB_EUNSUPPORTED): rows < 2^31, width <= 2^20.
  */
 rrb_status rrb_quantize_rows(int64_t rows, int64_t width, int32_t dtype, const void *d_x,
                              const int32_t *d_offsets, int32_t groups, int8_t *d_q, float *d_scale,
@@ -456,10 +456,10 @@ rrb_status rrb_expert_gated_int8(const rrb_expert_spec *spec, const int8_t *d_x,
  * [experts][hidden][inner], and topk_idx, topk_w [tokens][topk] as rrb_moe_gate
  * writes them.  Weights are bf16, or (all three scales given) int8 with scales
  * [experts][inner], [experts][inner] and [experts][hidden].  Sums are fp32, h is
- * kept in two bf16 parts (16 bits), and y is rounded once.  Choices outside 0..experts - 1 take no part (experts
- * of another rank), nor does their weight; an expert that a token chose twice
- * counts twice.  A token without choices has y = 0.  Weights of experts without
- * tokens are not read.  Results do not depend on the launch: the same inputs give
+ * kept in two bf16 parts (16 bits), and y is rounded once.  Choices outside
+ * 0..experts - 1 take no part (experts of another rank), nor does their weight;
+ * an expert that a token chose twice counts twice.  A token without choices has
+ * y = 0.  Weights of experts without tokens are not read.  Results do not depend on the launch: the same inputs give
  * the same bits.  d_workspace holds h between the two kernels (caller-owned,
  * 16-byte aligned, of the size the query gives; in use until the call's work
  * completes).  Buffers need the alignment of their elements only; out and the
