@@ -455,7 +455,9 @@ __global__ void __launch_bounds__(kUpWaves * 64) decode_up_kernel(DecodeArgs a) 
 // ---- y ------------------------------------------------------------------------------
 
 // Adds an expert's sixteen channels of a token to its sums: those of both parts of
-// h, which are two columns, HALF apart.
+// h, which are two columns, HALF apart.  Where an infinite weight (or a NaN) has made
+// the first part's sum infinite it stands alone: the second part, 0 or of either
+// sign, would turn it into a NaN.
 template <int HALF>
 __device__ __forceinline__ void add_expert(f32x4_t acc, bool scaled, f32x4_t scale, int token, float share,
                                            f32x4_t *sums) {
@@ -464,7 +466,7 @@ __device__ __forceinline__ void add_expert(f32x4_t acc, bool scaled, f32x4_t sca
   for (int q = 0; q < 4; ++q) {
     // row_ror by 16 - HALF: lane i of a row receives lane (i + HALF) % 16.
     const int other = __builtin_amdgcn_mov_dpp(__float_as_int(acc[q]), 0x120 + 16 - HALF, 0xf, 0xf, false);
-    z[q] = acc[q] + __int_as_float(other);
+    z[q] = fabsf(acc[q]) < INFINITY ? acc[q] + __int_as_float(other) : acc[q];
     if (scaled) z[q] *= scale[q];
   }
   if (token < 0) return;
