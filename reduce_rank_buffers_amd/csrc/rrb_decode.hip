@@ -295,7 +295,10 @@ struct Block {
 };
 
 // acc += rows x xrows over the blocks first, first + step, .. below `last` of k, one
-// block ahead.  Only the last block of a row may be partial.
+// block ahead, two blocks a turn (with the loop's ends behind each, the compiler kept
+// copies of both: up to 512 bytes of scratch a lane, and 64 tokens on 16 experts, 2001
+// x 1001, took 122 us, integers 119, where these are 114 and 73).  Only the last block
+// of a row may be partial.
 template <bool INT, int M, int NC, int U>
 __device__ __forceinline__ void sum_blocks(f32x4_t (&acc)[M][NC],
                                            const typename Element<INT>::T *const (&rows)[M],
@@ -306,22 +309,17 @@ __device__ __forceinline__ void sum_blocks(f32x4_t (&acc)[M][NC],
   if (b < whole) {
     B even, odd;
     even.load(rows, xrows, b * B::K);
-    for (;;) {
-      b += step;
-      if (b >= whole) {
-        even.multiply(acc);
-        break;
-      }
-      odd.load(rows, xrows, b * B::K);
+    for (; b + 2 * step < whole; b += 2 * step) {
+      odd.load(rows, xrows, (b + step) * B::K);
       even.multiply(acc);
-      b += step;
-      if (b >= whole) {
-        odd.multiply(acc);
-        break;
-      }
-      even.load(rows, xrows, b * B::K);
+      even.load(rows, xrows, (b + 2 * step) * B::K);
       odd.multiply(acc);
     }
+    const bool more = b + step < whole;
+    if (more) odd.load(rows, xrows, (b + step) * B::K);
+    even.multiply(acc);
+    if (more) odd.multiply(acc);
+    b += more ? 2 * step : step;
   }
   if (b < last) {
     // (At once where the registers have room.)
@@ -334,9 +332,12 @@ __device__ __forceinline__ void sum_blocks(f32x4_t (&acc)[M][NC],
   }
 }
 
-// Fragments per block, so that two blocks leave registers for enough waves.
-template <int NC>
-constexpr int kDepth = NC == 4 ? 1 : NC == 2 ? 2 : 4;
+// Fragments per block, so that two blocks leave registers for two waves a SIMD and
+// more (integers have twice the columns' bytes per fragment: at bf16's depths 193 to
+// 272 registers, and 64 tokens on 16 experts, 2001 x 1001, took 83 us; at these 119
+// to 206, and 73).
+template <bool INT, int NC>
+constexpr int kDepth = INT ? (NC == 1 ? 2 : 1) : NC == 1 ? 4 : NC == 2 ? 2 : 1;
 
 // Calls `run` with NC = 1, 2 or 4 tiles of 16, whichever holds `tiles` first; MOST
 // bounds what is compiled.
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kUpWaves * 64) decode_up_kernel(DecodeArgs a) 
     const T *const rows[2] = {static_cast<const T *>(a.gate) + row * a.hidden,
                               static_cast<const T *>(a.up) + row * a.hidden};
     with_tiles<MOST>((who.many + 15) / 16, [&](auto tiles) {
-      constexpr int NC = decltype(tiles)::value, U = kDepth<NC>, K = U * kFragment<INT>;
+      constexpr int NC = decltype(tiles)::value, U = kDepth<INT, NC>, K = U * kFragment<INT>;
       const uint16_t *xrows[NC];
       int to[NC];
 #pragma unroll
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(WAVES * 64) decode_down_kernel(DecodeArgs a) {
   f32x4_t *const sums = all + wave * a.tokens * 4;
   for (int t = lane; t < a.tokens * 4; t += 64) sums[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int count = find_experts<NT, kMaxTokens, kRouteMaxExperts>(a, choices, &weights).experts;
-  constexpr int K = kFragment<INT> * kDepth<1>;  // a unit of the waves' shares: whole blocks of every depth
+  constexpr int K = kFragment<INT> * kDepth<INT, 1>;  // a unit of the waves' shares: whole blocks of every depth
   const int per = (a.inner + K - 1) / K;         // units per expert
   int b = static_cast<int>(static_cast<int64_t>(count) * per * wave / WAVES);
   const int end = static_cast<int>(static_cast<int64_t>(count) * per * (wave + 1) / WAVES);
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(WAVES * 64) decode_down_kernel(DecodeArgs a) {
     const T *const rows[1] = {static_cast<const T *>(a.down) + row * a.inner};
     for (int base = 0; base < who.many; base += 8 * MOST) {
       with_tiles<MOST>((who.many - base + 7) / 8, [&](auto tiles) {
-        constexpr int NC = decltype(tiles)::value, U = kDepth<NC>, PER = kDepth<1> / U;
+        constexpr int NC = decltype(tiles)::value, U = kDepth<INT, NC>, PER = kDepth<INT, 1> / U;
         const uint16_t *xrows[NC];
         int token[NC];
         float share[NC];

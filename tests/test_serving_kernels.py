@@ -1,0 +1,52 @@
+"""What the built library holds of the serving kernels, by the metadata of its
+own code objects.  Runs on the CPU."""
+
+import re
+import struct
+
+import pytest
+
+from reduce_rank_buffers_amd import _lib as L
+
+msgpack = pytest.importorskip("msgpack")
+
+
+@pytest.fixture(scope="module")
+def kernels(librrb):
+    """{mangled name: metadata} of every kernel in librrb.so: the notes named
+    AMDGPU, of type 32, of the code objects in it."""
+    with open(L.LIB_PATH, "rb") as f:
+        data = f.read()
+    out, at = {}, data.find(b"AMDGPU\0\0")
+    while at >= 0:
+        name, size, kind = struct.unpack("<III", data[at - 12:at])
+        if name == 7 and kind == 32:
+            for k in msgpack.unpackb(data[at + 8:at + 8 + size]).get("amdhsa.kernels", []):
+                out[k[".name"]] = k
+        at = data.find(b"AMDGPU\0\0", at + 8)
+    assert len(out) > 100
+    return out
+
+
+def _of(kernels, name):
+    """{template arguments: metadata} of the kernels of that name: integers and
+    truth values, and types by their mangled letter."""
+    out = {}
+    for mangled, k in kernels.items():
+        m = re.search(rf"\d{name}I((?:L[ib]\d+E|[a-z])+)E", mangled)
+        if m:
+            args = re.findall(r"L[ib](\d+)E|([a-z])", m.group(1))
+            out[tuple(int(n) if n else t for n, t in args)] = k
+    return out
+
+
+@pytest.mark.parametrize("name", ["decode_up_kernel", "decode_down_kernel", "decode_up_direct_kernel",
+                                  "decode_down_direct_kernel", "quantize_kernel", "product_kernel",
+                                  "product_direct_kernel", "product_turns_kernel"])
+def test_no_kernel_spills(kernels, name):
+    """None keeps vector registers in memory."""
+    found = _of(kernels, name)
+    assert found
+    spilled = {a: k[".private_segment_fixed_size"] for a, k in found.items()
+               if k[".private_segment_fixed_size"] or k[".vgpr_spill_count"]}
+    assert not spilled, f"{name}: bytes of scratch a lane: {spilled}"
