@@ -1331,22 +1331,25 @@ template <int FORM, bool GATED, typename EL>
 rrb_status launch_product(const ProductArgs<EL> &p, hipStream_t s) {
   bool direct = p.lda % kPer<EL> == 0 && p.ldb % kPer<EL> == 0;
   for (int h = 0; h < 2; ++h) direct = direct && aligned(p.a[h], 16) && aligned(p.b[h], 16);
-  if constexpr (sizeof(EL) == 1) return launch_integers<GATED>(p, direct, s);
-  if (!direct) {
-    if (estimate<FORM, GATED>(p, 128, 128, 2, 1.7, 2) <= estimate<FORM, GATED>(p, 64, 64, 4, 1.1, 1))
-      return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED, EL>, 256, p, s);
-    return launch_tiles<64, 64, FORM, GATED>(product_kernel<64, 64, 2, 2, FORM, GATED, EL>, 256, p, s);
+  if constexpr (sizeof(EL) == 1) {
+    return launch_integers<GATED>(p, direct, s);
+  } else {
+    if (!direct) {
+      if (estimate<FORM, GATED>(p, 128, 128, 2, 1.7, 2) <= estimate<FORM, GATED>(p, 64, 64, 4, 1.1, 1))
+        return launch_tiles<128, 128, FORM, GATED>(product_kernel<128, 128, 2, 2, FORM, GATED, EL>, 256, p, s);
+      return launch_tiles<64, 64, FORM, GATED>(product_kernel<64, 64, 2, 2, FORM, GATED, EL>, 256, p, s);
+    }
+    // A tile of at most 128 valid rows takes about half a 256-row step.
+    const bool half = FORM != kGradW && static_cast<int64_t>(p.groups) * 128 >= p.rows;
+    const double big = estimate<FORM, GATED>(p, 256, 256, 1, half ? 0.9 : 1.55, 8);
+    const double mid = estimate<FORM, GATED>(p, 64, 256, 1, 0.66, 4);
+    const double low = estimate<FORM, GATED>(p, 64, 64, 2, 0.42, 2);
+    if (big <= mid && big <= low)
+      return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED, EL>, 512, p, s);
+    if (mid <= low)
+      return launch_tiles<64, 256, FORM, GATED>(product_direct_kernel<64, 256, 2, 4, 3, FORM, GATED, EL>, 512, p, s);
+    return launch_tiles<64, 64, FORM, GATED>(product_direct_kernel<64, 64, 2, 2, 5, FORM, GATED, EL>, 256, p, s);
   }
-  // A tile of at most 128 valid rows takes about half a 256-row step.
-  const bool half = FORM != kGradW && static_cast<int64_t>(p.groups) * 128 >= p.rows;
-  const double big = estimate<FORM, GATED>(p, 256, 256, 1, half ? 0.9 : 1.55, 8);
-  const double mid = estimate<FORM, GATED>(p, 64, 256, 1, 0.66, 4);
-  const double low = estimate<FORM, GATED>(p, 64, 64, 2, 0.42, 2);
-  if (big <= mid && big <= low)
-    return launch_tiles<256, 256, FORM, GATED>(product_turns_kernel<FORM, GATED, EL>, 512, p, s);
-  if (mid <= low)
-    return launch_tiles<64, 256, FORM, GATED>(product_direct_kernel<64, 256, 2, 4, 3, FORM, GATED, EL>, 512, p, s);
-  return launch_tiles<64, 64, FORM, GATED>(product_direct_kernel<64, 64, 2, 2, 5, FORM, GATED, EL>, 256, p, s);
 }
 
 // What every entry point checks of its sizes.

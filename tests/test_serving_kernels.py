@@ -50,3 +50,15 @@ def test_no_kernel_spills(kernels, name):
     spilled = {a: k[".private_segment_fixed_size"] for a, k in found.items()
                if k[".private_segment_fixed_size"] or k[".vgpr_spill_count"]}
     assert not spilled, f"{name}: bytes of scratch a lane: {spilled}"
+
+
+def test_integer_products_built(kernels):
+    """The tile shapes that launch_integers chooses among, linear and gated, and
+    no others: of product_kernel and product_direct_kernel BM, BN, waves down and
+    across, stages (the second), form, gated, elements (a: int8), once."""
+    both = (0, 1)
+    of = lambda name: {a for a in _of(kernels, name) if "a" in a}
+    assert of("product_kernel") == {(*t, 0, g, "a") for t in ((128, 128, 2, 4), (64, 64, 2, 2)) for g in both}
+    assert of("product_direct_kernel") == {(*t, 0, g, "a", once) for g in both for *t, once in (
+        (32, 64, 2, 2, 4, 1), (64, 64, 2, 2, 5, 0), (64, 128, 2, 2, 3, 0), (128, 256, 2, 4, 3, 0))}
+    assert of("product_turns_kernel") == {(0, g, "a") for g in both}
