@@ -201,17 +201,23 @@ void launch_quantize(const QuantizeArgs &a, hipStream_t s) {
   void (*kernel)(QuantizeArgs);
   const int lanes = a.width > 8192 ? 1024 : a.width > 512 && (a.rows < 4096 || a.width > 4096) ? 256 : 64;
   const int turns = (a.width + lanes * 8 - 1) / (lanes * 8);
-#define RRB_PICK(LANES)                                          \
-  turns > 8    ? quantize_kernel<T, LANES, 0, true>              \
-  : turns <= 1 ? quantize_kernel<T, LANES, 1, true>              \
-  : turns <= 2 ? quantize_kernel<T, LANES, 2, true>              \
-  : turns <= 4 ? quantize_kernel<T, LANES, 4, true>              \
-               : quantize_kernel<T, LANES, LANES == 256 ? 4 : 8, true>
-  kernel = a.width < 8 ? quantize_kernel<T, 64, 0, false>
-           : lanes == 1024 ? RRB_PICK(1024)
-           : lanes == 256  ? RRB_PICK(256)
-                           : RRB_PICK(64);
-#undef RRB_PICK
+  // (A row of 64 lanes takes at most eight turns, of 256 four, of 1024 two or more.)
+  if (a.width < 8)
+    kernel = quantize_kernel<T, 64, 0, false>;
+  else if (lanes == 64)
+    kernel = turns <= 1   ? quantize_kernel<T, 64, 1, true>
+             : turns <= 2 ? quantize_kernel<T, 64, 2, true>
+             : turns <= 4 ? quantize_kernel<T, 64, 4, true>
+                          : quantize_kernel<T, 64, 8, true>;
+  else if (lanes == 256)
+    kernel = turns <= 1   ? quantize_kernel<T, 256, 1, true>
+             : turns <= 2 ? quantize_kernel<T, 256, 2, true>
+                          : quantize_kernel<T, 256, 4, true>;
+  else
+    kernel = turns <= 2   ? quantize_kernel<T, 1024, 2, true>
+             : turns <= 4 ? quantize_kernel<T, 1024, 4, true>
+             : turns <= 8 ? quantize_kernel<T, 1024, 8, true>
+                          : quantize_kernel<T, 1024, 0, true>;
   const int rows = lanes == 64 ? 4 : 1;
   const int64_t blocks = (a.rows + rows - 1) / rows;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : 1 << 20)),

@@ -62,3 +62,11 @@ def test_integer_products_built(kernels):
     assert of("product_direct_kernel") == {(*t, 0, g, "a", once) for g in both for *t, once in (
         (32, 64, 2, 2, 4, 1), (64, 64, 2, 2, 5, 0), (64, 128, 2, 2, 3, 0), (128, 256, 2, 4, 3, 0))}
     assert of("product_turns_kernel") == {(0, g, "a") for g in both}
+
+
+def test_quantisations_built(kernels):
+    """What launch_quantize's rule on widths and rows can come to, for bf16 (t)
+    and fp32 (f): lanes, turns held (0: any), rows of at least eight."""
+    want = {(64, 0, 0)} | {(64, n, 1) for n in (1, 2, 4, 8)} | {(256, n, 1) for n in (1, 2, 4)}
+    want |= {(1024, n, 1) for n in (2, 4, 8, 0)}
+    assert set(_of(kernels, "quantize_kernel")) == {(t, *a) for t in "tf" for a in want}
