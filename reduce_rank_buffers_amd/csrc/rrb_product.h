@@ -392,6 +392,7 @@ struct Place {
   int32_t row0, klen;   // klen: reduction length (per phase)
   int32_t e, n0, m0, mvalid;
   bool empty;
+  bool single;  // the group's only row tile (not kGradW)
 };
 
 // Tile (mt, nt) of group e, whose rows are first .. last - 1; BM x NCOLS
@@ -402,6 +403,7 @@ __device__ __forceinline__ Place<EL> place_at(const ProductArgs<EL> &p, int e, i
   t.e = e;
   t.n0 = nt * NCOLS;
   t.empty = false;
+  t.single = false;
   if (FORM == kGradW) {
     const int tiles = p.mtiles / p.halves;
     const int half = mt / tiles;
@@ -414,6 +416,7 @@ __device__ __forceinline__ Place<EL> place_at(const ProductArgs<EL> &p, int e, i
     t.c = p.c[half] + e * p.bstride + t.m0 * p.ldc;
   } else {
     t.m0 = 0;
+    t.single = last - first <= BM;
     t.row0 = first + mt * BM;
     t.mvalid = uniform(last - t.row0 < BM ? last - t.row0 : BM);
     t.klen = p.k;
@@ -789,6 +792,7 @@ __device__ __forceinline__ void load_two_to_lds(u32x4_t d, int at, int voffset0,
       : "memory");
 }
 
+// ONCE: the weights of a group that has one row of tiles go past the caches.
 template <int BM, int BN, int WR, int WC, int STAGES, int FORM, bool GATED, typename EL, bool ONCE = false>
 __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs<EL> p) {
   constexpr int PER = kPer<EL>, STEP = kSteps<EL>;
@@ -836,7 +840,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
 
   // Starts one step's loads into buffer `buf`; past the end through an empty
   // descriptor, so that every step counts the same.
-  auto issue = [&](int step, int buf) {
+  auto issue = [&](auto past, int step, int buf) {
     const int h = FORM == kGradX && step >= per ? 1 : 0;
     const int kstep = step - h * per;
     const int k0 = kstep * STEP;
@@ -880,7 +884,7 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
         }
         // The wave's eight rows are all gate rows or all up rows.
         const bool up = GATED && gated_up((i * NT + wave * 64) >> 3);
-        load_to_lds<ONCE>(up ? d1 : d0, tb + i * NT * 16, v, along);
+        load_to_lds<decltype(past)::value>(up ? d1 : d0, tb + i * NT * 16, v, along);
       }
     }
   };
@@ -888,35 +892,36 @@ __global__ void __launch_bounds__(WR *WC * 64) product_direct_kernel(ProductArgs
   const int wm = wave / WC * (BM / WR), wn = wave % WC * (BN / WC);
   typename Element<EL>::Sum acc[FM][FN];
   clear_tile(acc);
-  if (steps > 0) {
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+  // The steps, once for each way of the weights' loads (as a lambda they made the
+  // compiler order the other kernels' instructions anew).
+#define RRB_STEPS(PAST)                                                                                     \
+  constexpr std::integral_constant<bool, PAST> past;                                                        \
+  if (steps > 0) {                                                                                          \
+    _Pragma("unroll") for (int s = 0; s < STAGES - 1; ++s) issue(past, s, s);                               \
+  }                                                                                                         \
+  int buf = 0, free = STAGES - 1;                                                                           \
+  for (int s = 0; s < steps; ++s) {                                                                         \
+    /* This step's loads have landed, and every wave is done with the buffer that is loaded next. */        \
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (CA + CB)) : "memory"); \
+    issue(past, s + STAGES - 1, free);                                                                      \
+    free = buf;                                                                                             \
+    const unsigned char *ta = lds + buf * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;                          \
+    buf = buf + 1 == STAGES ? 0 : buf + 1;                                                                  \
+    _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) {                                                      \
+      typename Element<EL>::Fragment fa[FM], fb[FN];                                                        \
+      _Pragma("unroll") for (int j = 0; j < FN; ++j) fb[j] = fragment<B_COL, BN, EL>(tb, wn + j * 16, kk);  \
+      _Pragma("unroll") for (int i = 0; i < FM; ++i) fa[i] = fragment<A_COL, BM, EL>(ta, wm + i * 16, kk);  \
+      _Pragma("unroll") for (int i = 0; i < FM; ++i)                                                        \
+        _Pragma("unroll") for (int j = 0; j < FN; ++j)                                                      \
+          acc[i][j] = Element<EL>::multiply(fb[j], fa[i], acc[i][j]);                                       \
+    }                                                                                                       \
   }
-  int buf = 0, free = STAGES - 1;
-  for (int s = 0; s < steps; ++s) {
-    // This step's loads have landed, and every wave is done with the buffer
-    // that is loaded next.
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (CA + CB)) : "memory");
-    issue(s + STAGES - 1, free);
-    free = buf;
-    const unsigned char *ta = lds + buf * (A_BYTES + B_BYTES), *tb = ta + A_BYTES;
-    buf = buf + 1 == STAGES ? 0 : buf + 1;
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      typename Element<EL>::Fragment fa[FM], fb[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        fb[j] = fragment<B_COL, BN, EL>(tb, wn + j * 16, kk);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-        fa[i] = fragment<A_COL, BM, EL>(ta, wm + i * 16, kk);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = Element<EL>::multiply(fb[j], fa[i], acc[i][j]);
-    }
+  if (ONCE && t.single) {
+    RRB_STEPS(ONCE)
+  } else {
+    RRB_STEPS(false)
   }
+#undef RRB_STEPS
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   finish_tile<FORM, GATED, false>(p, t, acc, Spot{wm, GATED ? wn / 2 : wn, FM * 8, FN * (GATED ? 4 : 8)}, nullptr);
 }
@@ -1284,12 +1289,14 @@ double estimate_integers(const ProductArgs<int8_t> &p, int bm, int bn, int resid
 //   G 2, 1024, 4096 x 4096: 57, 45, 57, 71            G 1, 512, 8192 x 1024: 96, 64, 40, 27
 //   G 9, 334, 2000 x 1112: 35, 28, 26, 31             G 32, 160, 2048 x 1024: 34, 30, 36, 39
 //   G 16, 64, 4096 x 2048: 49, 45, 41, 36             gated, G 32, 74 to 410, 7168 x 2048: 244, 223, 296, 350
-// Groups of few rows take 32 x 64 tiles, three workgroups a CU, and their weights,
-// which one row of tiles reads, go past the caches (G 24, 1 row, 2048 x 7168: 75 at
-// 64 x 64, 71 past the caches, 61 at 32 x 64, 5.8 TB/s; 7168 x 2048 gated: 119, 110,
-// 105; G 32, 16 rows, 7168 x 2048: 88, 81, 75; G 1, 1 row, 4096 x 4096: 17, 17, 14.
-// Where three rows of tiles share the weights, G 32, 160 rows: 39 and 46 past the
-// caches).
+// Groups of few rows, on average, take 32 x 64 tiles, three workgroups a CU.  How many
+// rows each has the device knows: a group of one row of tiles has its weights past
+// the caches (G 24, 1 row, 2048 x 7168: 75 at 64 x 64, 71 past the caches, 61 at 32 x
+// 64, 5.8 TB/s; 7168 x 2048 gated: 119, 110, 105; G 32, 16 rows, 7168 x 2048: 88, 81,
+// 75; G 1, 1 row, 4096 x 4096: 17, 17, 13), in one of more the tiles share them (always
+// past the caches, through them for all, and by group; G 32, 800 rows of which 500 in
+// one, 2048 x 7168: 116, 112, 105; 7168 x 2048 gated: 193, 193, 173; all 1024 rows in one
+// of 32: 67, 52, 53 and 116, 73, 73).
 // Rows off 16-byte boundaries: 128 x 128 by eight waves where there are enough (one
 // step ahead, G 9, 334 rows, 2001 x 1111: 43 -> 31, gated 72 -> 42; G 1, 4000, 4001 x
 // 4001: 241 -> 136), else 64 x 64 (G 16, 1 row, 2001 x 1111: 24 and 21).

@@ -67,3 +67,27 @@ def test_decode_infinite_weight_of_a_whole_h(width, tokens):
                    one.to(DEV), one.to(DEV), down.to(DEV), y, activation="none")
     want = torch.tensor([float("inf"), float("-inf"), 3] + [0.0] * (width - 3)).expand(tokens, width)
     assert torch.equal(y.float().cpu(), want)
+
+
+# ---- groups of very unequal sizes ----------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes", [[7] * 5 + [500] + [9, 0, 1, 33, 32] + [4] * 20, [0] * 7 + [1024] + [0] * 24,
+                                   [65, 0, 1], [64], [33] + [31] * 3], ids=lambda s: f"{len(s)}x{max(s)}")
+@pytest.mark.parametrize("i,o", [(208, 264), (2064, 136)])
+def test_few_rows_on_average(sizes, i, o):
+    """Arenas of at most 32 rows a group on average (and some just above): groups
+    of one row tile, whose weights go past the caches, beside groups of many,
+    whose tiles share theirs."""
+    require_gpu()
+    S._linear_int8(S.Integers(42, sizes, i, o), "gelu", True, True)
+    S._gated_int8(S.Integers(43, sizes, i, o // 2, 2, 3), "silu")
+
+
+@pytest.mark.gpu
+def test_few_rows_of_an_arena():
+    """A slice of the groups over the whole arena: eight times the rows that the
+    offsets bound, the other rows left as they were."""
+    require_gpu()
+    S._linear_int8(S.Integers(44, [5, 0, 40, 1], 272, 200, 300, 20), "none", True, False)
+    S._gated_int8(S.Integers(45, [5, 0, 40, 1], 272, 200, 300, 20), "silu")
