@@ -91,3 +91,119 @@ def test_few_rows_of_an_arena():
     require_gpu()
     S._linear_int8(S.Integers(44, [5, 0, 40, 1], 272, 200, 300, 20), "none", True, False)
     S._gated_int8(S.Integers(45, [5, 0, 40, 1], 272, 200, 300, 20), "silu")
+
+
+# ---- both parts of h ---------------------------------------------------------------
+
+class Exact:
+    """A layer of whole numbers in which nothing is rounded but the result: x and
+    the weights small integers (int8: with scales that are powers of two), g and
+    u at most 255, so that h = g u has at most 16 bits and its two bf16 parts
+    hold it, and every sum below 2^24 quarters.  Half of the tokens take expert
+    0, so that experts have one token and many."""
+
+    def __init__(self, T, k, E, h, f, int8=False):
+        rng = X._rng(46, T, k, E, h, f)
+        self.shape, self.int8 = (T, k, E, h, f), int8
+        self.x = rng.integers(-3, 4, (T, h)).astype(np.float64)
+        self.idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+        for t in range(0, T, 2):
+            if 0 not in self.idx[t]:
+                self.idx[t, 0] = 0
+        self.w = 2.0 ** rng.integers(-2, 1, (T, k))
+        draw = lambda *s: np.clip(np.rint(rng.standard_normal(s) * 17 / h ** 0.5), -9, 9)
+        self.m = [draw(E, f, h), draw(E, f, h), rng.integers(-1, 2, (E, h, f)).astype(np.float64)]
+        self.s = [2.0 ** rng.integers(-1, 2, m.shape[:2]) if int8 else np.ones(m.shape[:2]) for m in self.m]
+
+    def expect(self, parts=lambda h: h):
+        """The result as a float64 array; `parts` is what becomes of a token's h."""
+        T, k, E, h, f = self.shape
+        y, mass = np.zeros((T, h)), np.zeros((T, h))
+        for e in range(E):
+            t, j = np.nonzero(self.idx == e)
+            g, u = (self.x[t] @ m[e].T for m in self.m[:2])
+            assert g.size == 0 or max(np.abs(g).max(), np.abs(u).max()) <= 255
+            hid = (g * self.s[0][e]) * (u * self.s[1][e])
+            add = self.w[t, j, None] * ((parts(hid) @ self.m[2][e].T) * self.s[2][e])
+            np.add.at(y, t, add)
+            np.add.at(mass, t, self.w[t, j, None] * ((np.abs(hid) @ np.abs(self.m[2][e]).T) * self.s[2][e]))
+        # (quarters of h's scales, 1/4, and of Wd's, 1/2, and weights, 1/4: multiples of 1/32)
+        assert mass.max() * 32 * 1.01 < 2 ** 24 or not self.int8
+        assert mass.max() * 4 * 1.01 < 2 ** 24
+        return y
+
+    def run(self, **kw):
+        to = lambda a, t: torch.from_numpy(a).to(t).to(DEV)
+        y = torch.full(self.x.shape, -7.25, dtype=BF, device=DEV)
+        rrb.moe_decode(to(self.x, BF), to(self.idx, torch.int32), to(self.w, torch.float32),
+                       *(to(m, torch.int8 if self.int8 else BF) for m in self.m), y, activation="none",
+                       scales=tuple(to(s, torch.float32) for s in self.s) if self.int8 else None, **kw)
+        return y
+
+
+def _round(y):
+    return torch.from_numpy(y).float().to(BF)
+
+
+# T, k, E, h, f, and the kernels they are for: the first kernel's tokens, the second's
+# tokens and waves (d: for few experts), or tiles of registers (r).
+EXACT = [
+    (3, 2, 5, 64, 48),      # 8; 8 with 8 waves, a token's two columns 4 apart
+    (8, 2, 3, 64, 48),      # 8; 8 with 8 waves, 8 apart
+    (6, 2, 4, 4112, 48),    # 8; 8 with 4 waves
+    (16, 2, 4, 64, 48),     # 16; 16 with 8 waves
+    (12, 2, 9, 4112, 64),   # 16; 16 with 4 waves
+    (40, 2, 32, 128, 64),   # 64; 64 with 8 waves
+    (40, 2, 32, 4112, 64),  # 64; 64 with 4 waves
+    (64, 8, 64, 4112, 48),  # 64; 64 with 4 waves, an expert with 32 tokens and more beside those of a few
+    (64, 4, 8, 128, 48),    # 64; 64 d
+    (3, 2, 5, 63, 47), (16, 2, 4, 63, 47), (24, 2, 3, 63, 47), (64, 4, 8, 63, 47),  # r: 1 1, 1 2, 2 4, 4 4
+    (9, 2, 600, 64, 32),    # r 1 2: more experts than the tables in LDS hold
+    (5, 2, 4, 64, 47), (5, 2, 4, 63, 48),  # bf16: one kernel of each kind
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", EXACT, ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("int8", [False, True])
+def test_decode_exact(shape, int8):
+    """Bit for bit, with nothing rounded but the result."""
+    require_gpu()
+    p = Exact(*shape, int8=int8)
+    assert torch.equal(p.run().cpu(), _round(p.expect()))
+
+
+@pytest.mark.parametrize("shape", EXACT, ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("int8", [False, True])
+def test_exact_layers_tell(shape, int8):
+    """What test_decode_exact would see: without h's second part, with that of
+    another channel, or with it taken off, more than a third of the results
+    differ."""
+    p = Exact(*shape, int8=int8)
+    want = _round(p.expect())
+    one = lambda h: torch.from_numpy(h).float().to(BF).double().numpy()
+    wrong = {"no second part": one, "of the next channel": lambda h: one(h) + np.roll(h - one(h), 1, axis=1),
+             "subtracted": lambda h: 2 * one(h) - h}
+    for what, parts in wrong.items():
+        off = (_round(p.expect(parts)) != want).double().mean().item()
+        assert off > 0.33, f"{what}: {off}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", S.LAYERS, ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("int8", [False, True])
+def test_decode_within_two_parts(shape, int8, monkeypatch):
+    """Random layers with h's rounding bounded by what two bf16 parts leave: half a
+    step of a remainder that is itself at most half a step of h, 2^-16 of it."""
+    require_gpu()
+    monkeypatch.setattr(S, "HALF", 2.0 ** -16)
+    k = S.LAYERS.index(shape)
+    S.Layer(47, *shape[:5], int8=int8, beyond=shape[5]).check(S.ACTS[(k + int8) % 5])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("int8", [False, True])
+def test_decode_large_within_two_parts(int8, monkeypatch):
+    """The layer's full widths likewise."""
+    monkeypatch.setattr(S, "HALF", 2.0 ** -16)
+    S.test_decode_large(int8)
