@@ -207,3 +207,44 @@ def test_decode_large_within_two_parts(int8, monkeypatch):
     """The layer's full widths likewise."""
     monkeypatch.setattr(S, "HALF", 2.0 ** -16)
     S.test_decode_large(int8)
+
+
+# ---- kernels that other sizes do not reach --------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [
+    (12, 2, 9, 4112, 64),   # 9 to 16 tokens, the second kernel with four waves
+    (40, 2, 32, 4112, 64),  # 17 to 64, four waves, not so few experts that all columns go at once
+    (64, 8, 64, 4112, 48),  # the same with 8 tokens an expert and more
+], ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("uneven", [False, True])
+def test_decode_wide(shape, int8, uneven):
+    """More than 256 tiles of channels, 9 tokens and more; uneven: every token on
+    the first expert, half of them on the second, so that these go by turns."""
+    require_gpu()
+    T, k, E, h, f = shape
+    rng = X._rng(48, *shape)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    if uneven:
+        for t in range(T):
+            rest = 2 + rng.permutation(E - 2)[:k]
+            rest[0] = 0
+            if t % 2 and k > 1:
+                rest[1] = 1
+            idx[t] = rest
+    S.Layer(48, *shape, int8=int8, idx=idx).check(S.ACTS[(T + int8) % 5])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,width", [(4096, 1000), (4097, 2048), (4100, 4090), (4096, 4096), (4099, 515),  # waves
+                                     (4096, 4097), (3, 40000), (2, 65536), (2, 70001), (1, 1 << 20)])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_quantize_many_and_wide_rows(n, width, dtype):
+    """A wave a row in two to eight turns, and workgroups whose rows take eight
+    turns and those that are read twice."""
+    require_gpu()
+    x = S._rows(X._rng(49, n, width), n, width, dtype)
+    q, s = S._quantize(S.Put(width & 1), x)
+    wq, ws = OE.quantize(x.double().numpy())
+    assert np.array_equal(s, ws) and np.array_equal(q, wq)
