@@ -248,3 +248,53 @@ def test_quantize_many_and_wide_rows(n, width, dtype):
     q, s = S._quantize(S.Put(width & 1), x)
     wq, ws = OE.quantize(x.double().numpy())
     assert np.array_equal(s, ws) and np.array_equal(q, wq)
+
+
+# ---- replays on changed inputs -------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes,i,o", [([40, 0, 90, 3], 176, 136), ([1, 0, 30, 3], 177, 135)])
+def test_products_replay_changed_inputs(sizes, i, o):
+    """Quantised rows and both products captured together: each replay, on rows and
+    group sizes that changed since the last, over results and intermediates that
+    hold junk, gives the bits of an eager step with buffers of its own."""
+    require_gpu()
+    p = S.Integers(50, sizes, i, o)
+    (wg, sg), (wu, su) = ([t.to(DEV) for t in p.weight()] for _ in range(2))
+    wd = torch.from_numpy(p.rng.integers(-127, 128, (p.G, i, o)).astype(np.int8)).to(DEV)
+    sd = torch.full((p.G, i), 0.01, device=DEV)
+    x = X._bf16(p.rng, (p.N, i)).to(DEV)
+    off = p.d_off.clone()
+
+    def buffers():
+        e = lambda n, t, v: torch.full((p.N, n) if n else (p.N,), v, dtype=t, device=DEV)
+        return (e(i, torch.int8, 77), e(0, torch.float32, float("nan")), e(o, BF, 5.0), e(o, torch.int8, 77),
+                e(0, torch.float32, float("nan")), e(i, BF, 5.0))
+
+    def step(q, s, h, hq, hs, y):
+        rrb.quantize_rows(x, q, s, offsets=off)
+        rrb.expert_gated_int8(q, s, off, wg, sg, wu, su, h)
+        rrb.quantize_rows(h, hq, hs, offsets=off)
+        rrb.expert_linear_int8(hq, hs, off, wd, sd, y, residual=x)
+
+    own = buffers()
+    step(*own)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*own)
+    seen = []
+    for turn in range(4):
+        x.copy_(X._bf16(p.rng, (p.N, i), 1 + turn))
+        off.copy_(torch.from_numpy(X._offsets(np.roll(sizes, turn))))
+        for t, junk in zip(own, buffers()):
+            t.copy_(junk)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in own]
+        eager = buffers()
+        step(*eager)
+        for a, b in zip(got, eager):
+            assert torch.equal(a, b)
+        assert not any(torch.equal(got[-1], y) for y in seen)
+        seen.append(got[-1])
