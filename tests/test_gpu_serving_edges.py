@@ -298,3 +298,48 @@ def test_products_replay_changed_inputs(sizes, i, o):
             assert torch.equal(a, b)
         assert not any(torch.equal(got[-1], y) for y in seen)
         seen.append(got[-1])
+
+
+# ---- limits of h ------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("f", [524280, 524288])
+def test_decode_h_of_two_gigabytes(f):
+    """64 tokens with 16 choices each and rows of h whose offsets come to the end of
+    31 bits (the kernel that reads h through a buffer), and past it (the one that
+    does not).  Whole numbers, Wd zero but for some channels of h, the first and
+    the last among them."""
+    require_gpu()
+    T, k, E, h = 64, 16, 16, 8
+    rng = X._rng(51, f)
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    some = np.unique(np.concatenate([[0, 7, 8, f - 1, f - 8, f - 9], rng.integers(0, f, 60)]))
+    on = torch.from_numpy(some).to(DEV)
+    draw = lambda *s: torch.empty(s, dtype=BF, device=DEV).random_(-3, 4, generator=gen)
+    x, wg, wu, wd = draw(T, h), draw(E, f, h), draw(E, f, h), torch.zeros(E, h, f, dtype=BF, device=DEV)
+    part = draw(E, h, len(some))
+    wd[:, :, on] = part
+    idx = torch.from_numpy(np.stack([rng.permutation(E) for _ in range(T)]).astype(np.int32))
+    w = torch.full((T, k), 0.5, device=DEV)
+    y = torch.empty(T, h, dtype=BF, device=DEV)
+    rrb.moe_decode(x, idx.to(DEV), w, wg, wu, wd, y, activation="none")
+    nx = X._np(x)
+    want, _ = OE.decode(nx, idx.numpy(), X._np(w), X._np(wg[:, on]), X._np(wu[:, on]), X._np(part), "none")
+    assert np.abs(want).max() < 2 ** 22
+    assert torch.equal(y.cpu(), _round(want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("f", [48, 47])
+@pytest.mark.parametrize("exponent", [-130, -100, 90])
+def test_decode_exact_of_any_magnitude(f, exponent):
+    """Whole h times a power of two down to bf16's subnormal numbers and up to its
+    largest, and Wd times the inverse of one."""
+    require_gpu()
+    p = Exact(6, 2, 4, 64, f)
+    want = p.expect()
+    half = exponent // 2
+    p.m[0] *= 2.0 ** half
+    p.m[1] *= 2.0 ** (exponent - half)
+    p.m[2] *= 2.0 ** -(exponent + 10)
+    assert torch.equal(p.run().cpu(), _round(want * 2.0 ** -10))
