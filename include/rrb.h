@@ -456,14 +456,16 @@ rrb_status rrb_expert_gated_int8(const rrb_expert_spec *spec, const int8_t *d_x,
  * [experts][hidden][inner], and topk_idx, topk_w [tokens][topk] as rrb_moe_gate
  * writes them.  Weights are bf16, or (all three scales given) int8 with scales
  * [experts][inner], [experts][inner] and [experts][hidden].  Sums are fp32, h is
- * kept in two bf16 parts (16 bits), and y is rounded once.  Choices outside
- * 0..experts - 1 take no part (experts of another rank), nor does their weight;
- * an expert that a token chose twice counts twice.  A token without choices has
- * y = 0.  Weights of experts without tokens are not read.  Results do not depend on the launch: the same inputs give
- * the same bits.  d_workspace holds h between the two kernels (caller-owned,
- * 16-byte aligned, of the size the query gives; in use until the call's work
- * completes).  Buffers need the alignment of their elements only; out and the
- * workspace must not overlap inputs or each other (RRB_EINVAL).  Limits
+ * kept in two bf16 parts (16 bits; values that round to an infinity in bf16 are
+ * one), and y is rounded once.  Choices outside 0..experts - 1 take no part
+ * (experts of another rank), nor does their weight; an expert that a token chose
+ * twice counts twice.  A token without choices has y = 0.  Weights of experts
+ * without tokens are not read; infinite ones and NaNs show in the tokens that
+ * meet them as the formula has it.  Results do not depend on the launch: the same
+ * inputs give the same bits.  d_workspace holds h between the two kernels
+ * (caller-owned, 16-byte aligned, of the size the query gives; in use until the
+ * call's work completes).  Buffers need the alignment of their elements only; out
+ * and the workspace must not overlap inputs or each other (RRB_EINVAL).  Limits
  * (RRB_EUNSUPPORTED): tokens <= 64, hidden and inner <= 2^20, experts <= 1024,
  * topk <= 16.
  */

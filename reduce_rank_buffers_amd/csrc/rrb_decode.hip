@@ -395,8 +395,9 @@ __device__ __forceinline__ f32x4_t load_scales(const float *scales, int e, int n
 // Sixteen channels of one expert per workgroup at a time: its waves take blocks of
 // k by turns, and wave 0 joins their sums in order.  For rows off 16-byte boundaries,
 // whose weights go straight into the matrix instruction's registers: bound by the
-// loads in flight and their alignment (5 tokens, 1001 x 333: 9.4 us and the second
-// kernel 8.0, mostly latency; 64 tokens on 16 experts, 2001 x 1001: 70 and 72, 1.8 TB/s).
+// loads in flight and their alignment (5 tokens, 1001 x 333: 10 us and the second kernel
+// 9, mostly latency; 64 tokens on 16 experts, 2001 x 1001: 61 and 52, 1.7 TB/s, integers
+// 37 and 35, 1.3).
 template <bool INT, int MOST>
 __global__ void __launch_bounds__(kUpWaves * 64) decode_up_kernel(DecodeArgs a) {
   typedef typename Element<INT>::T T;
